@@ -39,6 +39,15 @@ class FAError(RuntimeError):
         super().__init__(msg)
 
 
+class _PagedCache(ctypes.Structure):
+    """struct fa_paged_cache of include/fa.h."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("cache_seqlens", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
+                ("table_stride", ctypes.c_longlong), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -87,6 +96,19 @@ def load_library(path: str | None = None):
     lib.fa_fwd_fp8.restype = i
     lib.fa_quantize_fp8.argtypes = [vp, vp, ctypes.c_longlong, i, i, f, i, i, vp]
     lib.fa_quantize_fp8.restype = i
+    ll, pc = ctypes.c_longlong, ctypes.POINTER(_PagedCache)
+    lib.fa_append_paged.argtypes = [pc, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, i, i, i, i, i, i, i,
+                                    i, i, vp]
+    lib.fa_append_paged.restype = i
+    lib.fa_append_paged_fp8.argtypes = [pc, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, i, i, i, i, i,
+                                        i, i, i, f, f, i, vp]
+    lib.fa_append_paged_fp8.restype = i
+    lib.fa_decode_paged_workspace_size.argtypes = [i, i, i]
+    lib.fa_decode_paged_workspace_size.restype = sz
+    lib.fa_decode_paged.argtypes = [vp, pc, vp, vp, vp, sz, i, i, i, i, i, f, i, vp]
+    lib.fa_decode_paged.restype = i
+    lib.fa_decode_paged_fp8.argtypes = [vp, pc, vp, vp, vp, sz, i, i, i, i, i, f, f, f, i, vp]
+    lib.fa_decode_paged_fp8.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_last_cuda_error.restype = i
@@ -445,6 +467,205 @@ def decode_fp8(q, k_cache8, v_cache8, cache_seqlens, k_scale: float, v_scale: fl
         ws_bytes, B, H, Hkv, Nmax, d, float(scale), float(k_scale), float(v_scale),
         _dtype_code(q), _stream()), "fa_decode_fp8")
     return out, lse
+
+
+def _same_device(*ts):
+    """The one CUDA device of all tensors (None entries aside)."""
+    dev = ts[0].device
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+        if t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    return dev
+
+
+def _on_device(dev, fn, *args) -> int:
+    """fn(*args, current stream of dev) with dev current, as the library's calls expect."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B: int, d: int):
+    """struct fa_paged_cache of caches (pages, Hkv, page_size, d), and Hkv; ``dtype`` None: codes."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != d:
+        raise ValueError("the caches must share one (pages, Hkv, page_size, d) shape")
+    if k_cache.dtype != v_cache.dtype or (k_cache.element_size() != 1 if dtype is None
+                                          else k_cache.dtype != dtype):
+        raise TypeError("E4M3 caches must be 1-byte tensors" if dtype is None
+                        else "the caches must have the dtype of q, k and v")
+    st = k_cache.stride()
+    if st != v_cache.stride() or st[3] != 1:
+        raise ValueError("the caches must share their strides, with contiguous columns")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+        raise ValueError("page_table must be int32 (B, max_pages) with contiguous rows")
+    if cache_seqlens.dtype != torch.int32 or cache_seqlens.shape != (B,) \
+            or not cache_seqlens.is_contiguous():
+        raise ValueError("cache_seqlens must be a contiguous int32 tensor of B lengths")
+    pages, Hkv, page_size, _ = k_cache.shape
+    width = page_table.shape[1]
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+                       cache_seqlens.data_ptr(), st[0], st[1], st[2],
+                       page_table.stride(0) if B > 1 else width, pages, page_size, width), Hkv
+
+
+def _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, scales, cu_seqlens, cos_sin,
+                  interleaved, positions, q, q_out):
+    import torch
+    dev = _same_device(k, v, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, cos_sin,
+                       positions, q, q_out)
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must share one (T, Hkv, d) shape and dtype")
+    T, Hkv, d = k.shape
+    B = T
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 \
+                or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B+1 offsets")
+        B = cu_seqlens.numel() - 1
+    elif page_table.shape[0] != T:
+        raise ValueError("without cu_seqlens every sequence brings one token: T must be B")
+    pc, heads = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else k.dtype, B, d)
+    if heads != Hkv:
+        raise ValueError("the caches must have the heads of k and v")
+    for x, n in ((k, Hkv), (v, Hkv)) + (() if q is None else ((q, q.shape[1]),)):
+        if x.dim() != 3 or x.stride(2) != 1 and d > 1 or x.stride(1) != d and n > 1:
+            raise ValueError("heads and columns of a token must be contiguous")
+    H = Hkv
+    if q is not None:
+        H = q.shape[1]
+        if q.shape != (T, H, d) or q.dtype != k.dtype or H % Hkv:
+            raise ValueError("q must be (T, H, d) of k's dtype with H a multiple of Hkv")
+        q_out = torch.empty((T, H, d), dtype=q.dtype, device=dev) if q_out is None else q_out
+        if q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous and match q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot, max_pos = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be contiguous fp32 (max_pos, rot_dim)")
+        max_pos, rot = cos_sin.shape
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)
+                                  or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 tensor of T positions")
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    lib = load_library()
+    args = (ctypes.byref(pc), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), ptr(q),
+            0 if q is None else q.stride(0), ptr(q_out), ptr(cu_seqlens), ptr(positions),
+            ptr(cos_sin), max_pos, rot, int(interleaved), B, T, H, Hkv, d)
+    if scales:
+        _check(_on_device(dev, lib.fa_append_paged_fp8, *args, float(scales[0]), float(scales[1]),
+                          _dtype_code(k)), "fa_append_paged_fp8")
+    else:
+        _check(_on_device(dev, lib.fa_append_paged, *args, _dtype_code(k)), "fa_append_paged")
+    return q_out
+
+
+def append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens=None, cos_sin=None,
+                 interleaved: bool = False, positions=None, q=None, q_out=None):
+    """Write the keys and values k, v (T, Hkv, d) of new tokens into a paged cache.
+
+    k_cache, v_cache: (pages, Hkv, page_size, d) tensors of one set of strides with contiguous
+    columns (a transposed (pages, page_size, Hkv, d) tensor fits).  page_table: int32
+    (B, max_pages) page ids.  cache_seqlens: int32 (B,) lengths that count the new tokens in,
+    which are each sequence's last keys.  cu_seqlens: int32 (B+1,) offsets of the sequences'
+    tokens; without it every sequence brings one token (T = B), and one of length 0 none.
+    cos_sin: fp32 (max_pos, rot_dim), a row of cosines then sines of the rot_dim/2 pair angles
+    per position (``rope_table``); keys are turned by the row of their position (or of
+    ``positions``, int32 (T,)); pairs are columns (i, i + rot_dim/2), or (2i, 2i + 1) if
+    ``interleaved``.  With q (T, H, d) the same tokens' queries are turned into q_out, which
+    is returned (else None).  A token whose page or angle position lies outside its tensor
+    is left out, and ``device_status()`` then reports FA_ERR_INVALID_VALUE."""
+    return _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, None, cu_seqlens,
+                         cos_sin, interleaved, positions, q, q_out)
+
+
+def append_paged_fp8(k, v, k_cache8, v_cache8, page_table, cache_seqlens, k_scale: float,
+                     v_scale: float, cu_seqlens=None, cos_sin=None, interleaved: bool = False,
+                     positions=None, q=None, q_out=None):
+    """As ``append_paged`` into caches of E4M3 codes (uint8 or float8_e4m3fn, d = 128) standing
+    for k_scale * K and v_scale * V."""
+    return _append_paged(k, v, k_cache8, v_cache8, page_table, cache_seqlens, (k_scale, v_scale),
+                         cu_seqlens, cos_sin, interleaved, positions, q, q_out)
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """fp32 (max_pos, rot_dim) table for ``append_paged``: cosines, then sines, of the angles
+    p * base^(-2i / rot_dim), formed in 64 bits (an angle of a far position loses its fraction in
+    32) and rounded once."""
+    import torch
+    if max_pos < 1 or rot_dim < 0 or rot_dim % 2:
+        raise ValueError("max_pos must be positive and rot_dim even")
+    w = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / max(rot_dim, 1))
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * w
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def decode_paged_workspace_size(H: int, Hkv: int, d: int) -> int:
+    return int(load_library().fa_decode_paged_workspace_size(H, Hkv, d))
+
+
+def _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scales, scale, window, out, lse,
+                  workspace):
+    import torch
+    dev = _same_device(q, k_cache, v_cache, page_table, cache_seqlens, out, lse, workspace)
+    if q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous (B, H, d) tensor")
+    B, H, d = q.shape
+    pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else q.dtype, B, d)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else lse
+    if out.shape != q.shape or out.dtype != q.dtype or lse.shape != (B, H) \
+            or lse.dtype != torch.float32 or not (out.is_contiguous() and lse.is_contiguous()):
+        raise ValueError("out must match q; lse must be (B, H) fp32; both contiguous")
+    lib = load_library()
+    if workspace is None:
+        # torch's allocator, as for out and lse: capturable, and safe to reuse on this stream
+        workspace = torch.empty(lib.fa_decode_paged_workspace_size(H, Hkv, d), dtype=torch.uint8,
+                                device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    args = (q.data_ptr(), ctypes.byref(pc), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), B, H, Hkv, d, int(window),
+            1.0 / math.sqrt(d) if scale is None else float(scale))
+    if scales:
+        _check(_on_device(dev, lib.fa_decode_paged_fp8, *args, float(scales[0]), float(scales[1]),
+                          _dtype_code(q)), "fa_decode_paged_fp8")
+    else:
+        _check(_on_device(dev, lib.fa_decode_paged, *args, _dtype_code(q)), "fa_decode_paged")
+    return out, lse
+
+
+def decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scale: float | None = None,
+                 window: int = 0, out=None, lse=None, workspace=None):
+    """O (B, H, d), L (B, H) fp32 of one query row per (sequence, head) against the
+    cache_seqlens[b] keys of its sequence in a paged cache (see ``append_paged``), or with
+    ``window`` > 0 its last ``window`` keys.  Query head h uses K/V head h // (H // Hkv).  Keys
+    of pages with an id outside [0, pages) are not attended; a row without keys gets O = 0,
+    L = -inf.  ``workspace``: an optional CUDA tensor of at least
+    ``decode_paged_workspace_size(H, Hkv, d)`` bytes; calls that may overlap need one each."""
+    return _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, None, scale, window, out,
+                         lse, workspace)
+
+
+def decode_paged_fp8(q, k_cache8, v_cache8, page_table, cache_seqlens, k_scale: float,
+                     v_scale: float, scale: float | None = None, window: int = 0, out=None,
+                     lse=None, workspace=None):
+    """As ``decode_paged`` from caches of E4M3 codes (uint8 or float8_e4m3fn, d = 128) standing
+    for k_scale * K and v_scale * V."""
+    return _decode_paged(q, k_cache8, v_cache8, page_table, cache_seqlens, (k_scale, v_scale),
+                         scale, window, out, lse, workspace)
 
 
 def device_status() -> int:

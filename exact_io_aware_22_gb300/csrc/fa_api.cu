@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
@@ -347,7 +348,8 @@ fa_status fa_device_status(void* stream) {
   e = cudaMemcpy(p, &zero, sizeof(zero), cudaMemcpyHostToDevice);
   if (e != cudaSuccess) return cuda_fail(e);
   if (v & fa::FA_DEV_TIMEOUT) return FA_ERR_TIMEOUT;
-  return (v & fa::FA_DEV_SMEM_ALIGN) ? FA_ERR_UNSUPPORTED : FA_OK;
+  if (v & fa::FA_DEV_SMEM_ALIGN) return FA_ERR_UNSUPPORTED;
+  return (v & fa::FA_DEV_BAD_INDEX) ? FA_ERR_INVALID_VALUE : FA_OK;
 }
 
 fa_status fa_selftest_timeout(unsigned long long limit_ns, void* stream) {
@@ -741,6 +743,300 @@ fa_status fa_decode_fp8(const void* Q, const void* Kc8, const void* Vc8, const i
     return FA_ERR_UNSUPPORTED;
   return decode_impl(Q, Kc8, Vc8, cache_seqlens, O, L, workspace, workspace_bytes, B, H, Hkv,
                      Nmax, d, scale, dtype, stream, true, k_scale, v_scale);
+}
+
+// ---------------------------------------------------------------- paged caches
+namespace {
+
+// Bytes from a pool's first to past its last element.
+size_t pool_bytes(const fa_paged_cache& c, int Hkv, int d, int elem) {
+  return static_cast<size_t>((c.pages - 1) * c.page_stride + (Hkv - 1) * c.head_stride +
+                             (c.page_size - 1) * c.row_stride + d) * elem;
+}
+
+// No two elements of the two pools coincide: sorted by stride, each dimension of extent > 1
+// (the pair of pools among them, as a dimension of extent 2) must step over all that the
+// smaller ones span.
+bool pools_disjoint(const fa_paged_cache& c, int Hkv, int d, int elem) {
+  const uintptr_t k = reinterpret_cast<uintptr_t>(c.K), v = reinterpret_cast<uintptr_t>(c.V);
+  long long st[4] = {c.row_stride, c.head_stride, c.page_stride,
+                     static_cast<long long>((k < v ? v - k : k - v) / elem)};
+  long long n[4] = {c.page_size, Hkv, c.pages, 2};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (st[j] < st[i]) {
+        std::swap(st[i], st[j]);
+        std::swap(n[i], n[j]);
+      }
+  long long span = d;                            // elements spanned so far
+  for (int i = 0; i < 4; ++i) {
+    if (n[i] == 1) continue;
+    if (st[i] < span) return false;
+    span += (n[i] - 1) * st[i];
+  }
+  return true;
+}
+
+// Validates a paged cache with elements of `elem` bytes; fills the view.
+fa_status check_paged(const fa_paged_cache* c, int Hkv, int d, int elem, fa::PagedView* pg) {
+  if (!c || !c->K || !c->V || !c->page_table || !c->cache_seqlens) return FA_ERR_INVALID_VALUE;
+  if (c->pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->table_stride < c->max_pages)
+    return FA_ERR_INVALID_VALUE;
+  if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  if (d == 32 && c->page_size % 2 != 0) return FA_ERR_UNSUPPORTED;   // TMA boxes of 128 bytes
+  const long long st[3] = {c->row_stride, c->head_stride, c->page_stride};
+  const int n[3] = {c->page_size, Hkv, c->pages};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (st[i] < d) return FA_ERR_INVALID_VALUE;
+    if (st[i] >= (1LL << 40) / elem) return FA_ERR_UNSUPPORTED;
+    if (st[i] * elem % 16 != 0) return FA_ERR_MISALIGNED;
+    if (n[i] - 1 > (1LL << 46) / st[i]) return FA_ERR_UNSUPPORTED;   // byte spans stay in 64 bits
+  }
+  if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->page_table, 4) ||
+      !aligned(c->cache_seqlens, 4))
+    return FA_ERR_MISALIGNED;
+  if (c->table_stride >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  if (!pools_disjoint(*c, Hkv, d, elem)) return FA_ERR_INVALID_VALUE;
+  pg->table = c->page_table;
+  pg->seqlens = c->cache_seqlens;
+  pg->table_stride = c->table_stride;
+  pg->pages = c->pages;
+  pg->max_pages = c->max_pages;
+  pg->page = fa::make_fast_div(static_cast<uint32_t>(c->page_size));
+  return FA_OK;
+}
+
+// The strides with those of dimensions of extent 1, which no element uses, set to d.
+fa_paged_cache used_strides(const fa_paged_cache& c, int Hkv, int d) {
+  fa_paged_cache u = c;
+  if (c.page_size == 1) u.row_stride = d;
+  if (Hkv == 1) u.head_stride = d;
+  if (c.pages == 1) u.page_stride = d;
+  return u;
+}
+
+// 4-D map (d, page_size, Hkv, pages) of one pool, box = box_rows rows of one swizzle width.
+fa_status make_map_paged(CUtensorMap* m, const void* base, const fa_paged_cache& c, int Hkv, int d,
+                         CUtensorMapDataType type, int elem, unsigned box_rows) {
+  EncodeTiledFn enc;
+  fa_status st = get_encoder(&enc);
+  if (st != FA_OK) return st;
+  const int cols = elem == 1 ? 128 : fa::fwd_tile_info(d).box_cols;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.page_size),
+                        static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(c.pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.row_stride) * elem,
+                           static_cast<cuuint64_t>(c.head_stride) * elem,
+                           static_cast<cuuint64_t>(c.page_stride) * elem};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), box_rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, type, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   cols * elem == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+  return FA_OK;
+}
+
+// log2 of the largest power of two that divides page_size, at most that of `keys`: the rows
+// of one TMA box, which then never crosses a page.
+int box_rows_log2(int page_size, int keys) {
+  int l = 0;
+  while ((1 << (l + 1)) <= keys && page_size % (1 << (l + 1)) == 0) ++l;
+  return l;
+}
+
+fa_status append_impl(const fa_paged_cache* cache, const void* K, long long k_stride, const void* V,
+                      long long v_stride, const void* Q, long long q_stride, void* Qout,
+                      const int* cu_seqlens, const int* positions, const float* cos_sin,
+                      int max_pos, int rot_dim, int interleaved, int B, int T, int H, int Hkv,
+                      int d, float k_inv, float v_inv, bool c8, fa_dtype dtype, void* stream) {
+  fa_status st = check_common(B, H, 1, d, 0, 1.f, static_cast<int>(dtype));
+  if (st != FA_OK) return st;
+  if ((st = check_heads(H, Hkv)) != FA_OK) return st;
+  if (T < 1 || (!cu_seqlens && T != B)) return FA_ERR_INVALID_VALUE;
+  if (!K || !V || (Q == nullptr) != (Qout == nullptr)) return FA_ERR_INVALID_VALUE;
+  if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_VALUE;
+  if (rot_dim < 0 || rot_dim > d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (rot_dim > 0 && (!cos_sin || max_pos < 1)) return FA_ERR_INVALID_VALUE;
+  const long long kv_row = static_cast<long long>(Hkv) * d, q_row = static_cast<long long>(H) * d;
+  if (T > 1 && (k_stride < kv_row || v_stride < kv_row || (Q && q_stride < q_row)))
+    return FA_ERR_INVALID_VALUE;
+  if (T == 1) k_stride = v_stride = kv_row, q_stride = q_row;    // not used by any element
+  if (k_stride >= (1LL << 31) || v_stride >= (1LL << 31) || (Q && q_stride >= (1LL << 31)))
+    return FA_ERR_UNSUPPORTED;
+  if (k_stride % 8 != 0 || v_stride % 8 != 0 || (Q && q_stride % 8 != 0)) return FA_ERR_MISALIGNED;
+  for (const void* p : {K, V, Q, static_cast<const void*>(Qout)})
+    if (!aligned(p, 16)) return FA_ERR_MISALIGNED;
+  if ((rot_dim > 0 && !aligned(cos_sin, 16)) || !aligned(cu_seqlens, 4) || !aligned(positions, 4))
+    return FA_ERR_MISALIGNED;
+  fa::AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const int elem = c8 ? 1 : 2;
+  if ((st = check_paged(cache, Hkv, d, elem, &a.pg)) != FA_OK) return st;
+  const fa_paged_cache c = used_strides(*cache, Hkv, d);
+  // outputs: the two pools (disjoint by check_paged) and Qout
+  const size_t pb = pool_bytes(c, Hkv, d, elem), qo = static_cast<size_t>(T) * q_row * 2;
+  const void* outs[3] = {c.K, c.V, Qout};
+  const size_t outsz[3] = {pb, pb, qo};
+  const void* ins[8] = {K, V, Q, cu_seqlens, positions, cos_sin, c.page_table, c.cache_seqlens};
+  const size_t tb = static_cast<size_t>(T - 1);
+  const size_t insz[8] = {(tb * k_stride + kv_row) * 2, (tb * v_stride + kv_row) * 2,
+                          (tb * q_stride + q_row) * 2, (static_cast<size_t>(B) + 1) * 4,
+                          static_cast<size_t>(T) * 4,
+                          rot_dim > 0 ? static_cast<size_t>(max_pos) * rot_dim * 4 : 0,
+                          static_cast<size_t>((B - 1) * c.table_stride + c.max_pages) * 4,
+                          static_cast<size_t>(B) * 4};
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < 8; ++j)
+      if (ins[j] && insz[j] && overlap(outs[i], outsz[i], ins[j], insz[j]))
+        return FA_ERR_INVALID_VALUE;
+    if (i < 2 && Qout && overlap(outs[i], outsz[i], Qout, qo)) return FA_ERR_INVALID_VALUE;
+  }
+  if ((st = ctl_for_launch(&a.ctl)) != FA_OK) return st;
+  a.K = K;
+  a.V = V;
+  a.Q = Q;
+  a.Qout = Qout;
+  a.Kc = c.K;
+  a.Vc = c.V;
+  a.cu = cu_seqlens;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_stride = q_stride;
+  a.page_stride = c.page_stride;
+  a.head_stride = c.head_stride;
+  a.row_stride = c.row_stride;
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.rot = rot_dim;
+  a.max_pos = max_pos;
+  a.k_inv = k_inv;
+  a.v_inv = v_inv;
+  cudaError_t e = fa::launch_append(a, d, dtype == FA_BF16, c8, interleaved != 0,
+                                    static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return FA_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                            void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int d,
+                            int window, float scale, fa_dtype dtype, void* stream, bool c8,
+                            float k_scale, float v_scale) {
+  fa_status st = check_common(B, H, 1, d, 0, scale, static_cast<int>(dtype));
+  if (st != FA_OK) return st;
+  if ((st = check_heads(H, Hkv)) != FA_OK) return st;
+  if (window < 0 || !Q || !O || !L) return FA_ERR_INVALID_VALUE;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4) || (workspace && !aligned(workspace, 16)))
+    return FA_ERR_MISALIGNED;
+  fa::DecodePagedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const int elem = c8 ? 1 : 2;
+  if ((st = check_paged(cache, Hkv, d, elem, &a.pg)) != FA_OK) return st;
+  const fa_paged_cache c = used_strides(*cache, Hkv, d);
+  const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
+  if (B * fa::decode_paged_units(H, Hkv, d, c8, cap) > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa::decode_paged_ws_bytes(H, Hkv, d);
+  if (workspace && workspace_bytes < need) return FA_ERR_INVALID_VALUE;
+  const size_t qb = static_cast<size_t>(B) * H * d * 2, lb = static_cast<size_t>(B) * H * 4;
+  const size_t pb = pool_bytes(c, Hkv, d, elem);
+  const void* outs[3] = {O, L, workspace};
+  const size_t outsz[3] = {qb, lb, need};
+  const void* ins[5] = {Q, c.K, c.V, c.page_table, c.cache_seqlens};
+  const size_t insz[5] = {qb, pb, pb,
+                          static_cast<size_t>((B - 1) * c.table_stride + c.max_pages) * 4,
+                          static_cast<size_t>(B) * 4};
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < 5; ++j)
+      if (overlap(outs[i], outsz[i], ins[j], insz[j])) return FA_ERR_INVALID_VALUE;
+    for (int j = i + 1; j < 3; ++j)
+      if (outs[j] && overlap(outs[i], outsz[i], outs[j], outsz[j])) return FA_ERR_INVALID_VALUE;
+  }
+  const int lg = box_rows_log2(c.page_size, fa::decode_paged_keys(d, c8));
+  const CUtensorMapDataType type = c8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if ((st = make_map_paged(&a.tmK, c.K, c, Hkv, d, type, elem, 1u << lg)) != FA_OK) return st;
+  if ((st = make_map_paged(&a.tmV, c.V, c, Hkv, d, type, elem, 1u << lg)) != FA_OK) return st;
+  if ((st = ctl_for_launch(&a.ctl)) != FA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ws = workspace;
+  if (!ws) {
+    cudaError_t e = cudaMallocAsync(&ws, need, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  a.Q = Q;
+  a.O = O;
+  a.L = L;
+  a.ws = ws;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.window = window;
+  a.box_log2 = lg;
+  a.c_log2 = scale * (c8 ? k_scale : 1.f) * 1.4426950408889634f;
+  a.o_scale = c8 ? v_scale : 1.f;
+  cudaError_t e = fa::launch_decode_paged(a, d, dtype == FA_BF16, c8, s);
+  if (!workspace) {
+    cudaError_t e2 = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = e2;
+  }
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+bool good_scale(float x) { return std::isfinite(x) && x > 0.f && std::isfinite(1.f / x); }
+
+}  // namespace
+
+fa_status fa_append_paged(const fa_paged_cache* cache, const void* K, long long k_stride,
+                          const void* V, long long v_stride, const void* Q, long long q_stride,
+                          void* Qout, const int* cu_seqlens, const int* positions,
+                          const float* cos_sin, int max_pos, int rot_dim, int interleaved, int B,
+                          int T, int H, int Hkv, int d, fa_dtype dtype, void* stream) {
+  return append_impl(cache, K, k_stride, V, v_stride, Q, q_stride, Qout, cu_seqlens, positions,
+                     cos_sin, max_pos, rot_dim, interleaved, B, T, H, Hkv, d, 1.f, 1.f, false,
+                     dtype, stream);
+}
+
+fa_status fa_append_paged_fp8(const fa_paged_cache* cache, const void* K, long long k_stride,
+                              const void* V, long long v_stride, const void* Q, long long q_stride,
+                              void* Qout, const int* cu_seqlens, const int* positions,
+                              const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                              int B, int T, int H, int Hkv, int d, float k_scale, float v_scale,
+                              fa_dtype dtype, void* stream) {
+  if (!good_scale(k_scale) || !good_scale(v_scale)) return FA_ERR_INVALID_VALUE;
+  if (d != 128) return FA_ERR_UNSUPPORTED;
+  return append_impl(cache, K, k_stride, V, v_stride, Q, q_stride, Qout, cu_seqlens, positions,
+                     cos_sin, max_pos, rot_dim, interleaved, B, T, H, Hkv, d, 1.f / k_scale,
+                     1.f / v_scale, true, dtype, stream);
+}
+
+size_t fa_decode_paged_workspace_size(int H, int Hkv, int d) {
+  if (check_common(1, H, 1, d, 0, 1.f, FA_FP16) != FA_OK || check_heads(H, Hkv) != FA_OK) return 0;
+  return fa::decode_paged_ws_bytes(H, Hkv, d);
+}
+
+fa_status fa_decode_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                          void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int d,
+                          int window, float scale, fa_dtype dtype, void* stream) {
+  return decode_paged_impl(Q, cache, O, L, workspace, workspace_bytes, B, H, Hkv, d, window, scale,
+                           dtype, stream, false, 1.f, 1.f);
+}
+
+fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                              void* workspace, size_t workspace_bytes, int B, int H, int Hkv,
+                              int d, int window, float scale, float k_scale, float v_scale,
+                              fa_dtype dtype, void* stream) {
+  if (!good_scale(k_scale) || !good_scale(v_scale)) return FA_ERR_INVALID_VALUE;
+  if (d != 128) return FA_ERR_UNSUPPORTED;
+  return decode_paged_impl(Q, cache, O, L, workspace, workspace_bytes, B, H, Hkv, d, window, scale,
+                           dtype, stream, true, k_scale, v_scale);
 }
 
 }  // extern "C"

@@ -1,0 +1,780 @@
+// fa_decode_paged.cu -- one new query row per (sequence, head) over a paged key/value cache.
+//
+// Mathematics.  Softmax over disjoint key ranges is carried as partial states (m, l, acc)
+// that merge exactly (m' = max(m1, m2), l' = l1 2^(m1-m') + l2 2^(m2-m'), acc likewise), in
+// base 2 with scale * log2(e) applied to the fp32 scores: the tutorial page "What is
+// FlashAttention?", "Softmax in pieces".  A state without keys is (-inf, 0, 0).
+//
+// Bound: the cache's bytes.  Each K and V row is read once from HBM and serves all query
+// heads of its group (up to 16 per CTA), so the products are kept off the critical path: they
+// run as warp-level tensor-core products (m16n8k16) with the *keys* as the rows,
+//     S^T (16 keys x 8 heads) = K Q^T,      O^T (16 columns x 8 heads) += V^T P^T,
+// so a group of up to 8 heads pads nothing but n = 8, K and V^T are fragments that ldmatrix
+// reads from the tiles as TMA laid them down, and S^T becomes the second product's operand by
+// transposing 8 x 8 blocks between lanes (movmatrix).  P goes in as two 16-bit terms (its
+// rounding and the remainder's), so that rounding P costs the result nothing.
+//
+// Work split.  Lengths live on the device and are ragged.  The keys of all rows (sequence,
+// K/V head, group of heads) are laid end to end in units of one ring stage of every warp, and
+// the grid's CTAs take equal ranges of units; a range may end inside a row.  A row inside one
+// CTA's range is finished there; a row cut by range borders leaves one partial state per CTA,
+// and decode_paged_merge_kernel joins them in CTA order, so results do not depend on timing.
+// CTA c keeps at most two such states: its first row's (slot 0) and its last row's (slot 1).
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+#include <cuda_fp8.h>
+
+namespace fa {
+
+namespace {
+
+constexpr int DP_WARPS = 4;
+constexpr int DP_STAGES = 2;
+constexpr int DP_CTAS_PER_SM = 3;
+constexpr int DP_GRID = 152 * DP_CTAS_PER_SM;    // one resident wave
+constexpr int DP_MERGE_THREADS = 128;
+
+// One ring stage of a warp: KEYS keys of K, then of V, about 4 KiB each.
+template <int D, bool C8>
+struct Geom {
+  static constexpr int ELEM = C8 ? 1 : 2;
+  static constexpr int BOXC = C8 ? D : (D == 32 ? 32 : 64);   // columns of one TMA box
+  static constexpr int ROWB = BOXC * ELEM;                    // bytes of a box row: one swizzle span
+  static constexpr int SWM = ROWB == 128 ? 7 : 3;             // 16-byte chunk bits ^= row bits
+  static constexpr int HALVES = D / BOXC;
+  static constexpr int KEYS = 4096 / (D * ELEM);              // 16, 32 or 64
+  static constexpr int BOXB = KEYS * ROWB;
+  static constexpr int TILEB = HALVES * BOXB;                 // 4 KiB
+  static constexpr int STAGEB = 2 * TILEB;
+  static constexpr int UNIT = DP_WARPS * KEYS;                // keys of one work unit
+};
+
+template <int D, bool C8>
+constexpr int ring_bytes() { return DP_WARPS * DP_STAGES * Geom<D, C8>::STAGEB; }
+// two warps' states of 8 heads: m, l, then acc, heads 16 bytes apart mod 128
+template <int D>
+constexpr int red_bytes() { return 2 * 8 * (D + 4) * 4; }
+template <int D, bool C8>
+constexpr int smem_bytes() {
+  return 1024 + ring_bytes<D, C8>() + red_bytes<D>() + DP_WARPS * DP_STAGES * 8 + 64;
+}
+
+// Workspace: one header per CTA, then two slots of `rows` partial states per CTA.
+struct Header {
+  int row;     // the row CTA c shares with CTA c - 1 (b * rows per sequence + row), or -1
+  int c0, c1;  // first and last CTA of that row
+  int slot0;   // the slot of c0's state
+};
+__host__ __device__ constexpr size_t hdr_bytes() { return DP_GRID * sizeof(Header); }
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// Transpose of an 8 x 8 block of 16-bit values held as (row lane / 4, columns 2 (lane % 4)).
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two E4M3 codes (the low or high half of w) as f16 values, exactly.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t even_odd(uint32_t w) {   // bytes 0, 2, 1, 3
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, 0x3120;" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ float ld_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_f32(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+// 2^(m - ref) of a state with maximum m relative to a larger one; a state without keys weighs 0.
+__device__ __forceinline__ float weight(float m, float ref) {
+  return m == -INFINITY ? 0.f : ex2(m - ref);
+}
+
+// Keys [lo, n) of a sequence are attended; its units start at key a0 = lo rounded down to
+// whole stages.
+struct SeqKeys {
+  int lo, n, a0, units;
+};
+template <int KEYS, int UNIT>
+__device__ __forceinline__ SeqKeys seq_keys(const PagedView& pg, int b, int window) {
+  const long long cap = static_cast<long long>(pg.max_pages) * pg.page.div;
+  SeqKeys s;
+  s.n = static_cast<int>(min(static_cast<long long>(max(pg.seqlens[b], 0)), cap));
+  s.lo = window > 0 && window < s.n ? s.n - window : 0;
+  s.a0 = s.lo & ~(KEYS - 1);
+  s.units = (s.n - s.a0 + UNIT - 1) / UNIT;
+  return s;
+}
+
+// A position in a CTA's range: row r of sequence b (K/V head and group of heads), unit u of
+// the row; the range covers the row's units up to ue, and `left` units after those.
+struct Cursor {
+  int b, r, u, ue, left;
+  SeqKeys s;
+};
+
+template <int D, bool BF16, bool C8, int NT>
+__global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
+    decode_paged_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const void* Q, void* O, float* L,
+                        uint8_t* ws, int B, int H, int Hkv, int window, int box_log2, float c_log2,
+                        float o_scale, const PagedView pg, KernelCtl ctl) {
+  using G = Geom<D, C8>;
+  constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT;
+  constexpr bool MB = BF16 && !C8;               // operands of the products: bf16 or f16
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;         // fragment row, column pair
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
+  const uint32_t ring = sb + warp * DP_STAGES * G::STAGEB;
+  const uint32_t red = sb + ring_bytes<D, C8>();
+  const uint32_t bars = red + red_bytes<D>() + warp * DP_STAGES * 8;
+  const uint32_t scan = red + red_bytes<D>() + DP_WARPS * DP_STAGES * 8;
+  if (lane == 0) {
+    for (int st = 0; st < DP_STAGES; ++st) mbar_init(bars + st * 8, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  grid_dep_launch();                             // the merge kernel may set up
+  grid_dep_wait();                               // lengths, table, cache and q are written
+
+  // ---------------------------------------------------------------- this CTA's units
+  const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rps = Hkv * n_rg;   // rows per sequence
+  const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);                // sequences per thread
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    if (b < B) mine += seq_keys<KEYS, G::UNIT>(pg, b, window).units * rps;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int w = 1; w < 32; w *= 2) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, w);
+    if (lane >= w) incl += o;
+  }
+  volatile int* sc = reinterpret_cast<volatile int*>(smem_raw + (scan - raw));   // [4] sums, [4] start
+  if (lane == 31) sc[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < DP_WARPS; ++w) {
+    if (w < warp) before += sc[w];
+    total += sc[w];
+  }
+  incl += before;
+  const int cta = blockIdx.x, n_cta = gridDim.x;
+  const int upc = max((total + n_cta - 1) / n_cta, 1);          // units per CTA
+  const int u0 = min(cta * upc, total), u1 = min(u0 + upc, total);
+  if (u0 < u1 && incl > u0 && incl - mine <= u0) {              // one thread holds unit u0
+    int at = incl - mine;
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      const int n = b < B ? seq_keys<KEYS, G::UNIT>(pg, b, window).units * rps : 0;
+      if (at + n > u0) {
+        sc[4] = b;
+        sc[5] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+
+  // rows of sequences without keys: O = 0, L = -inf
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  for (int b = cta; b < B; b += n_cta) {
+    if (pg.seqlens[b] > 0) continue;
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(O) + static_cast<size_t>(b) * H * D);
+    for (int i = threadIdx.x; i < H * D / 2; i += 32 * DP_WARPS) o[i] = 0u;
+    for (int i = threadIdx.x; i < H; i += 32 * DP_WARPS) L[static_cast<size_t>(b) * H + i] = -INFINITY;
+  }
+  Header* hdr = reinterpret_cast<Header*>(ws);
+  float* part = reinterpret_cast<float*>(ws + hdr_bytes());
+  if (u0 >= u1) {
+    if (threadIdx.x == 0) hdr[cta].row = -1;
+    return;
+  }
+
+  Cursor cur;
+  cur.b = sc[4];
+  cur.s = seq_keys<KEYS, G::UNIT>(pg, cur.b, window);
+  cur.r = (u0 - sc[5]) / cur.s.units;
+  cur.u = (u0 - sc[5]) % cur.s.units;
+  cur.ue = min(cur.s.units, cur.u + (u1 - u0));
+  cur.left = u1 - u0 - (cur.ue - cur.u);
+  const int first_row_start = u0 - cur.u;        // unit at which the first row starts
+  if (threadIdx.x == 0) {
+    Header h = {-1, 0, 0, 0};
+    if (cur.u > 0) {
+      h.row = cur.b * rps + cur.r;
+      h.c0 = first_row_start / upc;
+      h.c1 = (first_row_start + cur.s.units - 1) / upc;
+      h.slot0 = first_row_start > h.c0 * upc ? 1 : 0;
+    }
+    hdr[cta] = h;
+  }
+  // to the first unit of the next row of the range; false at its end
+  auto next_row = [&](Cursor& x) -> bool {
+    if (x.left <= 0) return false;
+    if (++x.r == rps) {
+      x.r = 0;
+      do {
+        ++x.b;
+        if (x.b >= B) return false;              // not reached: `left` counts units that exist
+        x.s = seq_keys<KEYS, G::UNIT>(pg, x.b, window);
+      } while (x.s.units == 0);
+    }
+    x.u = 0;
+    x.ue = min(x.s.units, x.left);
+    x.left -= x.ue;
+    return true;
+  };
+
+  // ---------------------------------------------------------------- this warp's ring
+  // Tiles go out in the range's order, DP_STAGES ahead of their use and across row borders.
+  // Lane i fetches the page of the stage's box i one tile before it issues it.
+  const int box = 1 << box_log2, n_box = KEYS >> box_log2;
+  Cursor pr = cur;
+  bool pr_more = true;
+  int issued = 0, used = 0;
+  int pid = -1, prow = 0, phk = 0;               // this lane's box of the tile to issue next
+  bool p_has = false;
+  // moves pr to the next tile this warp has, and starts the fetch of its pages
+  auto fetch = [&]() {
+    p_has = false;
+    while (pr_more) {
+      if (pr.u == pr.ue) {
+        pr_more = next_row(pr);
+        continue;
+      }
+      const int k0 = pr.s.a0 + (pr.u * DP_WARPS + warp) * KEYS;
+      ++pr.u;
+      if (k0 >= pr.s.n) continue;
+      const int k = k0 + (lane << box_log2);
+      const uint32_t p = pg.page.quot(k);
+      prow = k - static_cast<int>(p * pg.page.div);
+      phk = pr.r / n_rg;
+      pid = lane < n_box && k < pr.s.n ? pg.table[pr.b * pg.table_stride + p] : -1;
+      p_has = true;
+      return;
+    }
+  };
+  // boxes of the tile in stage st whose page exists
+  uint32_t okm[DP_STAGES];
+  auto issue = [&](int st) {
+    const uint32_t bar = bars + st * 8, dst = ring + st * G::STAGEB;
+    const bool ok = pid >= 0 && pid < pg.pages;
+    okm[st] = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) mbar_arrive_expect_tx(bar, G::STAGEB);
+    __syncwarp();
+    if (lane < n_box) {
+      const int w = ok ? pid : pg.pages;         // past the pool: the box reads as zeros
+      const uint32_t d0 = dst + (lane << box_log2) * G::ROWB;
+#pragma unroll
+      for (int hf = 0; hf < G::HALVES; ++hf) {
+        tma_load_4d(d0 + hf * G::BOXB, &tmK, bar, hf * G::BOXC, prow, phk, w);
+        tma_load_4d(d0 + G::TILEB + hf * G::BOXB, &tmV, bar, hf * G::BOXC, prow, phk, w);
+      }
+    }
+    ++issued;
+  };
+#pragma unroll
+  for (int st = 0; st < DP_STAGES; ++st) okm[st] = 0;
+  fetch();
+#pragma unroll
+  for (int st = 0; st < DP_STAGES; ++st) {
+    if (p_has) {
+      issue(st);
+      fetch();
+    }
+  }
+
+  // shared-memory byte offsets of this lane's ldmatrix rows: lane i gives row i % 8 of block
+  // i / 8.  K blocks: (keys 0-7 | 8-15) x (chunk 0 | 1); V blocks for 16-bit caches: chunks
+  // vary first, then keys; for codes: keys first, as for K.
+  const int mr = lane & 7, m0 = (lane >> 3) & 1, m1 = lane >> 4;
+  auto tile_off = [&](int key, int chunk) -> uint32_t {
+    // 16-byte chunk `chunk` of a key's row, in the swizzled box layout
+    const uint32_t off = key * G::ROWB + (chunk % (G::ROWB / 16)) * 16;
+    return (chunk / (G::ROWB / 16)) * G::BOXB + (off ^ (((off >> 7) & G::SWM) << 4));
+  };
+
+  bool ok = true, more = true, first = true;
+  while (more) {
+    // ---- one row segment: units [u, ue) of row r of sequence b
+    const int seg_u = cur.u;
+    const int hk = cur.r / n_rg, rg = cur.r % n_rg;
+    const int nrow = min(RG, grp - rg * RG);     // heads of this row
+    const size_t h0 = static_cast<size_t>(cur.b) * H + hk * grp + rg * RG;
+    // q as the products' second operand: head 8 nt + g, columns 16 ks + 2c (+ 8), or for
+    // codes 16 ks + 4c (+ 2), the order in which ldmatrix hands out the codes of K
+    uint32_t qf[NT][KS][2];
+    float cs[NT][2];                             // scale * log2(e) of this lane's heads 2c, 2c + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool in = 8 * nt + g < nrow;
+      const uint16_t* q = static_cast<const uint16_t*>(Q) + (h0 + 8 * nt + g) * D;
+      if constexpr (C8 && BF16) {
+        // bf16 q as f16 after an exact power-of-two scaling that brings the head's largest
+        // magnitude to [1, 2): entries 2^-14 below the largest lose bits, no entry overflows
+        float v[KS][4], mx = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint2 w = make_uint2(0u, 0u);
+          if (in) w = *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * c);
+          const float2 a = unpack2<true>(w.x), b2 = unpack2<true>(w.y);
+          v[ks][0] = a.x; v[ks][1] = a.y; v[ks][2] = b2.x; v[ks][3] = b2.y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(v[ks][e]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // the power of two at mx: its exponent bits (0 and infinities: no scaling)
+        uint32_t eb = __float_as_uint(mx) & 0x7f800000u;
+        if (eb == 0u || eb >= 0x7e800000u) eb = 0x3f800000u;
+        const float dn = __uint_as_float(0x7f000000u - eb);     // 1 / up
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[nt][ks][0] = pack2<false>(v[ks][0] * dn, v[ks][1] * dn);
+          qf[nt][ks][1] = pack2<false>(v[ks][2] * dn, v[ks][3] * dn);
+        }
+        const float up = __uint_as_float(eb) * c_log2;          // lane 4h holds head h's
+        cs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+        cs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+      } else {
+        cs[nt][0] = cs[nt][1] = c_log2;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t* qq = reinterpret_cast<const uint32_t*>(q + 16 * ks + (C8 ? 4 : 2) * c);
+          qf[nt][ks][0] = in ? qq[0] : 0u;
+          qf[nt][ks][1] = in ? qq[C8 ? 1 : 4] : 0u;
+        }
+      }
+    }
+    float m[NT][2], l[NT][2], acc[NT][KS][4];    // heads 8 nt + 2c, + 1; columns g (+ 8) of each 16
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.f;
+    }
+
+    for (; cur.u < cur.ue && ok; ++cur.u) {
+      const int k0 = cur.s.a0 + (cur.u * DP_WARPS + warp) * KEYS;
+      if (k0 >= cur.s.n) continue;
+      const int st = used % DP_STAGES;
+      if (!(ok = mbar_wait_warp(bars + st * 8, (used / DP_STAGES) & 1, ctl))) break;
+      const uint32_t kt = ring + st * G::STAGEB, vt = kt + G::TILEB;
+      uint32_t have = okm[0];
+#pragma unroll
+      for (int i = 1; i < DP_STAGES; ++i)
+        if (st == i) have = okm[i];
+      // keys of the tile that are attended: [klo, khi), less those of absent pages
+      const int klo = max(cur.s.lo - k0, 0), khi = min(cur.s.n - k0, KEYS);
+      const uint32_t all = n_box == 32 ? 0xffffffffu : (1u << n_box) - 1u;
+      const bool edge = klo > 0 || khi < KEYS || have != all;
+      if (klo > 0 || khi < KEYS) {
+        // V rows outside may hold anything, and 0 x NaN is NaN: clear them
+        for (int i = lane; i < KEYS * (D * G::ELEM / 16); i += 32) {
+          const int key = i % KEYS, ch = i / KEYS;
+          if (key < klo || key >= khi)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + tile_off(key, ch)),
+                         "r"(0u)
+                         : "memory");
+        }
+        fence_proxy_async_smem();                // before a later copy into this stage
+        __syncwarp();
+      }
+
+      // S^T of the tile: keys 16 mt + g (+ 8), heads 8 nt + 2c, + 1
+      float s[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+        if constexpr (C8) {
+#pragma unroll
+          for (int kp = 0; kp < KS / 2; ++kp) {
+            uint32_t w[4];
+            ldsm4(kt + tile_off(16 * mt + mr + 8 * m0, 2 * kp + m1), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {codes_lo(w[2 * h]), codes_lo(w[2 * h + 1]),
+                                     codes_hi(w[2 * h]), codes_hi(w[2 * h + 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<MB>(s[mt][nt], a, qf[nt][2 * kp + h][0], qf[nt][2 * kp + h][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a[4];
+            ldsm4(kt + tile_off(16 * mt + mr + 8 * m0, 2 * ks + m1), a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<MB>(s[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        }
+      }
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int key = 16 * mt + 8 * hf + g;
+            if (key < klo || key >= khi || !((have >> (key >> box_log2)) & 1u)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) s[mt][nt][2 * hf] = s[mt][nt][2 * hf + 1] = -INFINITY;
+            }
+          }
+      }
+      // Running maximum, moved only when some score of the warp exceeds it by 2^8 (then
+      // every lane of a head takes the head's new maximum): numerator and denominator carry
+      // the same m, so a stale one changes nothing, and p <= 2^8.
+      bool rise = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) v = fmax3(v, s[mt][nt][e], s[mt][nt][2 + e]);
+          mx[nt][e] = v * cs[nt][e];
+          rise |= mx[nt][e] > m[nt][e] + 8.0f;
+        }
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = mx[nt][e];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float mn = fmaxf(m[nt][e], v), al = weight(m[nt][e], mn);
+            m[nt][e] = mn;
+            l[nt][e] *= al;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              acc[nt][i][e] *= al;
+              acc[nt][i][2 + e] *= al;
+            }
+          }
+      }
+      // p = 2^(s c - m); P^T as 16-bit hi + lo terms, transposed into the second operand
+      uint32_t ph[MT][NT][2], pl[MT][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float ma = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float mb = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float pa = ex2(fmaf(s[mt][nt][2 * hf], cs[nt][0], -ma));
+            const float pb = ex2(fmaf(s[mt][nt][2 * hf + 1], cs[nt][1], -mb));
+            l[nt][0] += pa;
+            l[nt][1] += pb;
+            const uint32_t hi = pack2<MB>(pa, pb);
+            const float2 back = unpack2<MB>(hi);
+            ph[mt][nt][hf] = movm_t(hi);
+            pl[mt][nt][hf] = movm_t(pack2<MB>(pa - back.x, pb - back.y));
+          }
+      }
+      // O^T += V^T P^T over the tile's 16-key steps
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if constexpr (C8) {
+          // blocks: (keys 0-7 | 8-15) x (chunk 2j | 2j + 1); a transposed block of code pairs
+          // holds columns 2g, 2g + 1 of its chunk for keys 2c, 2c + 1: the even columns make
+          // one fragment of 16 output columns, the odd ones the next
+#pragma unroll
+          for (int j = 0; j < KS / 2; ++j) {
+            uint32_t w[4];
+            ldsm4_t(vt + tile_off(16 * mt + mr + 8 * m0, 2 * j + m1), w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = even_odd(w[i]);
+            const uint32_t ae[4] = {codes_lo(w[0]), codes_lo(w[2]), codes_lo(w[1]), codes_lo(w[3])};
+            const uint32_t ao[4] = {codes_hi(w[0]), codes_hi(w[2]), codes_hi(w[1]), codes_hi(w[3])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<MB>(acc[nt][2 * j], ae, ph[mt][nt][0], ph[mt][nt][1]);
+              mma<MB>(acc[nt][2 * j], ae, pl[mt][nt][0], pl[mt][nt][1]);
+              mma<MB>(acc[nt][2 * j + 1], ao, ph[mt][nt][0], ph[mt][nt][1]);
+              mma<MB>(acc[nt][2 * j + 1], ao, pl[mt][nt][0], pl[mt][nt][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            ldsm4_t(vt + tile_off(16 * mt + mr + 8 * m1, 2 * i + m0), a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<MB>(acc[nt][i], a, ph[mt][nt][0], ph[mt][nt][1]);
+              mma<MB>(acc[nt][i], a, pl[mt][nt][0], pl[mt][nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();                              // stage read by every lane
+      ++used;
+      if (p_has) {
+#pragma unroll
+        for (int i = 0; i < DP_STAGES; ++i)
+          if (st == i) issue(i);
+        fetch();
+      }
+    }
+
+    // ---- join the warps: 2, 3 into 0, 1, then 1 into 0, through shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 4; w <= 16; w *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
+    constexpr int HS = (D + 4) * 4;              // bytes of a head's state
+    auto put = [&](uint32_t at, int nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t p = at + (2 * c + e) * HS;
+        if (g == 0) {
+          st_f32(p, m[nt][e]);
+          st_f32(p + 4, l[nt][e]);
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          st_f32(p + (4 + 16 * i + g) * 4, acc[nt][i][e]);
+          st_f32(p + (4 + 16 * i + 8 + g) * 4, acc[nt][i][2 + e]);
+        }
+      }
+    };
+    auto join = [&](uint32_t at, int nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t p = at + (2 * c + e) * HS;
+        const float mo = ld_f32(p), lo = ld_f32(p + 4);
+        const float mn = fmaxf(m[nt][e], mo);
+        const float wa = weight(m[nt][e], mn), wb = weight(mo, mn);
+        m[nt][e] = mn;
+        l[nt][e] = l[nt][e] * wa + lo * wb;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          acc[nt][i][e] = acc[nt][i][e] * wa + ld_f32(p + (4 + 16 * i + g) * 4) * wb;
+          acc[nt][i][2 + e] = acc[nt][i][2 + e] * wa + ld_f32(p + (4 + 16 * i + 8 + g) * 4) * wb;
+        }
+      }
+    };
+    static_assert(DP_WARPS == 4, "two-level join of four warps");
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt * 8 >= nrow) continue;              // the same for the whole CTA
+      __syncthreads();                           // earlier readers of the two buffers are done
+      if (warp >= 2) put(red + (warp - 2) * 8 * HS, nt);
+      __syncthreads();
+      if (warp < 2) join(red + warp * 8 * HS, nt);
+      __syncthreads();
+      if (warp == 1) put(red, nt);
+      __syncthreads();
+      if (warp == 0) join(red, nt);
+    }
+    // ---- a row that is whole in this CTA gives its result, one cut by a border its state
+    if (warp == 0) {
+      const bool whole = seg_u == 0 && cur.ue == cur.s.units;
+      const int slot = first || seg_u > 0 ? 0 : 1;
+      float* rec = part + (static_cast<size_t>(cta) * 2 + slot) * RG * (D + 4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * nt + 2 * c + e;
+          if (row >= nrow) continue;
+          const float lr = l[nt][e], f = whole ? (lr == 0.f ? 0.f : o_scale / lr) : 1.f;
+          T* o = static_cast<T*>(O) + (h0 + row) * D;
+          float* pr_ = rec + row * (D + 4);
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int col = C8 ? 32 * (i / 2) + 16 * hf + 2 * g + (i & 1) : 16 * i + 8 * hf + g;
+              const float v = lr == 0.f ? 0.f : acc[nt][i][2 * hf + e] * f;
+              if (whole) {
+                if constexpr (BF16) o[col] = __float2bfloat16_rn(v);
+                else o[col] = __float2half_rn(v);
+              } else {
+                pr_[4 + col] = v;
+              }
+            }
+          if (g == 0) {
+            if (whole) {
+              L[h0 + row] = lr == 0.f ? -INFINITY : (m[nt][e] + log2f(lr)) * 0.69314718055994531f;
+            } else {
+              pr_[0] = m[nt][e];
+              pr_[1] = lr;
+            }
+          }
+        }
+    }
+    first = false;
+    cur.u = cur.ue;
+    more = next_row(cur);
+  }
+  // after a wait that ran out (recorded in the status word): the copies still in flight land
+  // (bounded) before the CTA's shared memory is released
+  for (int i = used; i < issued; ++i)
+    mbar_wait_warp(bars + (i % DP_STAGES) * 8, (i / DP_STAGES) & 1, ctl);
+}
+
+// Joins the states of a row cut by range borders: CTA c takes part for the row it shares with
+// CTA c - 1.  The CTAs of one row divide its elements among them.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(DP_MERGE_THREADS)
+    decode_paged_merge_kernel(const uint8_t* ws, void* O, float* L, int H, int Hkv, int RG,
+                              float o_scale) {
+  grid_dep_launch();
+  grid_dep_wait();                               // the split kernel's states
+  const Header h = reinterpret_cast<const Header*>(ws)[blockIdx.x];
+  if (h.row < 0) return;
+  const float* part = reinterpret_cast<const float*>(ws + hdr_bytes());
+  const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rps = Hkv * n_rg;
+  const int b = h.row / rps, r = h.row % rps, hk = r / n_rg, rg = r % n_rg;
+  const int nrow = min(RG, grp - rg * RG);
+  const size_t h0 = static_cast<size_t>(b) * H + hk * grp + rg * RG;
+  const int n_sl = h.c1 - h.c0, sl = static_cast<int>(blockIdx.x) - h.c0 - 1;
+  for (int i = sl * DP_MERGE_THREADS + threadIdx.x; i < nrow * D; i += n_sl * DP_MERGE_THREADS) {
+    const int row = i / D, col = i % D;
+    const size_t step = static_cast<size_t>(2) * RG * (D + 4);
+    const float* p0 = part + (static_cast<size_t>(h.c0) * 2 + h.slot0) * RG * (D + 4) + row * (D + 4);
+    const float* p1 = part + (static_cast<size_t>(h.c0) + 1) * step + row * (D + 4);
+    float m = p0[0];
+#pragma unroll 8
+    for (int k = 0; k < n_sl; ++k) m = fmaxf(m, p1[k * step]);
+    float w = weight(p0[0], m);
+    float l = p0[1] * w, acc = p0[4 + col] * w;
+#pragma unroll 8
+    for (int k = 0; k < n_sl; ++k) {
+      const float* p = p1 + k * step;
+      w = weight(p[0], m);
+      l = fmaf(p[1], w, l);
+      acc = fmaf(p[4 + col], w, acc);
+    }
+    const float o = l == 0.f ? 0.f : acc / l * o_scale;
+    if constexpr (BF16) static_cast<__nv_bfloat16*>(O)[(h0 + row) * D + col] = __float2bfloat16_rn(o);
+    else static_cast<__half*>(O)[(h0 + row) * D + col] = __float2half_rn(o);
+    if (col == 0) L[h0 + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// Heads per CTA row: 8 per product column block, two blocks when a group has more than 8.
+int n_blocks(int H, int Hkv) { return H / Hkv > 8 ? 2 : 1; }
+
+template <int D, bool BF16, bool C8, int NT>
+cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
+  auto kern = decode_paged_kernel<D, BF16, C8, NT>;
+  constexpr int smem = smem_bytes<D, C8>();
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  const long long cap = static_cast<long long>(a.pg.max_pages) * a.pg.page.div;
+  const long long units =
+      a.B * decode_paged_units(a.H, a.Hkv, D, C8, a.window > 0 && a.window < cap ? a.window : cap);
+  const unsigned grid = static_cast<unsigned>(units < DP_GRID ? units : DP_GRID);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  trace_begin(TR_DEC_SPLIT, st);
+  e = launch_dependent(kern, grid, 32 * DP_WARPS, smem, st, a.tmK, a.tmV, a.Q, a.O, a.L, ws, a.B,
+                       a.H, a.Hkv, a.window, a.box_log2, a.c_log2, a.o_scale, a.pg, a.ctl);
+  trace_end(TR_DEC_SPLIT, st);
+  if (e != cudaSuccess || grid == 1) return e;   // one CTA: no row is cut
+  trace_begin(TR_DEC_MERGE, st);
+  e = launch_dependent(decode_paged_merge_kernel<D, BF16>, grid, DP_MERGE_THREADS, 0, st,
+                       static_cast<const uint8_t*>(ws), a.O, a.L, a.H, a.Hkv, 8 * NT, a.o_scale);
+  trace_end(TR_DEC_MERGE, st);
+  return e;
+}
+
+template <int D, bool BF16, bool C8>
+cudaError_t launch_nt(const DecodePagedArgs& a, cudaStream_t st) {
+  return n_blocks(a.H, a.Hkv) == 2 ? launch_t<D, BF16, C8, 2>(a, st)
+                                   : launch_t<D, BF16, C8, 1>(a, st);
+}
+
+}  // namespace
+
+int decode_paged_keys(int d, bool c8) { return 4096 / (d * (c8 ? 1 : 2)); }
+
+long long decode_paged_units(int H, int Hkv, int d, bool c8, long long n) {
+  // a window may start inside a stage: up to KEYS - 1 more keys
+  const int keys = decode_paged_keys(d, c8), unit = DP_WARPS * keys, grp = H / Hkv;
+  const int rows = Hkv * ((grp + 8 * n_blocks(H, Hkv) - 1) / (8 * n_blocks(H, Hkv)));
+  return (n + keys - 1 + unit - 1) / unit * rows;
+}
+
+size_t decode_paged_ws_bytes(int H, int Hkv, int d) {
+  return hdr_bytes() + static_cast<size_t>(DP_GRID) * 2 * 8 * n_blocks(H, Hkv) * (d + 4) * 4;
+}
+
+cudaError_t launch_decode_paged(const DecodePagedArgs& a, int d, bool bf16, bool c8,
+                                cudaStream_t st) {
+  if (c8) {
+    if (d != 128) return cudaErrorInvalidValue;
+    return bf16 ? launch_nt<128, true, true>(a, st) : launch_nt<128, false, true>(a, st);
+  }
+  if (d == 32) return bf16 ? launch_nt<32, true, false>(a, st) : launch_nt<32, false, false>(a, st);
+  if (d == 64) return bf16 ? launch_nt<64, true, false>(a, st) : launch_nt<64, false, false>(a, st);
+  if (d == 128)
+    return bf16 ? launch_nt<128, true, false>(a, st) : launch_nt<128, false, false>(a, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fa

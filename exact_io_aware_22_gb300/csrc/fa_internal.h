@@ -148,6 +148,58 @@ int decode_key_rows(int d, bool c8);
 int decode_parts(int B, int H, int Hkv, int Nmax, int* chunk);
 cudaError_t launch_decode(const DecodeArgs& a, int d, bool bf16, bool c8, cudaStream_t st);
 
+// Paged caches (fa_paged_cache in fa.h): pages of page.div rows, addressed through a table of
+// max_pages ids per sequence.
+struct PagedView {
+  const int* table;            // device int32, rows table_stride entries apart
+  const int* seqlens;          // device int32 [B]: keys per sequence
+  long long table_stride;
+  int pages, max_pages;        // pages in the pools, ids per sequence
+  FastDiv page;                // page size
+};
+
+// Appending new tokens' keys and values, rotated on the way; queries rotated beside them.
+struct AppendArgs {
+  const void* K;               // (T, Hkv, d), tokens k_stride elements apart; V and Q likewise
+  const void* V;
+  const void* Q;               // NULL: keys and values only
+  void* Qout;                  // (T, H, d)
+  void* Kc;                    // pools, element (page, head, row, c) at the strides below
+  void* Vc;
+  const int* cu;               // device int32 [B+1]: new tokens of each sequence (NULL: one each)
+  const int* positions;        // device int32 [T]: angle positions (NULL: key positions)
+  const float* cos_sin;        // (max_pos, rot): cos then sin of each pair's angle
+  long long k_stride, v_stride, q_stride;
+  long long page_stride, head_stride, row_stride;
+  int B, T, H, Hkv, rot, max_pos;
+  float k_inv, v_inv;          // E4M3 caches: 1 / descale factors
+  PagedView pg;
+  KernelCtl ctl;
+};
+cudaError_t launch_append(const AppendArgs& a, int d, bool bf16, bool c8, bool interleaved,
+                          cudaStream_t st);
+
+// One query row per (sequence, head) over a paged cache.
+struct DecodePagedArgs {
+  CUtensorMap tmK, tmV;        // 4-D maps (d, page_size, Hkv, pages), box 1 << box_log2 rows
+  const void* Q;               // (B, H, d)
+  void* O;
+  float* L;
+  void* ws;                    // headers and partial states (decode_paged_ws_bytes)
+  int B, H, Hkv, window;       // window 0: every key
+  int box_log2;
+  float c_log2, o_scale;       // scale * log2(e) (E4M3: times k_scale); 1 (E4M3: v_scale)
+  PagedView pg;
+  KernelCtl ctl;
+};
+// Keys per ring stage of one warp: what the TMA box's height has to divide.
+int decode_paged_keys(int d, bool c8);
+// Work units (one ring stage of every warp) per CTA row in a cache of n keys.
+long long decode_paged_units(int H, int Hkv, int d, bool c8, long long n);
+size_t decode_paged_ws_bytes(int H, int Hkv, int d);
+cudaError_t launch_decode_paged(const DecodePagedArgs& a, int d, bool bf16, bool c8,
+                                cudaStream_t st);
+
 // Forward on 8-bit E4M3 inputs, d = 128, dense (B, H, N, 128) layout.
 struct Fwd8Args {
   CUtensorMap tmQ, tmK;        // 3-D byte maps (128, N, B*H) / (128, N, B*Hkv), box 128 x 128

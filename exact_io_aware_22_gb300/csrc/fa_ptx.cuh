@@ -19,7 +19,14 @@ namespace fa {
 // reserve slack to realign it; it checks that the dynamic shared memory starts
 // on a 1024-byte boundary (the 128-byte swizzle atom needs it), and if not,
 // records FA_DEV_SMEM_ALIGN and returns before touching anything.
-enum : uint32_t { FA_DEV_OK = 0u, FA_DEV_TIMEOUT = 1u, FA_DEV_SMEM_ALIGN = 2u };
+// The append into a paged cache records FA_DEV_BAD_INDEX for a new token whose page id or
+// position lies outside the tensors it was given, and leaves that token out.
+enum : uint32_t {
+  FA_DEV_OK = 0u,
+  FA_DEV_TIMEOUT = 1u,
+  FA_DEV_SMEM_ALIGN = 2u,
+  FA_DEV_BAD_INDEX = 4u
+};
 
 struct KernelCtl {
   uint32_t* status;         // device status word (sticky OR of FA_DEV_* bits)
@@ -193,6 +200,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// 4-D tiled load: (column, row of a page, K/V head, page) of a paged cache.  A coordinate
+// past its dimension reads as zeros.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 
@@ -378,6 +396,24 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool bf16, b
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
          ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- paged caches
+// Quotient by a divisor fixed for a launch (a page size): x / div for 0 <= x < 2^31 as one
+// high multiplication, an addition and a shift (round-up method: with 2^(s-1) < div <= 2^s
+// and mul = floor(2^32 (2^s - div) / div) + 1, floor((mulhi(x, mul) + x) / 2^s) is exact;
+// the sum stays below 2^32 because x < 2^31).
+struct FastDiv {
+  uint32_t mul, shift, div;
+  __device__ __forceinline__ uint32_t quot(uint32_t x) const {
+    return (__umulhi(x, mul) + x) >> shift;
+  }
+};
+inline FastDiv make_fast_div(uint32_t div) {
+  uint32_t s = 0;
+  while ((1ull << s) < div) ++s;
+  const uint64_t m = ((1ull << 32) * ((1ull << s) - div)) / div + 1;
+  return {static_cast<uint32_t>(m), s, div};
 }
 
 // ---------------------------------------------------------------- block order

@@ -228,6 +228,105 @@ fa_status fa_decode_fp8(const void* Q, const void* Kc8, const void* Vc8, const i
                         int Hkv, int Nmax, int d, float scale, float k_scale, float v_scale,
                         fa_dtype dtype, void* stream);
 
+/* ---- Paged key/value caches.
+ * The caches of many sequences in one pool of equal pages (the FlashAttention note lists
+ * inference serving with a KV cache, and paged attention by name, among the method's uses:
+ * "Applications and Use Cases").  K and V are pools of `pages` pages, a page holding
+ * page_size key rows of each of the Hkv K/V heads; key j of sequence b, head hk, column c is
+ *     page p = page_table[b * table_stride + j / page_size], row r = j % page_size,
+ *     element p * page_stride + hk * head_stride + r * row_stride + c,
+ * the same strides (in elements, columns contiguous) for both pools, so (pages, Hkv,
+ * page_size, d), (pages, page_size, Hkv, d) and halves of one common pool all fit.
+ *   page_table     device int32 [B][max_pages], rows table_stride entries apart.  Pages may be
+ *                  shared by sequences that only read them.
+ *   cache_seqlens  device int32 [B]: keys of each sequence, clamped to [0, max_pages *
+ *                  page_size].  For the calls that bring new tokens it counts these in: the
+ *                  new tokens are the sequence's last keys.
+ *   A page id outside [0, pages) stands for an absent page: its keys are not attended (a
+ *   sliding window's dropped pages may be marked -1); nothing outside the pools is touched.
+ *   Supported: page_size >= 1 (even for d = 32), max_pages * page_size <= 2^30.
+ *   Errors of every call that takes one: FA_ERR_INVALID_VALUE for NULL members, pages,
+ *   page_size or max_pages < 1, table_stride < max_pages, or strides under which two elements
+ *   of the pools would coincide; FA_ERR_MISALIGNED for pools not 16-byte aligned or strides
+ *   that are not multiples of 16 bytes (dimensions of extent 1 excepted), or table or lengths
+ *   not 4-byte aligned; FA_ERR_UNSUPPORTED beyond the limits above, or for strides of 2^40
+ *   bytes or more. */
+typedef struct fa_paged_cache {
+  void* K;
+  void* V;
+  const int* page_table;
+  const int* cache_seqlens;
+  long long page_stride, head_stride, row_stride;
+  long long table_stride;
+  int pages, page_size, max_pages;
+} fa_paged_cache;
+
+/* Append: the keys and values of T new tokens go to their places in the paged cache, the
+ * first rot_dim columns of keys turned by the position angles (rotary position embedding) on
+ * the way; with Q, the same tokens' queries are turned too and written to Qout.
+ *   K, V         (T, Hkv, d), tokens k_stride / v_stride elements apart, heads and columns
+ *                contiguous (slices of one projection's output fit).  Q (T, H, d) likewise
+ *                with q_stride; Qout dense (T, H, d).  Q and Qout may be NULL, both.
+ *   cu_seqlens   device int32 [B+1]: sequence b brings tokens cu[b] .. cu[b+1]-1, its last
+ *                keys: token t gets key position cache_seqlens[b] - (cu[b+1] - t).  NULL: one
+ *                token per sequence (T = B).  Tokens before cu[0], at or past cu[B], or with a
+ *                negative position (a sequence of length 0) are left out: nothing of theirs is
+ *                written.
+ *   cos_sin      fp32 (max_pos, rot_dim), 16-byte aligned: row p holds cos, then sin, of the
+ *                rot_dim/2 pair angles of position p.  Pair i is columns (i, i + rot_dim/2),
+ *                with interleaved = 1 columns (2i, 2i + 1); (x, y) becomes (x cos - y sin,
+ *                y cos + x sin).  rot_dim = 0: no rotation (cos_sin unused, max_pos 0).
+ *   positions    device int32 [T] to look angles up by, or NULL: key positions.
+ *   A token whose angle position lies outside the table, or whose page is absent, is left out
+ *   (its query too for the former), and fa_device_status then reports FA_ERR_INVALID_VALUE.
+ *   Where two new tokens fall on one cache row, one of them stays.
+ *   Arithmetic in fp32, one rounding.
+ *   Errors: as for the cache, FA_ERR_INVALID_VALUE for NULL K or V, one of Q and Qout alone,
+ *   B, T or Hkv < 1, H not a multiple of Hkv, T != B without cu_seqlens, strides below a
+ *   token's row, cos_sin NULL or max_pos < 1 with rot_dim > 0, interleaved not 0/1 or outputs
+ *   that overlap inputs or each other; FA_ERR_UNSUPPORTED for d not 32/64/128, another dtype,
+ *   rot_dim not a multiple of 16 in [0, d], or 2^31 or more blocks of work;
+ *   FA_ERR_MISALIGNED for K, V, Q, Qout, cos_sin not 16-byte aligned, token strides that are
+ *   not multiples of 8 elements, or int arrays not 4-byte aligned.  Asynchronous on `stream`.
+ *   Launches of this call are not traced. */
+fa_status fa_append_paged(const fa_paged_cache* cache, const void* K, long long k_stride,
+                          const void* V, long long v_stride, const void* Q, long long q_stride,
+                          void* Qout, const int* cu_seqlens, const int* positions,
+                          const float* cos_sin, int max_pos, int rot_dim, int interleaved, int B,
+                          int T, int H, int Hkv, int d, fa_dtype dtype, void* stream);
+
+/* The same into pools of E4M3 codes standing for k_scale * K and v_scale * V: each code is
+ * x * (1 / scale), the reciprocal in fp32, rounded to nearest even and saturated at +-448.
+ * K, V, Q in fp16/bf16 (dtype); d must be 128 (FA_ERR_UNSUPPORTED); scales positive and
+ * finite, with finite reciprocals (FA_ERR_INVALID_VALUE).  Pool strides count codes. */
+fa_status fa_append_paged_fp8(const fa_paged_cache* cache, const void* K, long long k_stride,
+                              const void* V, long long v_stride, const void* Q, long long q_stride,
+                              void* Qout, const int* cu_seqlens, const int* positions,
+                              const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                              int B, int T, int H, int Hkv, int d, float k_scale, float v_scale,
+                              fa_dtype dtype, void* stream);
+
+/* Decoding over a paged cache: one query row per (sequence, head) attends to the
+ * cache_seqlens[b] keys of its sequence, or with window > 0 to the last `window` of them
+ * (the query counts as the last key, as in fa_fwd_swa).  Split over the keys and merged as
+ * fa_decode, with the ranges of the split cut from the lengths on the device, so that ragged
+ * batches share the GPU evenly.  Results do not depend on timing.
+ *   Q (B, H, d), O (B, H, d), L (B, H) as in fa_decode; a row without attended keys gets
+ *   O = 0, L = -inf.
+ *   workspace    fa_decode_paged_workspace_size(H, Hkv, d) bytes (16-byte aligned), or NULL:
+ *                allocated and freed on `stream`.  Its contents do not matter before a call.
+ *   Errors: as for the cache and fa_decode, and FA_ERR_INVALID_VALUE for window < 0. */
+size_t fa_decode_paged_workspace_size(int H, int Hkv, int d);
+fa_status fa_decode_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                          void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int d,
+                          int window, float scale, fa_dtype dtype, void* stream);
+
+/* The same from pools of E4M3 codes (d = 128) standing for k_scale * K and v_scale * V. */
+fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                              void* workspace, size_t workspace_bytes, int B, int H, int Hkv,
+                              int d, int window, float scale, float k_scale, float v_scale,
+                              fa_dtype dtype, void* stream);
+
 /* Static description of a status code. */
 const char* fa_status_string(fa_status s);
 
@@ -239,7 +338,8 @@ int fa_last_cuda_error(void);
  * word: FA_ERR_TIMEOUT if any kernel of this library gave up a bounded wait
  * since the last read; FA_ERR_UNSUPPORTED if a kernel found its dynamic shared
  * memory not aligned to 1024 bytes and skipped its work (not expected on
- * sm_103a); FA_OK otherwise (FA_ERR_CUDA if the read failed). */
+ * sm_103a); FA_ERR_INVALID_VALUE if an append left out a token whose page or angle
+ * position lies outside its tensors; FA_OK otherwise (FA_ERR_CUDA if the read failed). */
 fa_status fa_device_status(void* stream);
 
 /* Bound, in nanoseconds, on any single wait inside the kernels (default 2 s).
