@@ -469,106 +469,117 @@ def decode_fp8(q, k_cache8, v_cache8, cache_seqlens, k_scale: float, v_scale: fl
     return out, lse
 
 
-def _same_device(*ts):
-    """The one CUDA device of all tensors (None entries aside)."""
-    dev = ts[0].device
+# The calls on paged caches are made once per layer and generated token, so what they do on
+# the host counts: each looks at every tensor once and asks torch for the raw stream handle
+# (a Stream object takes longer to make than the rest of the call).
+def _one_device(*ts) -> int:
+    """Index of the one CUDA device of all tensors."""
+    dev = ts[0].get_device()
     for t in ts:
-        if t is None:
-            continue
         if not t.is_cuda:
             raise ValueError("all tensors must be CUDA tensors")
-        if t.device != dev:
+        if t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
     return dev
 
 
-def _on_device(dev, fn, *args) -> int:
+def _on_device(dev: int, fn, *args) -> int:
     """fn(*args, current stream of dev) with dev current, as the library's calls expect."""
     import torch
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if dev == torch._C._cuda_getDevice():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B: int, d: int):
     """struct fa_paged_cache of caches (pages, Hkv, page_size, d), and Hkv; ``dtype`` None: codes."""
     import torch
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != d:
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape != v_cache.shape or shape[3] != d:
         raise ValueError("the caches must share one (pages, Hkv, page_size, d) shape")
-    if k_cache.dtype != v_cache.dtype or (k_cache.element_size() != 1 if dtype is None
-                                          else k_cache.dtype != dtype):
+    t = k_cache.dtype
+    if t != v_cache.dtype or (k_cache.element_size() != 1 if dtype is None else t != dtype):
         raise TypeError("E4M3 caches must be 1-byte tensors" if dtype is None
                         else "the caches must have the dtype of q, k and v")
-    st = k_cache.stride()
     if st != v_cache.stride() or st[3] != 1:
         raise ValueError("the caches must share their strides, with contiguous columns")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
-            or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+    rows, ts = page_table.shape, page_table.stride()
+    if page_table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B \
+            or ts[1] != 1 and rows[1] > 1:
         raise ValueError("page_table must be int32 (B, max_pages) with contiguous rows")
     if cache_seqlens.dtype != torch.int32 or cache_seqlens.shape != (B,) \
             or not cache_seqlens.is_contiguous():
         raise ValueError("cache_seqlens must be a contiguous int32 tensor of B lengths")
-    pages, Hkv, page_size, _ = k_cache.shape
-    width = page_table.shape[1]
     return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                       cache_seqlens.data_ptr(), st[0], st[1], st[2],
-                       page_table.stride(0) if B > 1 else width, pages, page_size, width), Hkv
+                       cache_seqlens.data_ptr(), st[0], st[1], st[2], ts[0] if B > 1 else rows[1],
+                       shape[0], shape[2], rows[1]), shape[1]
+
+
+def _token_stride(x, n: int, d: int) -> int:
+    """Elements between the tokens of x (T, n, d), whose heads and columns must be contiguous."""
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or s1 != d and n > 1:
+        raise ValueError("heads and columns of a token must be contiguous")
+    return s0
 
 
 def _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, scales, cu_seqlens, cos_sin,
                   interleaved, positions, q, q_out):
     import torch
-    dev = _same_device(k, v, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, cos_sin,
-                       positions, q, q_out)
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+    dev = _one_device(k, v, k_cache, v_cache, page_table, cache_seqlens)
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
         raise ValueError("k and v must share one (T, Hkv, d) shape and dtype")
-    T, Hkv, d = k.shape
-    B = T
+    B = T = shape[0]
+    Hkv, d = shape[1], shape[2]
+    cu = pos = cs = qp = qo = None
+    H, q_stride, rot, max_pos = Hkv, 0, 0, 0
     if cu_seqlens is not None:
+        _one_device(k, cu_seqlens)
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 \
                 or not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B+1 offsets")
-        B = cu_seqlens.numel() - 1
+        B, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
     elif page_table.shape[0] != T:
         raise ValueError("without cu_seqlens every sequence brings one token: T must be B")
-    pc, heads = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else k.dtype, B, d)
+    pc, heads = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else dtype, B, d)
     if heads != Hkv:
         raise ValueError("the caches must have the heads of k and v")
-    for x, n in ((k, Hkv), (v, Hkv)) + (() if q is None else ((q, q.shape[1]),)):
-        if x.dim() != 3 or x.stride(2) != 1 and d > 1 or x.stride(1) != d and n > 1:
-            raise ValueError("heads and columns of a token must be contiguous")
-    H = Hkv
     if q is not None:
-        H = q.shape[1]
-        if q.shape != (T, H, d) or q.dtype != k.dtype or H % Hkv:
+        _one_device(k, q)
+        qs = q.shape
+        if len(qs) != 3 or qs[0] != T or qs[2] != d or q.dtype != dtype or qs[1] % Hkv:
             raise ValueError("q must be (T, H, d) of k's dtype with H a multiple of Hkv")
-        q_out = torch.empty((T, H, d), dtype=q.dtype, device=dev) if q_out is None else q_out
-        if q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous and match q")
+        H = qs[1]
+        if q_out is None:
+            q_out = torch.empty(qs, dtype=dtype, device=q.device)
+        elif q_out.shape != qs or q_out.dtype != dtype or not q_out.is_contiguous() \
+                or q_out.get_device() != dev:
+            raise ValueError("q_out must be contiguous, on q's device, and match q")
+        q_stride, qp, qo = _token_stride(q, H, d), q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rot, max_pos = 0, 0
     if cos_sin is not None:
+        _one_device(k, cos_sin)
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be contiguous fp32 (max_pos, rot_dim)")
-        max_pos, rot = cos_sin.shape
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)
-                                  or not positions.is_contiguous()):
-        raise ValueError("positions must be a contiguous int32 tensor of T positions")
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
+        (max_pos, rot), cs = cos_sin.shape, cos_sin.data_ptr()
+    if positions is not None:
+        _one_device(k, positions)
+        if positions.dtype != torch.int32 or positions.shape != (T,) \
+                or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 tensor of T positions")
+        pos = positions.data_ptr()
     lib = load_library()
-    args = (ctypes.byref(pc), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), ptr(q),
-            0 if q is None else q.stride(0), ptr(q_out), ptr(cu_seqlens), ptr(positions),
-            ptr(cos_sin), max_pos, rot, int(interleaved), B, T, H, Hkv, d)
+    args = (pc, k.data_ptr(), _token_stride(k, Hkv, d), v.data_ptr(), _token_stride(v, Hkv, d), qp,
+            q_stride, qo, cu, pos, cs, max_pos, rot, interleaved, B, T, H, Hkv, d)
     if scales:
-        _check(_on_device(dev, lib.fa_append_paged_fp8, *args, float(scales[0]), float(scales[1]),
-                          _dtype_code(k)), "fa_append_paged_fp8")
+        st = _on_device(dev, lib.fa_append_paged_fp8, *args, *scales, _dtype_code(k))
     else:
-        _check(_on_device(dev, lib.fa_append_paged, *args, _dtype_code(k)), "fa_append_paged")
+        st = _on_device(dev, lib.fa_append_paged, *args, _dtype_code(k))
+    if st:
+        _check(st, "fa_append_paged_fp8" if scales else "fa_append_paged")
     return q_out
 
 
@@ -619,31 +630,40 @@ def decode_paged_workspace_size(H: int, Hkv: int, d: int) -> int:
 def _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scales, scale, window, out, lse,
                   workspace):
     import torch
-    dev = _same_device(q, k_cache, v_cache, page_table, cache_seqlens, out, lse, workspace)
-    if q.dim() != 3 or not q.is_contiguous():
+    dev = _one_device(q, k_cache, v_cache, page_table, cache_seqlens)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous (B, H, d) tensor")
-    B, H, d = q.shape
-    pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else q.dtype, B, d)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else lse
-    if out.shape != q.shape or out.dtype != q.dtype or lse.shape != (B, H) \
-            or lse.dtype != torch.float32 or not (out.is_contiguous() and lse.is_contiguous()):
-        raise ValueError("out must match q; lse must be (B, H) fp32; both contiguous")
+    B, H, d = shape
+    pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else dtype, B, d)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous() \
+            or out.get_device() != dev:
+        raise ValueError("out must be contiguous, on q's device, and match q")
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    elif lse.shape != (B, H) or lse.dtype != torch.float32 or not lse.is_contiguous() \
+            or lse.get_device() != dev:
+        raise ValueError("lse must be contiguous fp32 (B, H) on q's device")
     lib = load_library()
     if workspace is None:
         # torch's allocator, as for out and lse: capturable, and safe to reuse on this stream
         workspace = torch.empty(lib.fa_decode_paged_workspace_size(H, Hkv, d), dtype=torch.uint8,
-                                device=dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    args = (q.data_ptr(), ctypes.byref(pc), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), B, H, Hkv, d, int(window),
-            1.0 / math.sqrt(d) if scale is None else float(scale))
-    if scales:
-        _check(_on_device(dev, lib.fa_decode_paged_fp8, *args, float(scales[0]), float(scales[1]),
-                          _dtype_code(q)), "fa_decode_paged_fp8")
+                                device=q.device)
+        ws_bytes = workspace.numel()
     else:
-        _check(_on_device(dev, lib.fa_decode_paged, *args, _dtype_code(q)), "fa_decode_paged")
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be contiguous, on q's device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    args = (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes, B, H,
+            Hkv, d, window, 1.0 / math.sqrt(d) if scale is None else scale)
+    if scales:
+        st = _on_device(dev, lib.fa_decode_paged_fp8, *args, *scales, _dtype_code(q))
+    else:
+        st = _on_device(dev, lib.fa_decode_paged, *args, _dtype_code(q))
+    if st:
+        _check(st, "fa_decode_paged_fp8" if scales else "fa_decode_paged")
     return out, lse
 
 
