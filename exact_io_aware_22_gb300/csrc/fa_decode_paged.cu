@@ -16,10 +16,13 @@
 //
 // Work split.  Lengths live on the device and are ragged.  The keys of all rows (sequence,
 // K/V head, group of heads) are laid end to end in units of one ring stage of every warp, and
-// the grid's CTAs take equal ranges of units; a range may end inside a row.  A row inside one
-// CTA's range is finished there; a row cut by range borders leaves one partial state per CTA,
-// and decode_paged_merge_kernel joins them in CTA order, so results do not depend on timing.
-// CTA c keeps at most two such states: its first row's (slot 0) and its last row's (slot 1).
+// the grid's CTAs take equal ranges; a range may end inside a row.  A row inside one CTA's
+// range is finished there; a row cut by range borders leaves one partial state per CTA, and
+// decode_paged_merge_kernel joins them in CTA order, so results do not depend on timing.
+// CTA c keeps at most two such states: of the row that began in an earlier CTA (slot 0) and of
+// the row that goes on in the next one (slot 1).  Ranges are equal in cost: a row of u units
+// counts 2u + 1, since beginning and ending a row takes about as long as half a unit.  Unit i
+// of a row then sits at the row's position 2i + 1, and a CTA has the units at its positions.
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -64,7 +67,6 @@ constexpr int smem_bytes() {
 struct Header {
   int row;     // the row CTA c shares with CTA c - 1 (b * rows per sequence + row), or -1
   int c0, c1;  // first and last CTA of that row
-  int slot0;   // the slot of c0's state
 };
 __host__ __device__ constexpr size_t hdr_bytes() { return DP_GRID * sizeof(Header); }
 
@@ -130,6 +132,9 @@ __device__ __forceinline__ float ld_f32(uint32_t a) {
 __device__ __forceinline__ void st_f32(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
 // 2^(m - ref) of a state with maximum m relative to a larger one; a state without keys weighs 0.
 __device__ __forceinline__ float weight(float m, float ref) {
   return m == -INFINITY ? 0.f : ex2(m - ref);
@@ -151,8 +156,11 @@ __device__ __forceinline__ SeqKeys seq_keys(const PagedView& pg, int b, int wind
   return s;
 }
 
-// A position in a CTA's range: row r of sequence b (K/V head and group of heads), unit u of
-// the row; the range covers the row's units up to ue, and `left` units after those.
+// Cost of a row of `units` units (see above).
+__host__ __device__ constexpr int row_cost(int units) { return units > 0 ? 2 * units + 1 : 0; }
+
+// A place in a CTA's range: row r of sequence b (K/V head and group of heads), unit u of the
+// row; the range covers the row's units up to ue, and `left` positions after the row's.
 struct Cursor {
   int b, r, u, ue, left;
   SeqKeys s;
@@ -180,16 +188,29 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     fence_mbar_init();
   }
   __syncwarp();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  // Finding the first keys is a chain of dependent loads (lengths, page table); what they
+  // will read is brought to L2 at once: one 128-byte line of the table per thread of the grid.
+  {
+    const long long i = static_cast<long long>(blockIdx.x) * (32 * DP_WARPS) + threadIdx.x;
+    const int lpr = (pg.max_pages + 31) >> 5;    // lines per table row
+    if (i < static_cast<long long>(B) * lpr)
+      prefetch_l2(pg.table + (i / lpr) * pg.table_stride + (i % lpr) * 32);
+    if (i < (B + 31) >> 5) prefetch_l2(pg.seqlens + i * 32);
+  }
   grid_dep_launch();                             // the merge kernel may set up
   grid_dep_wait();                               // lengths, table, cache and q are written
 
-  // ---------------------------------------------------------------- this CTA's units
+  // ---------------------------------------------------------------- this CTA's range
   const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rps = Hkv * n_rg;   // rows per sequence
   const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);                // sequences per thread
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = threadIdx.x * per + i;
-    if (b < B) mine += seq_keys<KEYS, G::UNIT>(pg, b, window).units * rps;
+    if (b < B) mine += row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * rps;
   }
   int incl = mine;
 #pragma unroll
@@ -208,14 +229,16 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   }
   incl += before;
   const int cta = blockIdx.x, n_cta = gridDim.x;
-  const int upc = max((total + n_cta - 1) / n_cta, 1);          // units per CTA
-  const int u0 = min(cta * upc, total), u1 = min(u0 + upc, total);
-  if (u0 < u1 && incl > u0 && incl - mine <= u0) {              // one thread holds unit u0
+  const int per_cta = max((total - 1) / n_cta + 1, 2);          // positions per CTA
+  const int x0 = static_cast<int>(min(static_cast<long long>(cta) * per_cta,
+                                      static_cast<long long>(total)));
+  const int x1 = x0 + min(per_cta, total - x0);
+  if (x0 < x1 && incl > x0 && incl - mine <= x0) {              // one thread holds position x0
     int at = incl - mine;
     for (int i = 0; i < per; ++i) {
       const int b = threadIdx.x * per + i;
-      const int n = b < B ? seq_keys<KEYS, G::UNIT>(pg, b, window).units * rps : 0;
-      if (at + n > u0) {
+      const int n = b < B ? row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * rps : 0;
+      if (at + n > x0) {
         sc[4] = b;
         sc[5] = at;
         break;
@@ -235,7 +258,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   }
   Header* hdr = reinterpret_cast<Header*>(ws);
   float* part = reinterpret_cast<float*>(ws + hdr_bytes());
-  if (u0 >= u1) {
+  if (x0 >= x1) {
     if (threadIdx.x == 0) hdr[cta].row = -1;
     return;
   }
@@ -243,37 +266,42 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   Cursor cur;
   cur.b = sc[4];
   cur.s = seq_keys<KEYS, G::UNIT>(pg, cur.b, window);
-  cur.r = (u0 - sc[5]) / cur.s.units;
-  cur.u = (u0 - sc[5]) % cur.s.units;
-  cur.ue = min(cur.s.units, cur.u + (u1 - u0));
-  cur.left = u1 - u0 - (cur.ue - cur.u);
-  const int first_row_start = u0 - cur.u;        // unit at which the first row starts
-  if (threadIdx.x == 0) {
-    Header h = {-1, 0, 0, 0};
-    if (cur.u > 0) {
-      h.row = cur.b * rps + cur.r;
-      h.c0 = first_row_start / upc;
-      h.c1 = (first_row_start + cur.s.units - 1) / upc;
-      h.slot0 = first_row_start > h.c0 * upc ? 1 : 0;
-    }
-    hdr[cta] = h;
+  {
+    const int w = row_cost(cur.s.units), x = (x0 - sc[5]) % w, take = min(w - x, x1 - x0);
+    cur.r = (x0 - sc[5]) / w;
+    cur.u = x / 2;
+    cur.ue = min(cur.s.units, (x + take) / 2);
+    cur.left = x1 - x0 - take;
   }
-  // to the first unit of the next row of the range; false at its end
+  // to the range's units of the next row that has some; false at its end
   auto next_row = [&](Cursor& x) -> bool {
-    if (x.left <= 0) return false;
-    if (++x.r == rps) {
-      x.r = 0;
-      do {
-        ++x.b;
-        if (x.b >= B) return false;              // not reached: `left` counts units that exist
-        x.s = seq_keys<KEYS, G::UNIT>(pg, x.b, window);
-      } while (x.s.units == 0);
-    }
-    x.u = 0;
-    x.ue = min(x.s.units, x.left);
-    x.left -= x.ue;
+    do {
+      if (x.left <= 0) return false;
+      if (++x.r == rps) {
+        x.r = 0;
+        do {
+          if (++x.b >= B) return false;          // not reached: `left` counts existing rows
+          x.s = seq_keys<KEYS, G::UNIT>(pg, x.b, window);
+        } while (x.s.units == 0);
+      }
+      const int take = min(row_cost(x.s.units), x.left);
+      x.u = 0;
+      x.ue = min(x.s.units, take / 2);
+      x.left -= take;
+    } while (x.u == x.ue);
     return true;
   };
+  {
+    const int row0 = x0 - (x0 - sc[5]) % row_cost(cur.s.units);   // the first row's position
+    Header h = {-1, 0, 0};
+    if (cur.u > 0 && cur.u < cur.ue) {           // its unit 0 lies in an earlier CTA
+      h.row = cur.b * rps + cur.r;
+      h.c0 = (row0 + 1) / per_cta;
+      h.c1 = (row0 + 2 * cur.s.units - 1) / per_cta;
+    }
+    if (threadIdx.x == 0) hdr[cta] = h;
+  }
+  if (cur.u == cur.ue && !next_row(cur)) return;  // only positions without a unit
 
   // ---------------------------------------------------------------- this warp's ring
   // Tiles go out in the range's order, DP_STAGES ahead of their use and across row borders.
@@ -344,45 +372,64 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     return (chunk / (G::ROWB / 16)) * G::BOXB + (off ^ (((off >> 7) & G::SWM) << 4));
   };
 
-  bool ok = true, more = true, first = true;
+  // Words of q of a row's heads 8 nt + g as they lie in memory: columns 16 ks + 2c (+ 1) and
+  // + 8, or for codes 16 ks + 4c (+ 3), the order in which ldmatrix hands out the codes of K.
+  // A row's words are loaded before the previous row is joined, which hides their latency.
+  uint32_t qw[NT][KS][2];
+  auto load_q = [&](const Cursor& x) {
+    const int hk = x.r / n_rg, rg = x.r % n_rg, nrow = min(RG, grp - rg * RG);
+    const size_t h0 = static_cast<size_t>(x.b) * H + hk * grp + rg * RG;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t* q = static_cast<const uint32_t*>(Q) + (h0 + 8 * nt + g) * (D / 2);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qw[nt][ks][0] = qw[nt][ks][1] = 0u;
+        if (8 * nt + g < nrow) {
+          qw[nt][ks][0] = q[8 * ks + (C8 ? 2 : 1) * c];
+          qw[nt][ks][1] = q[8 * ks + (C8 ? 2 * c + 1 : c + 4)];
+        }
+      }
+    }
+  };
+  load_q(cur);
+
+  bool ok = true, more = true;
   while (more) {
     // ---- one row segment: units [u, ue) of row r of sequence b
     const int seg_u = cur.u;
     const int hk = cur.r / n_rg, rg = cur.r % n_rg;
     const int nrow = min(RG, grp - rg * RG);     // heads of this row
     const size_t h0 = static_cast<size_t>(cur.b) * H + hk * grp + rg * RG;
-    // q as the products' second operand: head 8 nt + g, columns 16 ks + 2c (+ 8), or for
-    // codes 16 ks + 4c (+ 2), the order in which ldmatrix hands out the codes of K
+    // q as the products' second operand
     uint32_t qf[NT][KS][2];
     float cs[NT][2];                             // scale * log2(e) of this lane's heads 2c, 2c + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool in = 8 * nt + g < nrow;
-      const uint16_t* q = static_cast<const uint16_t*>(Q) + (h0 + 8 * nt + g) * D;
       if constexpr (C8 && BF16) {
         // bf16 q as f16 after an exact power-of-two scaling that brings the head's largest
         // magnitude to [1, 2): entries 2^-14 below the largest lose bits, no entry overflows
-        float v[KS][4], mx = 0.f;
+        float mx = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint2 w = make_uint2(0u, 0u);
-          if (in) w = *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * c);
-          const float2 a = unpack2<true>(w.x), b2 = unpack2<true>(w.y);
-          v[ks][0] = a.x; v[ks][1] = a.y; v[ks][2] = b2.x; v[ks][3] = b2.y;
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(v[ks][e]));
-        }
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = unpack2<true>(qw[nt][ks][e]);
+            mx = fmax3(mx, fabsf(f.x), fabsf(f.y));
+          }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         // the power of two at mx: its exponent bits (0 and infinities: no scaling)
         uint32_t eb = __float_as_uint(mx) & 0x7f800000u;
         if (eb == 0u || eb >= 0x7e800000u) eb = 0x3f800000u;
-        const float dn = __uint_as_float(0x7f000000u - eb);     // 1 / up
+        const float dn = __uint_as_float(0x7f000000u - eb);     // 1 / 2^e
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qf[nt][ks][0] = pack2<false>(v[ks][0] * dn, v[ks][1] * dn);
-          qf[nt][ks][1] = pack2<false>(v[ks][2] * dn, v[ks][3] * dn);
-        }
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = unpack2<true>(qw[nt][ks][e]);
+            qf[nt][ks][e] = pack2<false>(f.x * dn, f.y * dn);
+          }
         const float up = __uint_as_float(eb) * c_log2;          // lane 4h holds head h's
         cs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
         cs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
@@ -390,9 +437,8 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
         cs[nt][0] = cs[nt][1] = c_log2;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t* qq = reinterpret_cast<const uint32_t*>(q + 16 * ks + (C8 ? 4 : 2) * c);
-          qf[nt][ks][0] = in ? qq[0] : 0u;
-          qf[nt][ks][1] = in ? qq[C8 ? 1 : 4] : 0u;
+          qf[nt][ks][0] = qw[nt][ks][0];
+          qf[nt][ks][1] = qw[nt][ks][1];
         }
       }
     }
@@ -578,6 +624,13 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
       }
     }
 
+    const bool whole = seg_u == 0 && cur.ue == cur.s.units;
+    // warps that had keys: all, or the first few of a segment shorter than a unit
+    const int n_warps = cur.ue - seg_u > 1 ? DP_WARPS
+        : (cur.s.n - cur.s.a0 - seg_u * G::UNIT + KEYS - 1) / KEYS;
+    cur.u = cur.ue;
+    more = next_row(cur);
+    if (more) load_q(cur);
     // ---- join the warps: 2, 3 into 0, 1, then 1 into 0, through shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -620,21 +673,21 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     static_assert(DP_WARPS == 4, "two-level join of four warps");
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt * 8 >= nrow) continue;              // the same for the whole CTA
+      if (nt * 8 >= nrow || n_warps == 1) continue;   // the same for the whole CTA
       __syncthreads();                           // earlier readers of the two buffers are done
-      if (warp >= 2) put(red + (warp - 2) * 8 * HS, nt);
-      __syncthreads();
-      if (warp < 2) join(red + warp * 8 * HS, nt);
-      __syncthreads();
+      if (n_warps > 2) {
+        if (warp >= 2) put(red + (warp - 2) * 8 * HS, nt);
+        __syncthreads();
+        if (warp < 2) join(red + warp * 8 * HS, nt);
+        __syncthreads();
+      }
       if (warp == 1) put(red, nt);
       __syncthreads();
       if (warp == 0) join(red, nt);
     }
     // ---- a row that is whole in this CTA gives its result, one cut by a border its state
     if (warp == 0) {
-      const bool whole = seg_u == 0 && cur.ue == cur.s.units;
-      const int slot = first || seg_u > 0 ? 0 : 1;
-      float* rec = part + (static_cast<size_t>(cta) * 2 + slot) * RG * (D + 4);
+      float* rec = part + (static_cast<size_t>(cta) * 2 + (seg_u > 0 ? 0 : 1)) * RG * (D + 4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -667,9 +720,6 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
           }
         }
     }
-    first = false;
-    cur.u = cur.ue;
-    more = next_row(cur);
   }
   // after a wait that ran out (recorded in the status word): the copies still in flight land
   // (bounded) before the CTA's shared memory is released
@@ -719,8 +769,7 @@ __global__ void __launch_bounds__(DP_MERGE_THREADS)
           ml[e] = make_float2(-INFINITY, 0.f);
           v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k < n) {
-            // the first CTA's state may be in its second slot
-            const float* p = p1 + k * step + (k == 0 ? h.slot0 * (RG * (D + 4)) : 0);
+            const float* p = p1 + k * step + (k == 0 ? RG * (D + 4) : 0);   // the first: slot 1
             ml[e] = *reinterpret_cast<const float2*>(p);
             v[e] = *reinterpret_cast<const float4*>(p + 4 + col);
           }
@@ -788,9 +837,9 @@ cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const long long cap = static_cast<long long>(a.pg.max_pages) * a.pg.page.div;
-  const long long units =
-      a.B * decode_paged_units(a.H, a.Hkv, D, C8, a.window > 0 && a.window < cap ? a.window : cap);
-  const unsigned grid = static_cast<unsigned>(units < DP_GRID ? units : DP_GRID);
+  const long long most =                         // positions, two per CTA at least
+      a.B * decode_paged_cost(a.H, a.Hkv, D, C8, a.window > 0 && a.window < cap ? a.window : cap) / 2;
+  const unsigned grid = static_cast<unsigned>(most < DP_GRID ? (most > 1 ? most : 1) : DP_GRID);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   trace_begin(TR_DEC_SPLIT, st);
   e = launch_dependent(kern, grid, 32 * DP_WARPS, smem, st, a.tmK, a.tmV, a.Q, a.O, a.L, ws, a.B,
@@ -814,11 +863,11 @@ cudaError_t launch_nt(const DecodePagedArgs& a, cudaStream_t st) {
 
 int decode_paged_keys(int d, bool c8) { return 4096 / (d * (c8 ? 1 : 2)); }
 
-long long decode_paged_units(int H, int Hkv, int d, bool c8, long long n) {
+long long decode_paged_cost(int H, int Hkv, int d, bool c8, long long n) {
   // a window may start inside a stage: up to KEYS - 1 more keys
   const int keys = decode_paged_keys(d, c8), unit = DP_WARPS * keys, grp = H / Hkv;
   const int rows = Hkv * ((grp + 8 * n_blocks(H, Hkv) - 1) / (8 * n_blocks(H, Hkv)));
-  return (n + keys - 1 + unit - 1) / unit * rows;
+  return (2 * ((n + keys - 1 + unit - 1) / unit) + 1) * rows;
 }
 
 size_t decode_paged_ws_bytes(int H, int Hkv, int d) {

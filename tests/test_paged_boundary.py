@@ -116,10 +116,10 @@ def test_odd_pages_of_32_columns(lib):
 
 def test_workspace_size(lib):
     f = lib.fa_decode_paged_workspace_size
-    # headers of 16 bytes and two slots of 8 (groups of more than 8 heads: 16) states of d + 4
+    # headers of 12 bytes and two slots of 8 (groups of more than 8 heads: 16) states of d + 4
     # floats for each of the 152 x 3 CTAs
-    assert f(8, 2, 128) == 456 * (16 + 2 * 8 * 132 * 4)
-    assert f(64, 4, 32) == 456 * (16 + 2 * 16 * 36 * 4)
+    assert f(8, 2, 128) == 456 * (12 + 2 * 8 * 132 * 4)
+    assert f(64, 4, 32) == 456 * (12 + 2 * 16 * 36 * 4)
     assert f(8, 3, 128) == 0 and f(8, 2, 48) == 0 and f(0, 1, 64) == 0
 
 
