@@ -940,7 +940,9 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   if ((st = check_paged(cache, Hkv, d, elem, &a.pg)) != FA_OK) return st;
   const fa_paged_cache c = used_strides(*cache, Hkv, d);
   const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
-  if (B * fa::decode_paged_cost(H, Hkv, d, c8, cap) > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if (B * fa::decode_paged_cost(Hkv, d, c8, cap) > 0x7fffffffLL ||
+      !fa::decode_paged_group_fits(H, Hkv))
+    return FA_ERR_UNSUPPORTED;
   const size_t need = fa::decode_paged_ws_bytes(H, Hkv, d);
   if (workspace && workspace_bytes < need) return FA_ERR_INVALID_VALUE;
   const size_t qb = static_cast<size_t>(B) * H * d * 2, lb = static_cast<size_t>(B) * H * 4;

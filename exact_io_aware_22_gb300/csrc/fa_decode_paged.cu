@@ -6,7 +6,8 @@
 // FlashAttention?", "Softmax in pieces".  A state without keys is (-inf, 0, 0).
 //
 // Bound: the cache's bytes.  Each K and V row is read once from HBM and serves all query
-// heads of its group (up to 16 per CTA), so the products are kept off the critical path: they
+// heads of its group (up to 16 per CTA; the CTAs of a larger group's parts walk the same keys
+// side by side, so that all but one find them in L2), so the products are kept off the critical path: they
 // run as warp-level tensor-core products (m16n8k16) with the *keys* as the rows,
 //     S^T (16 keys x 8 heads) = K Q^T,      O^T (16 columns x 8 heads) += V^T P^T,
 // so a group of up to 8 heads pads nothing but n = 8, K and V^T are fragments that ldmatrix
@@ -15,7 +16,7 @@
 // rounding and the remainder's), so that rounding P costs the result nothing.
 //
 // Work split.  Lengths live on the device and are ragged.  The keys of all rows (sequence,
-// K/V head, group of heads) are laid end to end in units of one ring stage of every warp, and
+// K/V head) are laid end to end in units of one ring stage of every warp, and
 // the grid's CTAs take equal ranges; a range may end inside a row.  A row inside one CTA's
 // range is finished there; a row cut by range borders leaves one partial state per CTA, and
 // decode_paged_merge_kernel joins them in CTA order, so results do not depend on timing.
@@ -33,10 +34,12 @@ namespace fa {
 namespace {
 
 constexpr int DP_WARPS = 4;
-constexpr int DP_STAGES = 2;
-constexpr int DP_CTAS_PER_SM = 3;
-constexpr int DP_GRID = 152 * DP_CTAS_PER_SM;    // one resident wave
 constexpr int DP_MERGE_THREADS = 128;
+// Ring stages per warp and CTAs per SM, by column blocks NT (8 heads each): 192 KiB of ring on
+// an SM either way.  Two blocks need more than the 168 registers that three CTAs leave.
+__host__ __device__ constexpr int stages_of(int NT) { return NT == 1 ? 2 : 3; }
+__host__ __device__ constexpr int ctas_of(int NT) { return NT == 1 ? 3 : 2; }
+__host__ __device__ constexpr int grid_of(int NT) { return 152 * ctas_of(NT); }   // one wave
 
 // One ring stage of a warp: KEYS keys of K, then of V, about 4 KiB each.
 template <int D, bool C8>
@@ -53,22 +56,24 @@ struct Geom {
   static constexpr int UNIT = DP_WARPS * KEYS;                // keys of one work unit
 };
 
-template <int D, bool C8>
-constexpr int ring_bytes() { return DP_WARPS * DP_STAGES * Geom<D, C8>::STAGEB; }
+template <int D, bool C8, int NT>
+__host__ __device__ constexpr int ring_bytes() { return DP_WARPS * stages_of(NT) * Geom<D, C8>::STAGEB; }
 // two warps' states of 8 heads: m, l, then acc, heads 16 bytes apart mod 128
 template <int D>
-constexpr int red_bytes() { return 2 * 8 * (D + 4) * 4; }
-template <int D, bool C8>
+__host__ __device__ constexpr int red_bytes() { return 2 * 8 * (D + 4) * 4; }
+template <int D, bool C8, int NT>
 constexpr int smem_bytes() {
-  return 1024 + ring_bytes<D, C8>() + red_bytes<D>() + DP_WARPS * DP_STAGES * 8 + 64;
+  return 1024 + ring_bytes<D, C8, NT>() + red_bytes<D>() + DP_WARPS * stages_of(NT) * 8 + 64;
 }
 
 // Workspace: one header per CTA, then two slots of `rows` partial states per CTA.
 struct Header {
-  int row;     // the row CTA c shares with CTA c - 1 (b * rows per sequence + row), or -1
-  int c0, c1;  // first and last CTA of that row
+  int row;     // the row (b * Hkv + hk) that range x shares with range x - 1, or -1
+  int c0, c1;  // first and last range of that row
 };
-__host__ __device__ constexpr size_t hdr_bytes() { return DP_GRID * sizeof(Header); }
+__host__ __device__ constexpr size_t hdr_bytes(int NT) {
+  return (grid_of(NT) * sizeof(Header) + 15) / 16 * 16;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -159,32 +164,31 @@ __device__ __forceinline__ SeqKeys seq_keys(const PagedView& pg, int b, int wind
 // Cost of a row of `units` units (see above).
 __host__ __device__ constexpr int row_cost(int units) { return units > 0 ? 2 * units + 1 : 0; }
 
-// A place in a CTA's range: row r of sequence b (K/V head and group of heads), unit u of the
-// row; the range covers the row's units up to ue, and `left` positions after the row's.
+// A place in a CTA's range: row r (K/V head) of sequence b, unit u of the row; the range covers the row's units up to ue, and `left` positions after the row's.
 struct Cursor {
   int b, r, u, ue, left;
   SeqKeys s;
 };
 
 template <int D, bool BF16, bool C8, int NT>
-__global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
+__global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     decode_paged_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const void* Q, void* O, float* L,
                         uint8_t* ws, int B, int H, int Hkv, int window, int box_log2, float c_log2,
                         float o_scale, const PagedView pg, KernelCtl ctl) {
   using G = Geom<D, C8>;
-  constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT;
+  constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT, STAGES = stages_of(NT);
   constexpr bool MB = BF16 && !C8;               // operands of the products: bf16 or f16
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;         // fragment row, column pair
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), sb = (raw + 1023u) & ~1023u;
-  const uint32_t ring = sb + warp * DP_STAGES * G::STAGEB;
-  const uint32_t red = sb + ring_bytes<D, C8>();
-  const uint32_t bars = red + red_bytes<D>() + warp * DP_STAGES * 8;
-  const uint32_t scan = red + red_bytes<D>() + DP_WARPS * DP_STAGES * 8;
+  const uint32_t ring = sb + warp * STAGES * G::STAGEB;
+  const uint32_t red = sb + ring_bytes<D, C8, NT>();
+  const uint32_t bars = red + red_bytes<D>() + warp * STAGES * 8;
+  const uint32_t scan = red + red_bytes<D>() + DP_WARPS * STAGES * 8;
   if (lane == 0) {
-    for (int st = 0; st < DP_STAGES; ++st) mbar_init(bars + st * 8, 1);
+    for (int st = 0; st < STAGES; ++st) mbar_init(bars + st * 8, 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -205,12 +209,14 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   grid_dep_wait();                               // lengths, table, cache and q are written
 
   // ---------------------------------------------------------------- this CTA's range
-  const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rps = Hkv * n_rg;   // rows per sequence
+  // CTA = (range, part of the head group); the range's rows are (sequence, K/V head)
+  const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rg = blockIdx.x % n_rg;
+  const int nrow = min(RG, grp - rg * RG);       // heads of this part
   const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);                // sequences per thread
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = threadIdx.x * per + i;
-    if (b < B) mine += row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * rps;
+    if (b < B) mine += row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * Hkv;
   }
   int incl = mine;
 #pragma unroll
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     total += sc[w];
   }
   incl += before;
-  const int cta = blockIdx.x, n_cta = gridDim.x;
+  const int cta = blockIdx.x / n_rg, n_cta = gridDim.x / n_rg;   // range index, ranges
   const int per_cta = max((total - 1) / n_cta + 1, 2);          // positions per CTA
   const int x0 = static_cast<int>(min(static_cast<long long>(cta) * per_cta,
                                       static_cast<long long>(total)));
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     int at = incl - mine;
     for (int i = 0; i < per; ++i) {
       const int b = threadIdx.x * per + i;
-      const int n = b < B ? row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * rps : 0;
+      const int n = b < B ? row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * Hkv : 0;
       if (at + n > x0) {
         sc[4] = b;
         sc[5] = at;
@@ -250,16 +256,16 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
 
   // rows of sequences without keys: O = 0, L = -inf
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  for (int b = cta; b < B; b += n_cta) {
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
     if (pg.seqlens[b] > 0) continue;
     uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(O) + static_cast<size_t>(b) * H * D);
     for (int i = threadIdx.x; i < H * D / 2; i += 32 * DP_WARPS) o[i] = 0u;
     for (int i = threadIdx.x; i < H; i += 32 * DP_WARPS) L[static_cast<size_t>(b) * H + i] = -INFINITY;
   }
   Header* hdr = reinterpret_cast<Header*>(ws);
-  float* part = reinterpret_cast<float*>(ws + hdr_bytes());
+  float* part = reinterpret_cast<float*>(ws + hdr_bytes(NT));
   if (x0 >= x1) {
-    if (threadIdx.x == 0) hdr[cta].row = -1;
+    if (threadIdx.x == 0) hdr[blockIdx.x].row = -1;
     return;
   }
 
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   auto next_row = [&](Cursor& x) -> bool {
     do {
       if (x.left <= 0) return false;
-      if (++x.r == rps) {
+      if (++x.r == Hkv) {
         x.r = 0;
         do {
           if (++x.b >= B) return false;          // not reached: `left` counts existing rows
@@ -295,16 +301,16 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     const int row0 = x0 - (x0 - sc[5]) % row_cost(cur.s.units);   // the first row's position
     Header h = {-1, 0, 0};
     if (cur.u > 0 && cur.u < cur.ue) {           // its unit 0 lies in an earlier CTA
-      h.row = cur.b * rps + cur.r;
+      h.row = cur.b * Hkv + cur.r;
       h.c0 = (row0 + 1) / per_cta;
       h.c1 = (row0 + 2 * cur.s.units - 1) / per_cta;
     }
-    if (threadIdx.x == 0) hdr[cta] = h;
+    if (threadIdx.x == 0) hdr[blockIdx.x] = h;
   }
   if (cur.u == cur.ue && !next_row(cur)) return;  // only positions without a unit
 
   // ---------------------------------------------------------------- this warp's ring
-  // Tiles go out in the range's order, DP_STAGES ahead of their use and across row borders.
+  // Tiles go out in the range's order, STAGES ahead of their use and across row borders.
   // Lane i fetches the page of the stage's box i one tile before it issues it.
   const int box = 1 << box_log2, n_box = KEYS >> box_log2;
   Cursor pr = cur;
@@ -326,14 +332,14 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
       const int k = k0 + (lane << box_log2);
       const uint32_t p = pg.page.quot(k);
       prow = k - static_cast<int>(p * pg.page.div);
-      phk = pr.r / n_rg;
+      phk = pr.r;
       pid = lane < n_box && k < pr.s.n ? pg.table[pr.b * pg.table_stride + p] : -1;
       p_has = true;
       return;
     }
   };
   // boxes of the tile in stage st whose page exists
-  uint32_t okm[DP_STAGES];
+  uint32_t okm[STAGES];
   auto issue = [&](int st) {
     const uint32_t bar = bars + st * 8, dst = ring + st * G::STAGEB;
     const bool ok = pid >= 0 && pid < pg.pages;
@@ -352,10 +358,10 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     ++issued;
   };
 #pragma unroll
-  for (int st = 0; st < DP_STAGES; ++st) okm[st] = 0;
+  for (int st = 0; st < STAGES; ++st) okm[st] = 0;
   fetch();
 #pragma unroll
-  for (int st = 0; st < DP_STAGES; ++st) {
+  for (int st = 0; st < STAGES; ++st) {
     if (p_has) {
       issue(st);
       fetch();
@@ -377,8 +383,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   // A row's words are loaded before the previous row is joined, which hides their latency.
   uint32_t qw[NT][KS][2];
   auto load_q = [&](const Cursor& x) {
-    const int hk = x.r / n_rg, rg = x.r % n_rg, nrow = min(RG, grp - rg * RG);
-    const size_t h0 = static_cast<size_t>(x.b) * H + hk * grp + rg * RG;
+    const size_t h0 = static_cast<size_t>(x.b) * H + x.r * grp + rg * RG;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint32_t* q = static_cast<const uint32_t*>(Q) + (h0 + 8 * nt + g) * (D / 2);
@@ -398,9 +403,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   while (more) {
     // ---- one row segment: units [u, ue) of row r of sequence b
     const int seg_u = cur.u;
-    const int hk = cur.r / n_rg, rg = cur.r % n_rg;
-    const int nrow = min(RG, grp - rg * RG);     // heads of this row
-    const size_t h0 = static_cast<size_t>(cur.b) * H + hk * grp + rg * RG;
+    const size_t h0 = static_cast<size_t>(cur.b) * H + cur.r * grp + rg * RG;
     // q as the products' second operand
     uint32_t qf[NT][KS][2];
     float cs[NT][2];                             // scale * log2(e) of this lane's heads 2c, 2c + 1
@@ -456,12 +459,12 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     for (; cur.u < cur.ue && ok; ++cur.u) {
       const int k0 = cur.s.a0 + (cur.u * DP_WARPS + warp) * KEYS;
       if (k0 >= cur.s.n) continue;
-      const int st = used % DP_STAGES;
-      if (!(ok = mbar_wait_warp(bars + st * 8, (used / DP_STAGES) & 1, ctl))) break;
+      const int st = used % STAGES;
+      if (!(ok = mbar_wait_warp(bars + st * 8, (used / STAGES) & 1, ctl))) break;
       const uint32_t kt = ring + st * G::STAGEB, vt = kt + G::TILEB;
       uint32_t have = okm[0];
 #pragma unroll
-      for (int i = 1; i < DP_STAGES; ++i)
+      for (int i = 1; i < STAGES; ++i)
         if (st == i) have = okm[i];
       // keys of the tile that are attended: [klo, khi), less those of absent pages
       const int klo = max(cur.s.lo - k0, 0), khi = min(cur.s.n - k0, KEYS);
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
       ++used;
       if (p_has) {
 #pragma unroll
-        for (int i = 0; i < DP_STAGES; ++i)
+        for (int i = 0; i < STAGES; ++i)
           if (st == i) issue(i);
         fetch();
       }
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
     }
     // ---- a row that is whole in this CTA gives its result, one cut by a border its state
     if (warp == 0) {
-      float* rec = part + (static_cast<size_t>(cta) * 2 + (seg_u > 0 ? 0 : 1)) * RG * (D + 4);
+      float* rec = part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_u > 0 ? 0 : 1)) * RG * (D + 4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
   // after a wait that ran out (recorded in the status word): the copies still in flight land
   // (bounded) before the CTA's shared memory is released
   for (int i = used; i < issued; ++i)
-    mbar_wait_warp(bars + (i % DP_STAGES) * 8, (i / DP_STAGES) & 1, ctl);
+    mbar_wait_warp(bars + (i % STAGES) * 8, (i / STAGES) & 1, ctl);
 }
 
 // Joins the states of a row cut by range borders: CTA c takes part for the row it shares with
@@ -736,30 +739,32 @@ __global__ void __launch_bounds__(32 * DP_WARPS, DP_CTAS_PER_SM)
 // a call with 16 caches of up to 32768 keys).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(DP_MERGE_THREADS)
-    decode_paged_merge_kernel(const uint8_t* ws, void* O, float* L, int H, int Hkv, int RG,
+    decode_paged_merge_kernel(const uint8_t* ws, void* O, float* L, int H, int Hkv, int NT,
                               float o_scale) {
   constexpr int PER = 8;                         // states a thread loads at once
   __shared__ float sh[DP_MERGE_THREADS][7];      // m, l, acc; rows of 7 words: no bank conflicts
   grid_dep_wait();                               // the split kernel's states
   const Header h = reinterpret_cast<const Header*>(ws)[blockIdx.x];
   if (h.row < 0) return;
-  const float* part = reinterpret_cast<const float*>(ws + hdr_bytes());
-  const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rps = Hkv * n_rg;
-  const int b = h.row / rps, r = h.row % rps, hk = r / n_rg, rg = r % n_rg;
+  const float* part = reinterpret_cast<const float*>(ws + hdr_bytes(NT));
+  const int RG = 8 * NT, grp = H / Hkv, n_rg = (grp + RG - 1) / RG;
+  const int x = blockIdx.x / n_rg, rg = blockIdx.x % n_rg;
+  const int b = h.row / Hkv, hk = h.row % Hkv;
   const int nrow = min(RG, grp - rg * RG);
   const size_t h0 = static_cast<size_t>(b) * H + hk * grp + rg * RG;
-  const int n_sl = h.c1 - h.c0, sl = static_cast<int>(blockIdx.x) - h.c0 - 1, n = n_sl + 1;
+  const int n_sl = h.c1 - h.c0, sl = x - h.c0 - 1, n = n_sl + 1;
   int gs = 0;                                    // threads per output: up to 16, PER / 2 states each
   while (gs < 4 && (PER / 2 << gs) < n) ++gs;
   const int tg = threadIdx.x & ((1 << gs) - 1), outs = DP_MERGE_THREADS >> gs;
   const int n_out = nrow * (D / 4);
-  const size_t step = static_cast<size_t>(2) * RG * (D + 4);
+  const size_t step = static_cast<size_t>(2) * n_rg * RG * (D + 4);
   for (int base = sl * outs; base < n_out; base += n_sl * outs) {   // the same for the whole CTA
     const int i = base + (threadIdx.x >> gs);
     const int row = i / (D / 4), col = 4 * (i % (D / 4));
     float m = -INFINITY, l = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
     if (i < n_out) {
-      const float* p1 = part + static_cast<size_t>(h.c0) * step + row * (D + 4);
+      const float* p1 =
+          part + (static_cast<size_t>(h.c0) * n_rg + rg) * 2 * RG * (D + 4) + row * (D + 4);
       for (int k0 = tg; k0 < n; k0 += PER << gs) {
         float2 ml[PER];
         float4 v[PER];
@@ -827,28 +832,30 @@ __global__ void __launch_bounds__(DP_MERGE_THREADS)
   }
 }
 
-// Heads per CTA row: 8 per product column block, two blocks when a group has more than 8.
+// Column blocks of a CTA's products: two when a group has more than 8 heads.
 int n_blocks(int H, int Hkv) { return H / Hkv > 8 ? 2 : 1; }
 
 template <int D, bool BF16, bool C8, int NT>
 cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   auto kern = decode_paged_kernel<D, BF16, C8, NT>;
-  constexpr int smem = smem_bytes<D, C8>();
+  constexpr int smem = smem_bytes<D, C8, NT>();
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const long long cap = static_cast<long long>(a.pg.max_pages) * a.pg.page.div;
-  const long long most =                         // positions, two per CTA at least
-      a.B * decode_paged_cost(a.H, a.Hkv, D, C8, a.window > 0 && a.window < cap ? a.window : cap) / 2;
-  const unsigned grid = static_cast<unsigned>(most < DP_GRID ? (most > 1 ? most : 1) : DP_GRID);
+  const long long most =                         // positions, two per range at least
+      a.B * decode_paged_cost(a.Hkv, D, C8, a.window > 0 && a.window < cap ? a.window : cap) / 2;
+  const int n_rg = (a.H / a.Hkv + 8 * NT - 1) / (8 * NT);
+  const long long fit = grid_of(NT) / n_rg, ranges = most < fit ? (most > 1 ? most : 1) : fit;
+  const unsigned grid = static_cast<unsigned>(ranges * n_rg);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   trace_begin(TR_DEC_SPLIT, st);
   e = launch_dependent(kern, grid, 32 * DP_WARPS, smem, st, a.tmK, a.tmV, a.Q, a.O, a.L, ws, a.B,
                        a.H, a.Hkv, a.window, a.box_log2, a.c_log2, a.o_scale, a.pg, a.ctl);
   trace_end(TR_DEC_SPLIT, st);
-  if (e != cudaSuccess || grid == 1) return e;   // one CTA: no row is cut
+  if (e != cudaSuccess || ranges == 1) return e;   // no row is cut
   trace_begin(TR_DEC_MERGE, st);
   e = launch_dependent(decode_paged_merge_kernel<D, BF16>, grid, DP_MERGE_THREADS, 0, st,
-                       static_cast<const uint8_t*>(ws), a.O, a.L, a.H, a.Hkv, 8 * NT, a.o_scale);
+                       static_cast<const uint8_t*>(ws), a.O, a.L, a.H, a.Hkv, NT, a.o_scale);
   trace_end(TR_DEC_MERGE, st);
   return e;
 }
@@ -863,15 +870,20 @@ cudaError_t launch_nt(const DecodePagedArgs& a, cudaStream_t st) {
 
 int decode_paged_keys(int d, bool c8) { return 4096 / (d * (c8 ? 1 : 2)); }
 
-long long decode_paged_cost(int H, int Hkv, int d, bool c8, long long n) {
+long long decode_paged_cost(int Hkv, int d, bool c8, long long n) {
   // a window may start inside a stage: up to KEYS - 1 more keys
-  const int keys = decode_paged_keys(d, c8), unit = DP_WARPS * keys, grp = H / Hkv;
-  const int rows = Hkv * ((grp + 8 * n_blocks(H, Hkv) - 1) / (8 * n_blocks(H, Hkv)));
-  return (2 * ((n + keys - 1 + unit - 1) / unit) + 1) * rows;
+  const int keys = decode_paged_keys(d, c8), unit = DP_WARPS * keys;
+  return (2 * ((n + keys - 1 + unit - 1) / unit) + 1) * Hkv;
+}
+
+bool decode_paged_group_fits(int H, int Hkv) {
+  const int nt = n_blocks(H, Hkv);
+  return (H / Hkv + 8 * nt - 1) / (8 * nt) <= grid_of(nt);
 }
 
 size_t decode_paged_ws_bytes(int H, int Hkv, int d) {
-  return hdr_bytes() + static_cast<size_t>(DP_GRID) * 2 * 8 * n_blocks(H, Hkv) * (d + 4) * 4;
+  const int nt = n_blocks(H, Hkv);
+  return hdr_bytes(nt) + static_cast<size_t>(grid_of(nt)) * 2 * 8 * nt * (d + 4) * 4;
 }
 
 cudaError_t launch_decode_paged(const DecodePagedArgs& a, int d, bool bf16, bool c8,

@@ -195,7 +195,9 @@ struct DecodePagedArgs {
 // Keys per ring stage of one warp: what the TMA box's height has to divide.
 int decode_paged_keys(int d, bool c8);
 // Cost of one sequence of n keys as the split counts it (an upper bound for windows).
-long long decode_paged_cost(int H, int Hkv, int d, bool c8, long long n);
+long long decode_paged_cost(int Hkv, int d, bool c8, long long n);
+// Whether a group of H / Hkv heads fits the grid.
+bool decode_paged_group_fits(int H, int Hkv);
 size_t decode_paged_ws_bytes(int H, int Hkv, int d);
 cudaError_t launch_decode_paged(const DecodePagedArgs& a, int d, bool bf16, bool c8,
                                 cudaStream_t st);

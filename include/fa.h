@@ -315,7 +315,8 @@ fa_status fa_append_paged_fp8(const fa_paged_cache* cache, const void* K, long l
  *   O = 0, L = -inf.
  *   workspace    fa_decode_paged_workspace_size(H, Hkv, d) bytes (16-byte aligned), or NULL:
  *                allocated and freed on `stream`.  Its contents do not matter before a call.
- *   Errors: as for the cache and fa_decode, and FA_ERR_INVALID_VALUE for window < 0. */
+ *   Errors: as for the cache and fa_decode, FA_ERR_INVALID_VALUE for window < 0, and
+ *   FA_ERR_UNSUPPORTED for more than 4864 query heads per K/V head. */
 size_t fa_decode_paged_workspace_size(int H, int Hkv, int d);
 fa_status fa_decode_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
                           void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int d,

@@ -66,6 +66,8 @@ DECODE = [
     ((1, 31, 32, 33, 0, 127, 128, 129), 3, 3, 128, "fp16", 16, "e4m3", 0, "nhd"),
     ((300, 7), 16, 1, 128, "bf16", 1, "e4m3", 0, "pair"),
     ((300, 170), 24, 2, 128, "fp16", 24, "e4m3", 50, "hnd"),
+    ((900, 33), 100, 1, 64, "fp16", 16, "16", 0, "hnd"),              # 100 heads: seven parts
+    ((900, 5000, 33), 70, 2, 128, "bf16", 16, "e4m3", 0, "hnd"),
     ((0, 0, 0), 4, 2, 64, "bf16", 16, "16", 0, "hnd"),                # nothing cached at all
 ]
 

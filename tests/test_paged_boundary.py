@@ -95,7 +95,7 @@ def test_strides_of_single_entries_do_not_matter(lib):
     (dict(O=5 * M), INVALID), (dict(O=M + 512), INVALID), (dict(L=2 * M), INVALID),
     (dict(O=3 * M), INVALID), (dict(L=4 * M), INVALID), (dict(L=6 * M + 16), INVALID),
     (dict(ws=6 * M, ws_bytes=1 << 30), INVALID), (dict(ws=2 * M, ws_bytes=1 << 30), INVALID),
-    (dict(B=2 ** 31 - 1), UNSUPPORTED),
+    (dict(B=2 ** 31 - 1), UNSUPPORTED), (dict(H=4880, Hkv=1), UNSUPPORTED),
 ])
 def test_decode_rejects(lib, kw, code):
     assert decode(lib, **kw) == code
@@ -116,10 +116,10 @@ def test_odd_pages_of_32_columns(lib):
 
 def test_workspace_size(lib):
     f = lib.fa_decode_paged_workspace_size
-    # headers of 12 bytes and two slots of 8 (groups of more than 8 heads: 16) states of d + 4
-    # floats for each of the 152 x 3 CTAs
+    # per CTA (152 x 3; 152 x 2 for groups of more than 8 heads) a header of 12 bytes and two
+    # slots of 8 (16) states of d + 4 floats
     assert f(8, 2, 128) == 456 * (12 + 2 * 8 * 132 * 4)
-    assert f(64, 4, 32) == 456 * (12 + 2 * 16 * 36 * 4)
+    assert f(64, 4, 32) == 304 * (12 + 2 * 16 * 36 * 4)
     assert f(8, 3, 128) == 0 and f(8, 2, 48) == 0 and f(0, 1, 64) == 0
 
 
