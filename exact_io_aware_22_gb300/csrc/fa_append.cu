@@ -78,7 +78,6 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
 // One thread per (token, head of Q|K|V, 16 columns).
 template <int D, bool BF16, bool C8, bool INTER>
 __global__ void __launch_bounds__(APP_THREADS) append_kernel(const AppendArgs a) {
-  grid_dep_launch();
   grid_dep_wait();                               // inputs written, cache rows free to overwrite
   constexpr int IPH = D / 16;                    // items per head
   const int heads = (a.Q ? a.H : 0) + 2 * a.Hkv;
@@ -175,11 +174,8 @@ cudaError_t launch_append_t(const AppendArgs& a, bool interleaved, cudaStream_t 
       static_cast<long long>(a.T) * ((a.Q ? a.H : 0) + 2 * a.Hkv) * (D / 16);
   const long long grid = (items + APP_THREADS - 1) / APP_THREADS;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return interleaved
-             ? launch_dependent(append_kernel<D, BF16, C8, true>, static_cast<unsigned>(grid),
-                                APP_THREADS, 0, st, a)
-             : launch_dependent(append_kernel<D, BF16, C8, false>, static_cast<unsigned>(grid),
-                                APP_THREADS, 0, st, a);
+  auto kern = interleaved ? append_kernel<D, BF16, C8, true> : append_kernel<D, BF16, C8, false>;
+  return launch_dependent(kern, static_cast<unsigned>(grid), APP_THREADS, 0, st, a);
 }
 
 template <int D>

@@ -735,8 +735,9 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
 // states of one output are divided among 2^gs threads, so that a thread has few loads, all
 // in flight at once (their latency is what this kernel takes), and joined through shared
 // memory in a fixed order.  It does not let the next kernel start early: CTAs of the next
-// call's split kernel then took up SMs before this call's had finished (0.292 against 0.245 ms
-// a call with 16 caches of up to 32768 keys).
+// call's split kernel, three to an SM with all of its registers, would be placed around this
+// kernel's, and where a hole of the wrong size is left between them the third has to wait for
+// another to end (0.276 against 0.240 ms a call with 16 caches of up to 32768 keys).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(DP_MERGE_THREADS)
     decode_paged_merge_kernel(const uint8_t* ws, void* O, float* L, int H, int Hkv, int NT,
