@@ -109,6 +109,8 @@ def load_library(path: str | None = None):
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_fp8.argtypes = [vp, pc, vp, vp, vp, sz, i, i, i, i, i, f, f, f, i, vp]
     lib.fa_decode_paged_fp8.restype = i
+    lib.fa_fwd_paged.argtypes = [vp, pc, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, vp]
+    lib.fa_fwd_paged.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_last_cuda_error.restype = i
@@ -686,6 +688,43 @@ def decode_paged_fp8(q, k_cache8, v_cache8, page_table, cache_seqlens, k_scale: 
     for k_scale * K and v_scale * V."""
     return _decode_paged(q, k_cache8, v_cache8, page_table, cache_seqlens, (k_scale, v_scale),
                          scale, window, out, lse, workspace)
+
+
+def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_seqlen: int,
+              causal: bool = True, scale: float | None = None, window: int = 0, out=None,
+              lse=None):
+    """O, L of packed new tokens over a paged cache (see ``append_paged``): q (total, H, d), the
+    rows of sequence b at cu_seqlens[b] .. cu_seqlens[b+1]-1 (int32, B+1 entries), its last
+    positions: causal row i of nq sees keys up to cache_seqlens[b] - nq + i, with ``window`` > 0
+    of those the last ``window``.  max_seqlen bounds every nq.  L is (H, total) fp32; a row
+    without keys gets O = 0, L = -inf."""
+    import torch
+    dev = _one_device(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous (total, H, d) tensor")
+    total, H, d = shape
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 \
+            or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B+1 offsets")
+    B = cu_seqlens.numel() - 1
+    window = _window(causal, window)
+    pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B, d)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous() \
+            or out.get_device() != dev:
+        raise ValueError("out must be contiguous, on q's device, and match q")
+    if lse is None:
+        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
+    elif lse.shape != (H, total) or lse.dtype != torch.float32 or not lse.is_contiguous() \
+            or lse.get_device() != dev:
+        raise ValueError("lse must be contiguous fp32 (H, total) on q's device")
+    _check(_on_device(dev, load_library().fa_fwd_paged, q.data_ptr(), pc, out.data_ptr(),
+                      lse.data_ptr(), cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d,
+                      int(causal), window, 1.0 / math.sqrt(d) if scale is None else scale,
+                      _dtype_code(q)), "fa_fwd_paged")
+    return out, lse
 
 
 def device_status() -> int:

@@ -992,6 +992,54 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
+fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                         const int* cu_seqlens, int B, int total, int max_seqlen, int H, int Hkv,
+                         int d, int causal, int window, float scale, fa_dtype dtype, void* stream) {
+  fa_status st = check_common(B, H, max_seqlen, d, causal, scale, static_cast<int>(dtype));
+  if (st != FA_OK) return st;
+  if ((st = check_heads(H, Hkv)) != FA_OK) return st;
+  if ((st = check_packed(cu_seqlens, total)) != FA_OK) return st;
+  if (window < 0 || (window > 0 && !causal) || !Q || !O || !L) return FA_ERR_INVALID_VALUE;
+  if (max_seqlen > (1 << 29)) return FA_ERR_UNSUPPORTED;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4)) return FA_ERR_MISALIGNED;
+  fa::FwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = check_paged(cache, Hkv, d, 2, &a.pg)) != FA_OK) return st;
+  const fa_paged_cache c = used_strides(*cache, Hkv, d);
+  const size_t qb = static_cast<size_t>(total) * H * d * 2, lb = static_cast<size_t>(total) * H * 4;
+  const size_t pb = pool_bytes(c, Hkv, d, 2);
+  const void* ins[6] = {Q, c.K, c.V, c.page_table, c.cache_seqlens, cu_seqlens};
+  const size_t insz[6] = {qb, pb, pb,
+                          static_cast<size_t>((B - 1) * c.table_stride + c.max_pages) * 4,
+                          static_cast<size_t>(B) * 4, (static_cast<size_t>(B) + 1) * 4};
+  for (int j = 0; j < 6; ++j)
+    if (overlap(O, qb, ins[j], insz[j]) || overlap(L, lb, ins[j], insz[j]))
+      return FA_ERR_INVALID_VALUE;
+  if (overlap(O, qb, L, lb)) return FA_ERR_INVALID_VALUE;
+  const bool bf16 = dtype == FA_BF16;
+  const int lg = box_rows_log2(c.page_size, 128);
+  const CUtensorMapDataType type =
+      bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if ((st = make_map_packed(&a.tmQ, Q, d, H, total, bf16)) != FA_OK) return st;
+  if ((st = make_map_paged(&a.tmK, c.K, c, Hkv, d, type, 2, 1u << lg)) != FA_OK) return st;
+  if ((st = make_map_paged(&a.tmV, c.V, c, Hkv, d, type, 2, 1u << lg)) != FA_OK) return st;
+  if ((st = ctl_for_launch(&a.ctl)) != FA_OK) return st;
+  a.cu_seqlens = cu_seqlens;
+  a.H = H;
+  a.total = total;
+  a.O = O;
+  a.L = L;
+  a.N = max_seqlen;
+  a.BH = B * H;
+  a.group = H / Hkv;
+  a.window = window < (1 << 30) ? window : 0;   // no cache holds more keys
+  a.box_log2 = lg;
+  a.c_log2 = scale * 1.4426950408889634f;
+  cudaError_t e = fa::launch_fwd_paged(a, d, bf16, causal != 0, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorInvalidConfiguration) return FA_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
 bool good_scale(float x) { return std::isfinite(x) && x > 0.f && std::isfinite(1.f / x); }
 
 }  // namespace
@@ -1039,6 +1087,14 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
   if (d != 128) return FA_ERR_UNSUPPORTED;
   return decode_paged_impl(Q, cache, O, L, workspace, workspace_bytes, B, H, Hkv, d, window, scale,
                            dtype, stream, true, k_scale, v_scale);
+}
+
+fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                       const int* cu_seqlens, int B, int total, int max_seqlen, int H, int Hkv,
+                       int d, int causal, int window, float scale, fa_dtype dtype, void* stream) {
+  if (!cu_seqlens) return FA_ERR_INVALID_VALUE;
+  return fwd_paged_impl(Q, cache, O, L, cu_seqlens, B, total, max_seqlen, H, Hkv, d, causal, window,
+                        scale, dtype, stream);
 }
 
 }  // extern "C"

@@ -23,6 +23,14 @@
 // more than RESCALE_LOG2 (log2 units), so the O rescale (TMEM load-multiply-
 // store) is skipped on almost every tile.  The result is still exact algebra:
 // numerator and denominator carry the same stale m, and every p <= 2^8.
+//
+// PAGED instances (fa_fwd_paged) take packed queries and the keys of a paged cache: the
+// queries of a sequence are its last positions, so a query row sees keys up to its own
+// index plus (keys - queries).  Their producer is a whole warp: each lane looks up the pages
+// of its boxes (the largest power of two of rows that divides the page size) one tile
+// ahead and loads them; a 128-row tile is laid out in shared memory as one box would be.
+// Boxes of absent pages read as zeros and their keys are masked; V rows past the last key,
+// which may hold anything, are cleared before the product that reads them (0 x NaN).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -53,6 +61,8 @@ struct Cfg {
   static constexpr int NBARS = 1 + 4 * STAGES + 7;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM_BYTES = SLOT_OFF + 16 + 1024;   // + alignment slack
+  static constexpr int MASK_OFF = (SLOT_OFF + 16 + 15) / 16 * 16;   // paged: key masks
+  static constexpr int PAGED_SMEM_BYTES = MASK_OFF + 8 * 16 + 1024;
   static constexpr int TMEM_COLS = 512;
   static constexpr int S_COL = 0;                           // S_t at t * 128
   static constexpr int O_COL = 256;                         // O_t at 256 + t * D
@@ -66,13 +76,132 @@ __device__ __forceinline__ uint32_t kmajor_koff(int kk) {
   return (e / C::ATOM) * C::CHUNK_BYTES + (e % C::ATOM) * 2;
 }
 
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
+// What a PAGED kernel gets besides the packed ones' arguments (nothing in the others).
+template <bool PAGED>
+struct PagedArgs {};
+template <>
+struct PagedArgs<true> {
+  PagedView pg;
+  int box_log2, causal;
+};
+// Keys of a sequence with nq query rows: query row i is at key position i + off and sees keys
+// up to i + hi (all of them unless causal) and from i + off - window + 1.
+struct KeyRows {
+  int n, off, hi;
+};
+constexpr int kNoLimit = 1 << 30;
+__device__ __forceinline__ KeyRows key_rows(const PagedArgs<true>& px, int b, int nq) {
+  const long long cap = static_cast<long long>(px.pg.max_pages) * px.pg.page.div;
+  KeyRows k;
+  k.n = static_cast<int>(min(static_cast<long long>(max(px.pg.seqlens[b], 0)), cap));
+  k.off = k.n - nq;
+  k.hi = px.causal ? k.off : kNoLimit;
+  return k;
+}
+__device__ __forceinline__ KeyRows key_rows(const PagedArgs<false>&, int, int nq) {
+  return {nq, 0, 0};
+}
+// KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of nq, paged keys.
+__device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nq, int window, int& lo,
+                                            int& hi) {
+  const int last = min(r + BM - 1, nq - 1) + k.hi;
+  hi = last < 0 ? 0 : min((k.n + BN - 1) / BN, last / BN + 1);
+  lo = min(max(0, r + k.off - window + 1) / BN, hi);
+}
+
+// One warp's loads of 128-key tiles of a paged cache.  Lane i handles boxes i, i + 32, ...
+struct PagedTile {
+  int id[4], row[4];               // page (-1: absent; past the keys: -2) and first row
+  uint32_t smem_mask;              // ring of 8 key masks of 128 bits
+};
+constexpr int kMaskSlots = 8;
+__device__ __forceinline__ void paged_fetch(const PagedArgs<true>& px, int b, const KeyRows& k,
+                                            int krow, int lane, PagedTile& t) {
+  const int n_box = BN >> px.box_log2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int bx = lane + 32 * i, key = krow + (bx << px.box_log2);
+    t.id[i] = -2;
+    t.row[i] = 0;
+    if (bx < n_box && key < k.n) {
+      const int p = static_cast<int>(px.pg.page.quot(key));
+      t.row[i] = key - p * static_cast<int>(px.pg.page.div);
+      const int id = px.pg.table[b * px.pg.table_stride + p];
+      t.id[i] = id >= 0 && id < px.pg.pages ? id : -1;
+    }
+  }
+}
+// Keys of the tile that exist, as a bit mask, to slot `slot` of the ring (all lanes call).
+__device__ __forceinline__ void paged_mask(const PagedArgs<true>& px, int lane, const PagedTile& t,
+                                           int slot) {
+  uint32_t have = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) have |= (t.id[i] != -1 ? 1u : 0u) << i;
+  uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+  if (__any_sync(0xffffffffu, have != 15u)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int bx = (32 * i + lane) >> px.box_log2;      // the box of key 32 i + lane
+      const uint32_t h = __shfl_sync(0xffffffffu, have, bx & 31);
+      w[i] = __ballot_sync(0xffffffffu, (h >> (bx >> 5)) & 1u);
+    }
+  }
+  if (lane == 0)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t.smem_mask + slot * 16),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+template <int D>
+__device__ __forceinline__ void paged_load(const PagedArgs<true>& px, const CUtensorMap* map,
+                                           uint32_t dst, uint32_t bar, int hk, int lane,
+                                           const PagedTile& t) {
+  using C = Cfg<D>;
+  const int n_box = BN >> px.box_log2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int bx = lane + 32 * i;
+    if (bx < n_box) {
+      const int w = t.id[i] >= 0 ? t.id[i] : px.pg.pages;   // past the pool: zeros
+#pragma unroll
+      for (int c = 0; c < C::NCHUNK; ++c)
+        tma_load_4d(dst + c * C::CHUNK_BYTES + (bx << px.box_log2) * C::SW, map, bar, c * C::ATOM,
+                    t.row[i], hk, w);
+    }
+  }
+}
+// Masks the scores of absent keys; mask: the tile's slot of the ring.
+__device__ __forceinline__ void paged_holes(uint32_t mask, uint32_t (&s)[BN]) {
+  uint32_t w[4];
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(mask)
+               : "memory");
+  if ((w[0] & w[1] & w[2] & w[3]) == ~0u) return;
+#pragma unroll
+  for (int c = 0; c < BN; ++c)
+    if (!((w[c / 32] >> (c % 32)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+}
+// Clears row r of a V tile (all its columns, so the swizzle does not matter).
+template <int D>
+__device__ __forceinline__ void clear_row(uint32_t tile, int r) {
+  using C = Cfg<D>;
+#pragma unroll
+  for (int c = 0; c < C::NCHUNK; ++c)
+#pragma unroll
+    for (int i = 0; i < C::SW / 16; ++i)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                       tile + c * C::CHUNK_BYTES + r * C::SW + 16 * i),
+                   "r"(0u)
+                   : "memory");
+}
+
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
 __global__ void __launch_bounds__(THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, void* __restrict__ Out,
                float* __restrict__ Lout, int N, int n_qblk, int group, int window,
                const int* __restrict__ cu_seqlens, int H, int total, float c_log2,
-               KernelCtl ctl) {
+               KernelCtl ctl, const PagedArgs<PAGED> px) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -95,6 +224,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto cy = [&](int r, int head) { return sr.y(r, head); };
   auto cz = [&](int r, int head) { return sr.z(r, head); };
   const int row0 = qblk * (NT * BM);
+  const KeyRows kr = key_rows(px, bh / H, Nr);
+  const int Nk = PAGED ? kr.n : Nr;             // keys
   const int nkv = (Nr + BN - 1) / BN;
   // KV tiles [lo_t[t], n_t[t]) of Q tile t: up to the diagonal when causal; with a
   // sliding window of W keys, from the tile holding key (first row - W + 1)
@@ -103,14 +234,28 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int t = 0; t < NT; ++t) {
     const int r = row0 + t * BM;
     if (r >= Nr) n_t[t] = 0;
-    else if (CAUSAL) n_t[t] = min(nkv, min(r + BM - 1, Nr - 1) / BN + 1);
+    else if (PAGED) {
+      paged_tiles(kr, r, Nr, window, lo_t[t], n_t[t]);
+      continue;
+    } else if (CAUSAL) n_t[t] = min(nkv, min(r + BM - 1, Nr - 1) / BN + 1);
     else n_t[t] = nkv;
     lo_t[t] = WINDOW ? max(0, r - window + 1) / BN : 0;
   }
   const int j0 = lo_t[0];                       // the stream starts at tile 0's first KV tile
   const int n_max = max(n_t[0], n_t[1]);
   const int n_stream = n_max - j0;              // KV tiles loaded, j0 .. n_max - 1
-  if (n_stream <= 0) return;                    // query tiles past the end of a packed sequence
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  // row `grow` sees no key: O = 0, L = -inf
+  auto empty_row = [&](int grow) {
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + sr.off(grow, hq, H, N, D));
+    for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    Lout[static_cast<size_t>(hq) * total + sr.base + grow] = -INFINITY;
+  };
+  if (n_stream <= 0) {                          // query tiles past the end of a packed sequence
+    if constexpr (PAGED)                        // or before the first key
+      for (int r = row0 + threadIdx.x; r < min(row0 + NT * BM, Nr); r += THREADS) empty_row(r);
+    return;
+  }
 
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8 * i; };
   const int B_QF = 0;
@@ -146,7 +291,46 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     regs_dec<kRegsLow>();                          // warpgroup 0 (TMA, MMA issue): few registers
     // ------------------------------------------------------------ producer
-    if (lane == 0 && n_stream > 0) {
+    if constexpr (PAGED) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(B_QF), NT * C::TILE_BYTES);
+        for (int t = 0; t < NT; ++t)
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_3d(sb + C::Q_OFF + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ, bar(B_QF),
+                        c * C::ATOM, cy(row0 + t * BM, hq), cz(row0 + t * BM, hq));
+      }
+      bool ok = true;
+      PagedTile next;
+      next.smem_mask = sb + C::MASK_OFF;
+      paged_fetch(px, bh / H, kr, j0 * BN, lane, next);
+      int j = 0;
+      for (; j < n_stream; ++j) {
+        const int s = j % C::STAGES;
+        const uint32_t ph = (j / C::STAGES) & 1;
+        const PagedTile cur = next;
+        if (j + 1 < n_stream) paged_fetch(px, bh / H, kr, (j0 + j + 1) * BN, lane, next);
+        if (!(ok = mbar_wait_warp(bar(B_KE(s)), ph ^ 1, ctl))) break;
+        // the slot's last readers were the softmax threads of tile j - 8: they are done,
+        // since S(j - 2), whose K tile has just been released, waited for their P
+        paged_mask(px, lane, cur, j % kMaskSlots);
+        if (lane == 0) mbar_arrive_expect_tx(bar(B_KF(s)), C::TILE_BYTES);
+        __syncwarp();
+        paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), hk, lane, cur);
+        if (!(ok = mbar_wait_warp(bar(B_VE(s)), ph ^ 1, ctl))) { ++j; break; }
+        if (lane == 0) mbar_arrive_expect_tx(bar(B_VF(s)), C::TILE_BYTES);
+        __syncwarp();
+        paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), hk, lane, cur);
+      }
+      if (!ok) {                                // as below: wait for the copies in flight
+        mbar_wait_warp(bar(B_QF), 0, ctl);
+        for (int jj = max(0, j - C::STAGES); jj < j; ++jj) {
+          const int s = jj % C::STAGES;
+          const uint32_t ph = (jj / C::STAGES) & 1;
+          mbar_wait_warp(bar(B_KF(s)), ph, ctl);
+          mbar_wait_warp(bar(B_VF(s)), ph, ctl);
+        }
+      }
+    } else if (lane == 0 && n_stream > 0) {
       bool ok = true;
       mbar_arrive_expect_tx(bar(B_QF), NT * C::TILE_BYTES);
       for (int t = 0; t < NT; ++t)
@@ -268,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tO = tmem + lane_off + C::O_COL + t * D;
     const int nt = n_t[t] - lo_t[t];             // this tile's KV tiles, from lo_t[t]
     const int tile_row0 = row0 + t * BM;
-    const int lo_key = WINDOW ? grow - window + 1 : 0;   // first allowed key
+    const int lo_key = WINDOW ? grow + kr.off - window + 1 : 0;   // first allowed key
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -286,13 +470,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int kbase = (lo_t[t] + j) * BN;
       // masks: causal on the diagonal tile, key padding on the last tile, and with a
       // window the tiles reaching left of some row's first allowed key
-      const bool need_mask = (CAUSAL && kbase + BN - 1 > tile_row0) || (kbase + BN > Nr) ||
-                             (WINDOW && kbase < tile_row0 + BM - window);
+      const bool need_mask = (CAUSAL && kbase + BN - 1 > tile_row0 + kr.hi) || (kbase + BN > Nk) ||
+                             (WINDOW && kbase < tile_row0 + kr.off + BM - window);
       if (need_mask) {
-        const int lim = CAUSAL ? min(grow + 1, Nr) : Nr;   // keys in [lo_key, lim) are allowed
+        const int lim = CAUSAL ? min(grow + kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr[c] = __float_as_uint(-INFINITY);
+      }
+      if constexpr (PAGED) {
+        const int jj = lo_t[t] + j - j0;         // stream position
+        paged_holes(sb + C::MASK_OFF + (jj % kMaskSlots) * 16, sr);
+        if (kbase + BN > Nk) {                   // the last tile's V rows past the keys
+          if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
+          if (kbase + rit >= Nk) clear_row<D>(sb + C::V_OFF + (jj % C::STAGES) * C::TILE_BYTES, rit);
+          fence_proxy_async_smem();              // before this thread's arrival on p_full
+        }
       }
       // row maximum: four independent chains of 3-input max
       const float mx = row_max128(sr);
@@ -343,9 +536,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (ok && nt > 0 && mbar_wait_warp(bar(B_OF(t)), 0, ctl)) {
       tc_fence_after();
-      const float inv_l = 1.f / l_run;
+      // a row whose keys are all masked (paged only): l = 0 and acc = 0
+      const bool none = PAGED && l_run == 0.f;
+      const float inv_l = none ? 0.f : 1.f / l_run;
       const bool valid = grow < Nr;
-      using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* orow = reinterpret_cast<T*>(Out) + sr.off(grow, hq, H, N, D);
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
@@ -367,7 +561,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (valid)
         Lout[sr.packed ? static_cast<size_t>(hq) * total + sr.base + grow
                        : static_cast<size_t>(bh) * N + grow] =
-            (m_run + log2f(l_run)) * 0.69314718055994531f;
+            none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+    } else if (PAGED && nt <= 0 && grow < Nr) {
+      empty_row(grow);
     }
   } else {
     regs_dec<kRegsLow>();                          // warps 2 and 3: idle
@@ -381,21 +577,33 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
+template <bool PAGED>
+PagedArgs<PAGED> paged_args(const FwdArgs& a) {
+  PagedArgs<PAGED> px;
+  if constexpr (PAGED) {
+    px.pg = a.pg;
+    px.box_log2 = a.box_log2;
+    px.causal = a.causal;
+  }
+  return px;
+}
+
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED = false>
 cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
-  auto kern = fwd_kernel<D, BF16, CAUSAL, WINDOW, PACKED>;
+  constexpr int smem = PAGED ? C::PAGED_SMEM_BYTES : C::SMEM_BYTES;
+  auto kern = fwd_kernel<D, BF16, CAUSAL, WINDOW, PACKED, PAGED>;
   cudaError_t e = check_split_regs(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
-  e = ensure_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
+  e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int n_qblk = (a.N + NT * BM - 1) / (NT * BM);
   const long long grid = static_cast<long long>(n_qblk) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
-  e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, C::SMEM_BYTES, st, a.tmQ,
+  e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, smem, st, a.tmQ,
                        a.tmK, a.tmV, a.O, a.L, a.N, n_qblk, a.group, a.window, a.cu_seqlens, a.H,
-                       a.total, a.c_log2, a.ctl);
+                       a.total, a.c_log2, a.ctl, paged_args<PAGED>(a));
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -442,10 +650,12 @@ struct Cfg1 {
   static constexpr int CLC_OFF = (BAR_OFF + NBARS * 8 + 15) / 16 * 16;   // 16-byte response
   static constexpr int SLOT_OFF = CLC_OFF + 16;             // TMEM base, tile slots[2]
   static constexpr int SMEM_BYTES = SLOT_OFF + 16;
+  static constexpr int MASK_OFF = SLOT_OFF + 16;            // paged: key masks
+  static constexpr int PAGED_SMEM_BYTES = MASK_OFF + 8 * 16;
   static constexpr int TMEM_COLS = 256;
   static constexpr uint32_t S_COL = 0, P_COL = 128, O_COL = 192;
   // two CTAs per SM, each with the 1 KiB the system reserves per CTA
-  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM must fit");
+  static_assert(2 * (PAGED_SMEM_BYTES + 1024) <= 233472, "two CTAs per SM must fit");
   static_assert(O_COL + D <= TMEM_COLS, "TMEM layout");
 };
 
@@ -453,10 +663,12 @@ struct Cfg1 {
 struct Tile1 {
   int bh, hq, hk, row0, lo, nt;
   SeqRows sr;
+  KeyRows kr;
 };
-template <bool CAUSAL, bool WINDOW, bool PACKED>
+template <bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
 __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int window,
-                                       const int* __restrict__ cu_seqlens, int H, int total) {
+                                       const int* __restrict__ cu_seqlens, int H, int total,
+                                       const PagedArgs<PAGED>& px) {
   Tile1 t;
   const BlockPos bp = block_pos(n_qt, id);
   t.bh = bp.bh;
@@ -466,6 +678,13 @@ __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int w
   t.hq = t.sr.packed ? t.bh % H : t.bh;
   t.hk = t.sr.packed ? (t.bh % H) / group : t.bh / group;
   t.row0 = qt * BM;
+  t.kr = key_rows(px, t.bh / H, Nr);
+  if constexpr (PAGED) {
+    int hi;
+    paged_tiles(t.kr, t.row0, Nr, window, t.lo, hi);
+    t.nt = t.row0 >= Nr ? 0 : hi - t.lo;
+    return t;
+  }
   // up to the diagonal when causal; with a sliding window of W keys, from the tile
   // holding key (first row - W + 1); none for a tile past the end of a packed sequence
   const int nkv = (Nr + BN - 1) / BN;
@@ -476,13 +695,13 @@ __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int w
 }
 }  // namespace one
 
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
 __global__ void __launch_bounds__(one::THREADS, 2)
     fwd1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, void* __restrict__ Out,
                 float* __restrict__ Lout, int N, int n_qt, int group, int window,
                 const int* __restrict__ cu_seqlens, int H, int total, float c_log2,
-                KernelCtl ctl) {
+                KernelCtl ctl, const PagedArgs<PAGED> px) {
   using C = Cfg<D>;
   using C1 = one::Cfg1<D>;
   constexpr int STAGES = C1::STAGES;
@@ -496,7 +715,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto tile_of = [&](int id) {
-    return one::tile1<CAUSAL, WINDOW, PACKED>(id, n_qt, N, group, window, cu_seqlens, H, total);
+    return one::tile1<CAUSAL, WINDOW, PACKED, PAGED>(id, n_qt, N, group, window, cu_seqlens, H,
+                                                     total, px);
   };
 
   auto bar = [&](int i) -> uint32_t { return sb + C1::BAR_OFF + 8 * i; };
@@ -545,16 +765,23 @@ __global__ void __launch_bounds__(one::THREADS, 2)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer, scheduler
-    if (lane == 0) {
+    // one thread; for paged keys the whole warp, whose first lane does what is done once
+    if (PAGED || lane == 0) {
+      const bool lead = !PAGED || lane == 0;
+      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        return PAGED ? mbar_wait_warp(b, parity, ctl) : mbar_wait(b, parity, ctl);
+      };
       bool ok = true;
       int tile = static_cast<int>(blockIdx.x);
       int g = 0, kq = 0, nk = 0, nv = 0;         // steps, Q tiles, K and V tiles loaded
       bool pending = false;                       // a request for the next tile is out
       int n_req = 0;                               // requests made
       for (int k = 0; ok; ++k) {
-        if (!(ok = mbar_wait(bar(B_TE(k & 1)), ((k >> 1) & 1) ^ 1, ctl))) break;
-        slot[k & 1] = tile;
-        mbar_arrive(bar(B_TF(k & 1)));          // release: the slot write is seen with the phase
+        if (!(ok = wait(bar(B_TE(k & 1)), ((k >> 1) & 1) ^ 1))) break;
+        if (lead) {
+          slot[k & 1] = tile;
+          mbar_arrive(bar(B_TF(k & 1)));        // release: the slot write is seen with the phase
+        }
         if (tile < 0) break;
         // ask for the next tile together with this tile's last loads: early enough that
         // the answer is there when they complete, late enough that a CTA takes a tile
@@ -562,8 +789,10 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         // CTAs that still had most of a long tile ahead, and took tiles from CTAs that had
         // not started yet when all would have fit at once)
         auto request = [&]() {
-          mbar_arrive_expect_tx(bar(B_CLC), 16);
-          clc_try_cancel(clc_resp, bar(B_CLC));
+          if (lead) {
+            mbar_arrive_expect_tx(bar(B_CLC), 16);
+            clc_try_cancel(clc_resp, bar(B_CLC));
+          }
           pending = true;
           ++n_req;
         };
@@ -571,46 +800,70 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         if (t.nt <= 0) request();
         if (t.nt > 0) {
           const int qb = kq & 1;
-          if (!(ok = mbar_wait(bar(B_QE(qb)), ((kq >> 1) & 1) ^ 1, ctl))) break;
-          mbar_arrive_expect_tx(bar(B_QF(qb)), C1::TILE_BYTES);
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_3d(sb + C1::Q_OFF + qb * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ,
-                        bar(B_QF(qb)), c * C::ATOM, t.sr.y(t.row0, t.hq), t.sr.z(t.row0, t.hq));
+          if (!(ok = wait(bar(B_QE(qb)), ((kq >> 1) & 1) ^ 1))) break;
+          if (lead) {
+            mbar_arrive_expect_tx(bar(B_QF(qb)), C1::TILE_BYTES);
+            for (int c = 0; c < C::NCHUNK; ++c)
+              tma_load_3d(sb + C1::Q_OFF + qb * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ,
+                          bar(B_QF(qb)), c * C::ATOM, t.sr.y(t.row0, t.hq), t.sr.z(t.row0, t.hq));
+          }
           ++kq;
+          PagedTile next;
+          next.smem_mask = sb + C1::MASK_OFF;
+          if constexpr (PAGED) paged_fetch(px, t.bh / H, t.kr, t.lo * BN, lane, next);
           for (int j = 0; j < t.nt; ++j, ++g) {
             const int st = g % STAGES;
             const uint32_t ph = (g / STAGES) & 1;
             const int krow = (t.lo + j) * BN;
-            if (!(ok = mbar_wait(bar(B_KE(st)), ph ^ 1, ctl))) break;
-            mbar_arrive_expect_tx(bar(B_KF(st)), C1::TILE_BYTES);
-            for (int c = 0; c < C::NCHUNK; ++c)
-              tma_load_3d(sb + C1::K_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmK,
-                          bar(B_KF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
+            const PagedTile cur = next;
+            if constexpr (PAGED)
+              if (j + 1 < t.nt) paged_fetch(px, t.bh / H, t.kr, krow + BN, lane, next);
+            if (!(ok = wait(bar(B_KE(st)), ph ^ 1))) break;
+            // the mask slot's last readers were the softmax threads of step g - 8: they are
+            // done, since S(g - STAGES), whose K tile has just been released, came two steps
+            // or more after theirs
+            if constexpr (PAGED) paged_mask(px, lane, cur, g % kMaskSlots);
+            if (lead) mbar_arrive_expect_tx(bar(B_KF(st)), C1::TILE_BYTES);
+            if constexpr (PAGED) {
+              __syncwarp();
+              paged_load<D>(px, &tmK, sb + C1::K_OFF + st * C1::TILE_BYTES, bar(B_KF(st)), t.hk,
+                            lane, cur);
+            } else {
+              for (int c = 0; c < C::NCHUNK; ++c)
+                tma_load_3d(sb + C1::K_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmK,
+                            bar(B_KF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
+            }
             ++nk;
-            if (!(ok = mbar_wait(bar(B_VE(st)), ph ^ 1, ctl))) break;
-            mbar_arrive_expect_tx(bar(B_VF(st)), C1::TILE_BYTES);
-            for (int c = 0; c < C::NCHUNK; ++c)
-              tma_load_3d(sb + C1::V_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmV,
-                          bar(B_VF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
+            if (!(ok = wait(bar(B_VE(st)), ph ^ 1))) break;
+            if (lead) mbar_arrive_expect_tx(bar(B_VF(st)), C1::TILE_BYTES);
+            if constexpr (PAGED) {
+              __syncwarp();
+              paged_load<D>(px, &tmV, sb + C1::V_OFF + st * C1::TILE_BYTES, bar(B_VF(st)), t.hk,
+                            lane, cur);
+            } else {
+              for (int c = 0; c < C::NCHUNK; ++c)
+                tma_load_3d(sb + C1::V_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmV,
+                            bar(B_VF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
+            }
             ++nv;
             if (j + 1 == t.nt) request();
           }
           if (!ok) break;
         }
         // the next tile: a CTA that had not started, if any was left
-        if (!(ok = mbar_wait(bar(B_CLC), k & 1, ctl))) break;
+        if (!(ok = wait(bar(B_CLC), k & 1))) break;
         pending = false;
         tile = clc_result(clc_resp);
       }
       if (!ok) {
-        if (pending) mbar_wait(bar(B_CLC), (n_req - 1) & 1, ctl);   // the response lands in smem
+        if (pending) wait(bar(B_CLC), (n_req - 1) & 1);   // the response lands in smem
         // drain: wait (bounded) for the copies this thread may still have in flight, so
         // no bulk copy lands in shared memory after the CTA has gone
-        for (int i = max(0, kq - 2); i < kq; ++i) mbar_wait(bar(B_QF(i & 1)), (i >> 1) & 1, ctl);
+        for (int i = max(0, kq - 2); i < kq; ++i) wait(bar(B_QF(i & 1)), (i >> 1) & 1);
         for (int i = max(0, nk - STAGES); i < nk; ++i)
-          mbar_wait(bar(B_KF(i % STAGES)), (i / STAGES) & 1, ctl);
+          wait(bar(B_KF(i % STAGES)), (i / STAGES) & 1);
         for (int i = max(0, nv - STAGES); i < nv; ++i)
-          mbar_wait(bar(B_VF(i % STAGES)), (i / STAGES) & 1, ctl);
+          wait(bar(B_VF(i % STAGES)), (i / STAGES) & 1);
       }
     }
     __syncwarp();
@@ -701,10 +954,18 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (lane == 0) mbar_arrive(bar(B_TE(k & 1)));
       if (tile < 0) break;
       const one::Tile1 t = tile_of(tile);
-      if (t.nt == 0) continue;
-      const int Nr = t.sr.n;
+      const int Nr = t.sr.n, Nk = PAGED ? t.kr.n : Nr;   // query rows, keys
       const int grow = t.row0 + rit;             // query row
-      const int lo_key = WINDOW ? grow - window + 1 : 0;   // first allowed key
+      if (t.nt == 0) {
+        if (PAGED && grow < Nr) {                // a row before the first key: O = 0, L = -inf
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(Out) +
+                                                t.sr.off(grow, t.hq, H, N, D));
+          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+          Lout[static_cast<size_t>(t.hq) * total + t.sr.base + grow] = -INFINITY;
+        }
+        continue;
+      }
+      const int lo_key = WINDOW ? grow + t.kr.off - window + 1 : 0;   // first allowed key
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < t.nt; ++j, ++g) {
         if (!(ok = mbar_wait_warp(bar(B_SF), g & 1, ctl))) break;
@@ -723,13 +984,22 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         const int kbase = (t.lo + j) * BN;
         // masks: causal on the diagonal tile, key padding on the last tile, and with a
         // window the tiles reaching left of some row's first allowed key
-        const bool need_mask = (CAUSAL && kbase + BN - 1 > t.row0) || (kbase + BN > Nr) ||
-                               (WINDOW && kbase < t.row0 + BM - window);
+        const bool need_mask = (CAUSAL && kbase + BN - 1 > t.row0 + t.kr.hi) || (kbase + BN > Nk) ||
+                               (WINDOW && kbase < t.row0 + t.kr.off + BM - window);
         if (need_mask) {
-          const int lim = CAUSAL ? min(grow + 1, Nr) : Nr;   // keys in [lo_key, lim) are allowed
+          const int lim = CAUSAL ? min(grow + t.kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr_[c] = __float_as_uint(-INFINITY);
+        }
+        if constexpr (PAGED) {
+          paged_holes(sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
+          if (kbase + BN > Nk) {                 // the last tile's V rows past the keys
+            const int st = g % STAGES;
+            if (!(ok = mbar_wait_warp(bar(B_VF(st)), (g / STAGES) & 1, ctl))) break;
+            if (kbase + rit >= Nk) clear_row<D>(sb + C1::V_OFF + st * C1::TILE_BYTES, rit);
+            fence_proxy_async_smem();            // before this thread's arrival on p_full
+          }
         }
         const float mx = row_max128(sr_);
         const float m_tile = mx * c_log2;
@@ -797,7 +1067,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (!(ok = mbar_wait_warp(bar(B_OF), kq & 1, ctl))) break;
       ++kq;
       tc_fence_after();
-      const float inv_l = 1.f / l_run;
+      // a row whose keys are all masked (paged only): l = 0 and acc = 0
+      const bool none = PAGED && l_run == 0.f;
+      const float inv_l = none ? 0.f : 1.f / l_run;
       const bool valid = grow < Nr;
       // Each thread writes its row of O (16-bit) to this warp's 32 staging rows in shared
       // memory, 16-byte chunk c of row r at chunk c ^ (r mod CPR), so the eight lanes of
@@ -824,7 +1096,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (valid)
         Lout[t.sr.packed ? static_cast<size_t>(t.hq) * total + t.sr.base + grow
                          : static_cast<size_t>(t.bh) * N + grow] =
-            (m_run + log2f(l_run)) * 0.69314718055994531f;
+            none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
       __syncwarp();
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       constexpr int RPI = 32 / CPR;              // rows per store instruction
@@ -849,19 +1121,20 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   }
 }
 
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED = false>
 cudaError_t launch_fwd1_t(const FwdArgs& a, cudaStream_t st) {
   using C1 = one::Cfg1<D>;
-  auto kern = fwd1_kernel<D, BF16, CAUSAL, WINDOW, PACKED>;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C1::SMEM_BYTES);
+  constexpr int smem = PAGED ? C1::PAGED_SMEM_BYTES : C1::SMEM_BYTES;
+  auto kern = fwd1_kernel<D, BF16, CAUSAL, WINDOW, PACKED, PAGED>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int n_qt = (a.N + BM - 1) / BM;
   const long long grid = static_cast<long long>(n_qt) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
-  e = launch_dependent(kern, static_cast<unsigned>(grid), one::THREADS, C1::SMEM_BYTES, st, a.tmQ,
+  e = launch_dependent(kern, static_cast<unsigned>(grid), one::THREADS, smem, st, a.tmQ,
                        a.tmK, a.tmV, a.O, a.L, a.N, n_qt, a.group, a.window, a.cu_seqlens, a.H,
-                       a.total, a.c_log2, a.ctl);
+                       a.total, a.c_log2, a.ctl, paged_args<PAGED>(a));
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -899,6 +1172,23 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int d, bool bf16, bool causal, bool w
                          cudaStream_t st) {
   return bf16 ? launch_fwd_b<true>(a, d, causal, window, packed, st)
               : launch_fwd_b<false>(a, d, causal, window, packed, st);
+}
+
+// Queries packed, keys in pages: one instance per head dim and type, its masks at run time
+// (no window: one that reaches past every key).
+template <bool BF16>
+cudaError_t launch_fwd_paged_b(const FwdArgs& a, int d, cudaStream_t st) {
+  if (d == 32) return launch_fwd1_t<32, BF16, true, true, true, true>(a, st);
+  if (d == 64) return launch_fwd1_t<64, BF16, true, true, true, true>(a, st);
+  if (d == 128) return launch_fwd_t<128, BF16, true, true, true, true>(a, st);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_fwd_paged(const FwdArgs& args, int d, bool bf16, bool causal, cudaStream_t st) {
+  FwdArgs a = args;
+  a.causal = causal;
+  if (!causal || a.window == 0) a.window = kNoLimit;
+  return bf16 ? launch_fwd_paged_b<true>(a, d, st) : launch_fwd_paged_b<false>(a, d, st);
 }
 
 cudaError_t launch_fwd(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st) {

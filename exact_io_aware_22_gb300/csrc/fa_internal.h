@@ -82,6 +82,16 @@ struct FwdTileInfo {
 };
 FwdTileInfo fwd_tile_info(int d);
 
+// Paged caches (fa_paged_cache in fa.h): pages of page.div rows, addressed through a table of
+// max_pages ids per sequence.
+struct PagedView {
+  const int* table;            // device int32, rows table_stride entries apart
+  const int* seqlens;          // device int32 [B]: keys per sequence
+  long long table_stride;
+  int pages, max_pages;        // pages in the pools, ids per sequence
+  FastDiv page;                // page size
+};
+
 struct FwdArgs {
   CUtensorMap tmQ, tmK, tmV;   // 3-D maps (d, N, B*H) of Q; (d, N, B*Hkv) of K and V
   void* O;
@@ -94,10 +104,16 @@ struct FwdArgs {
   // then the longest sequence
   const int* cu_seqlens;
   int H, total;
+  // paged keys (launch_fwd_paged): tmK, tmV are then 4-D maps (d, page_size, Hkv, pages) with
+  // boxes of 1 << box_log2 rows
+  PagedView pg;
+  int box_log2;
+  int causal;
   float c_log2;                // scale * log2(e)
   KernelCtl ctl;
 };
 cudaError_t launch_fwd(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st);
+cudaError_t launch_fwd_paged(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st);
 
 struct BwdArgs {
   CUtensorMap tmQ, tmK, tmV, tmO, tmdO;
@@ -147,16 +163,6 @@ int decode_key_rows(int d, bool c8);
 // Splits and keys per split (written to *chunk) for caches of Nmax keys.
 int decode_parts(int B, int H, int Hkv, int Nmax, int* chunk);
 cudaError_t launch_decode(const DecodeArgs& a, int d, bool bf16, bool c8, cudaStream_t st);
-
-// Paged caches (fa_paged_cache in fa.h): pages of page.div rows, addressed through a table of
-// max_pages ids per sequence.
-struct PagedView {
-  const int* table;            // device int32, rows table_stride entries apart
-  const int* seqlens;          // device int32 [B]: keys per sequence
-  long long table_stride;
-  int pages, max_pages;        // pages in the pools, ids per sequence
-  FastDiv page;                // page size
-};
 
 // Appending new tokens' keys and values, rotated on the way; queries rotated beside them.
 struct AppendArgs {

@@ -328,6 +328,22 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
                               int d, int window, float scale, float k_scale, float v_scale,
                               fa_dtype dtype, void* stream);
 
+/* Forward of many new tokens over a paged cache (a prompt, a later part of one, or drafted
+ * tokens): sequence b holds query rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of the packed Q, the
+ * positions of its last keys (fa_append_paged has put the tokens' keys there): with nq query
+ * rows and nk = cache_seqlens[b] keys, causal query i sees keys j <= nk - nq + i, and with
+ * window > 0 of those the last `window`; not causal: all nk keys.
+ *   Layout   Q, O (total, H, d); L (H, total) as in fa_fwd_varlen; cu_seqlens, total and
+ *            max_seqlen too (offsets that break its rules leave rows uncomputed).  Rows of no
+ *            sequence are left as they were.  A row without keys gets O = 0, L = -inf.
+ *   A V element that is not finite reaches the query rows of its 128-key tile even where the
+ *   causal mask or the window hides its key (0 x NaN), as in fa_fwd; what lies in absent pages
+ *   and past the last key never does.
+ *   Errors   as for the cache and fa_fwd_varlen; FA_ERR_UNSUPPORTED for max_seqlen above 2^29. */
+fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
+                       const int* cu_seqlens, int B, int total, int max_seqlen, int H, int Hkv,
+                       int d, int causal, int window, float scale, fa_dtype dtype, void* stream);
+
 /* Static description of a status code. */
 const char* fa_status_string(fa_status s);
 

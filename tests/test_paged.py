@@ -351,7 +351,171 @@ def test_rope_table_of_far_positions():
         assert (t[p].cpu().double() - torch.cat([a.cos(), a.sin()])).abs().max() <= 2.0 ** -24
 
 
+# ------------------------------------------------------------------ many new tokens
+def run_fwd(new, before, H, Hkv, d, dtype, page, causal=True, window=0, layout="hnd", pad=(0, 0),
+            scale=None, table=None, lens=None, seed=0, qmul=1.0):
+    """new[b] query rows behind before[b] keys (or keys as in ``lens``)."""
+    fa = fa_()
+    lens = [a + b for a, b in zip(new, before)] if lens is None else lens
+    pool = pu.Pool(lens, Hkv, d, page, dtype, layout, seed=seed)
+    if table is not None:
+        table(pool)
+    g = torch.Generator().manual_seed(seed + 3)
+    total, t = sum(new) + sum(pad), pu.DT[dtype]
+    q = (torch.randn((total, H, d), generator=g) * qmul).to(t)
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    cu = [pad[0] + sum(new[:i]) for i in range(len(new) + 1)]
+    kc, vc, tb, sl = pool.cuda()
+    o = torch.full((total, H, d), 7.0, dtype=t, device="cuda")
+    lse = torch.full((H, total), 7.0, device="cuda")
+    r = fa.fwd_paged(q.cuda(), kc, vc, tb, sl, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                     max(max(new), 1), causal=causal, scale=scale, window=window, out=o, lse=lse)
+    ok()
+    assert r[0] is o and r[1] is lse
+    worst = []
+    for b, m in enumerate(new):
+        if m == 0:
+            continue
+        rows = slice(cu[b], cu[b] + m)
+        at = torch.arange(lens[b] - m, lens[b])
+        ref = pu.reference(pool, q[rows], b, at, scale, causal, window)
+        worst.append(pu.check_rows(o[rows], lse[:, rows].t(), ref, t, p_half=pu.HALF[t]))
+    print("worst", max(worst))
+    rest = torch.ones(total, dtype=torch.bool)
+    rest[pad[0]:pad[0] + sum(new)] = False
+    assert (o.cpu()[rest] == 7).all() and (lse.cpu()[:, rest] == 7).all(), "rows of no sequence"
+    return o, lse
+
+
+FWD = [
+    # new, before, H, Hkv, d, dtype, page, keywords
+    ((1,), (0,), 2, 1, 128, "bf16", 16, {}),
+    ((5, 5, 5), (100, 300, 0), 8, 2, 128, "bf16", 64, {}),
+    ((130, 1, 257, 64), (500, 127, 0, 64), 4, 2, 128, "bf16", 64, {}),
+    ((130, 1, 257, 64), (500, 127, 0, 64), 4, 4, 64, "fp16", 16, dict(layout="nhd")),
+    ((300, 40), (70, 900), 2, 1, 32, "bf16", 128, dict(layout="pair")),
+    ((300, 40), (70, 900), 2, 1, 32, "fp16", 2, dict(pad=(5, 9))),
+    ((140, 0, 33), (70, 90, 256), 6, 2, 128, "fp16", 1, dict(pad=(1, 130), layout="nhd")),
+    ((140, 0, 33), (70, 90, 256), 6, 2, 64, "bf16", 3, dict(pad=(0, 200))),
+    ((200, 300), (900, 15), 4, 2, 128, "bf16", 20, dict(window=100)),
+    ((200, 300), (900, 15), 4, 2, 64, "fp16", 48, dict(window=1)),
+    ((200, 300), (900, 15), 4, 2, 32, "bf16", 16, dict(window=129)),
+    ((200, 300), (900, 15), 4, 2, 128, "fp16", 256, dict(window=5000)),
+    ((200, 17), (300, 15), 4, 2, 128, "bf16", 100, dict(causal=False)),
+    ((200, 17), (300, 15), 4, 1, 64, "fp16", 8, dict(causal=False, layout="pair")),
+    ((700,), (0,), 2, 2, 64, "bf16", 64, dict(qmul=4.0)),
+    ((300,), (400,), 2, 2, 128, "bf16", 64, dict(scale=1.3)),
+]
+
+
+@pytest.mark.parametrize("case", FWD, ids=[str(c) for c in FWD])
+def test_fwd(case):
+    new, before, H, Hkv, d, dtype, page, kw = case
+    run_fwd(new, before, H, Hkv, d, dtype, page, seed=page, **kw)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16"), (32, "bf16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fwd_more_rows_than_keys(d, dtype, causal):
+    # causal rows before the first key see none; a sequence without any key; a tile of them
+    run_fwd((300, 10, 140, 600), None, 2, 1, d, dtype, 16, causal=causal, lens=[200, 3, 0, 130])
+
+
+@pytest.mark.parametrize("bad", [-1, 2 ** 31 - 1])
+@pytest.mark.parametrize("d,page", [(128, 16), (128, 64), (128, 1), (64, 16), (32, 6), (64, 128)])
+def test_fwd_absent_pages_are_not_attended(bad, d, page):
+    def holes(pool):
+        n = -(-700 // page)
+        pool.table[0, n // 2] = bad
+        pool.table[0, 0] = bad
+        pool.table[1, :] = bad                   # no page at all
+        pool.table[2, -(-40 // page) - 1] = pool.pages
+    run_fwd((200, 30, 20), (500, 10, 20), 4, 2, d, "bf16", page, table=holes)
+
+
+def test_fwd_offsets_that_break_the_rules_touch_nothing_outside():
+    fa = fa_()
+    pool = pu.Pool((90, 60), 2, 64, 16, "bf16")
+    kc, vc, tb, sl = pool.cuda()
+    q = torch.randn(100, 4, 64, device="cuda").bfloat16()
+    for cu in ((0, 200, 50), (-7, 50, 100), (60, 20, 90), (100, 100, 100)):
+        fa.fwd_paged(q, kc, vc, tb, sl, torch.tensor(cu, dtype=torch.int32, device="cuda"), 64)
+    ok()
+
+
+def test_fwd_repeats_and_replays_bit_for_bit():
+    fa = fa_()
+    for d in (128, 64):
+        pool = pu.Pool((700, 400, 33), 2, d, 16, "bf16")
+        kc, vc, tb, sl = pool.cuda()
+        cu = torch.tensor([0, 300, 310, 333], dtype=torch.int32, device="cuda")
+        q = torch.randn(333, 4, d, device="cuda").bfloat16()
+        want = fa.fwd_paged(q, kc, vc, tb, sl, cu, 300)
+        o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            fa.fwd_paged(q, kc, vc, tb, sl, cu, 300, out=o, lse=lse)
+        for _ in range(5):
+            o.zero_()
+            graph.replay()
+            again = fa.fwd_paged(q, kc, vc, tb, sl, cu, 300)
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+            assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+        ok()
+
+
 # ------------------------------------------------------------------ together
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
+def test_prompt_in_parts_equals_the_whole(d, dtype):
+    """Prompts appended and attended in two parts over pages, against fwd_varlen of the whole
+    prompts with the same rotated keys; then the last token again as a decoding step."""
+    fa = fa_()
+    H, Hkv, page, t = 8, 2, 16, pu.DT[dtype]
+    first, second = (200, 1, 64), (77, 130, 300)
+    lens = [a + b for a, b in zip(first, second)]
+    pool = pu.Pool(lens, Hkv, d, page, dtype, fill=float("nan"))
+    pool.store.fill_(float("nan"))
+    kc, vc, tb, _ = pool.cuda()
+    g = torch.Generator().manual_seed(9)
+    total = sum(lens)
+    q, k, v = (torch.randn((total, n, d), generator=g).to(t).cuda() for n in (H, Hkv, Hkv))
+    cs = fa.rope_table(1024, d)
+    starts = [sum(lens[:i]) for i in range(4)]
+
+    def cu(x):
+        return torch.tensor([sum(x[:i]) for i in range(4)], dtype=torch.int32, device="cuda")
+
+    o = torch.empty_like(q)
+    lse = torch.empty(H, total, device="cuda")
+    qr = torch.empty_like(q)
+    done = [0, 0, 0]
+    for part in (first, second):
+        rows = torch.cat([torch.arange(s + a, s + a + n) for s, a, n in zip(starts, done, part)]).cuda()
+        done = [a + n for a, n in zip(done, part)]
+        sl = torch.tensor(done, dtype=torch.int32, device="cuda")
+        qp = fa.append_paged(k[rows], v[rows], kc, vc, tb, sl, cu_seqlens=cu(part), cos_sin=cs,
+                             q=q[rows])
+        op, lp = fa.fwd_paged(qp, kc, vc, tb, sl, cu(part), max(part))
+        o[rows], lse[:, rows], qr[rows] = op, lp, qp
+    # the whole prompts, their rotated keys read back from the pages
+    kr = torch.cat([pool_keys(kc, tb, b, n, page) for b, n in enumerate(lens)])
+    want, lw = fa.fwd_varlen(qr, kr, v, cu(lens), max(lens))
+    ok()
+    assert (o.float() - want.float()).abs().max() <= 4 * pu.HALF[t] * want.float().abs().max()
+    assert (lse - lw).abs().max() <= 1e-5
+    last = torch.tensor([starts[i + 1] - 1 for i in range(3)], device="cuda")
+    od, ld = fa.decode_paged(qr[last], kc, vc, tb, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    ok()
+    assert (o[last].float() - od.float()).abs().max() <= 4 * pu.HALF[t] * want.float().abs().max()
+    assert (lse[:, last].t() - ld).abs().max() <= 1e-5
+
+
+def pool_keys(kc, tb, b, n, page):
+    j = torch.arange(n, device="cuda")
+    return kc[tb[b].long()[j // page], :, j % page].contiguous()
+
+
 @pytest.mark.parametrize("cache", ["16", "e4m3"])
 def test_generation_step_by_step(cache):
     """Prompts appended, then tokens one by one, each attended over what is cached: every step

@@ -149,6 +149,39 @@ def test_append_fp8_rejects(lib, kw, code):
     assert append(lib, fp8=True, **kw) == code
 
 
+def fwd(lib, pc=None, **kw):
+    a = dict(Q=5 * M, O=6 * M, L=7 * M, cu=8 * M, B=3, total=40, max_len=20, H=8, Hkv=2, d=128,
+             causal=1, window=0, scale=0.1, dtype=1)
+    a.update(kw)
+    pc = cache() if pc is None else pc
+    return lib.fa_fwd_paged(a["Q"], ctypes.byref(pc) if pc else None, a["O"], a["L"], a["cu"], a["B"],
+                            a["total"], a["max_len"], a["H"], a["Hkv"], a["d"], a["causal"],
+                            a["window"], a["scale"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,code", CACHE)
+def test_fwd_cache_rejects(lib, kw, code):
+    assert fwd(lib, pc=cache(**kw)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Q=0), INVALID), (dict(O=0), INVALID), (dict(L=0), INVALID), (dict(cu=0), INVALID),
+    (dict(B=0), INVALID), (dict(total=0), INVALID), (dict(max_len=0), INVALID),
+    (dict(max_len=(1 << 29) + 1), UNSUPPORTED), (dict(Hkv=3), INVALID), (dict(window=-1), INVALID),
+    (dict(window=5, causal=0), INVALID), (dict(causal=2), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(d=16), UNSUPPORTED), (dict(dtype=4), UNSUPPORTED), (dict(Q=5 * M + 8), MISALIGNED),
+    (dict(cu=8 * M + 2), MISALIGNED), (dict(L=7 * M + 1), MISALIGNED), (dict(O=5 * M + 4096), INVALID),
+    (dict(O=M), INVALID), (dict(L=2 * M + 64), INVALID), (dict(O=3 * M), INVALID),
+    (dict(L=4 * M), INVALID), (dict(L=8 * M), INVALID), (dict(L=6 * M + 64), INVALID),
+])
+def test_fwd_rejects(lib, kw, code):
+    assert fwd(lib, **kw) == code
+
+
+def test_fwd_without_cache_rejects(lib):
+    assert fwd(lib, pc=False) == INVALID
+
+
 def test_python_calls_refuse_cpu_tensors(lib):
     import exact_io_aware_22_gb300 as fa
     k = torch.zeros(2, 2, 64, dtype=torch.float16)
@@ -158,6 +191,8 @@ def test_python_calls_refuse_cpu_tensors(lib):
         fa.append_paged(k, k, c, c.clone(), t, n)
     with pytest.raises(ValueError, match="CUDA"):
         fa.decode_paged(k, c, c.clone(), t, n)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.fwd_paged(k, c, c.clone(), t, n, n, 1)
 
 
 @pytest.mark.parametrize("kw,what", [
