@@ -90,16 +90,24 @@ struct KeyRows {
   int n, off, hi;
 };
 constexpr int kNoLimit = 1 << 30;
-__device__ __forceinline__ KeyRows key_rows(const PagedArgs<true>& px, int b, int nq) {
+// Query and key rows of sequence b; paged: the three loads go out together.
+template <bool PACKED>
+__device__ __forceinline__ void rows_of(const PagedArgs<true>& px, const int* cu, int b, int N,
+                                        int total, SeqRows& sr, KeyRows& k) {
+  static_assert(PACKED, "paged queries are packed");
+  const int c0 = cu[b], c1 = cu[b + 1], len = px.pg.seqlens[b];
+  const int a = min(max(c0, 0), total), e = min(max(c1, a), total);
+  sr = {a, min(e - a, N), true};
   const long long cap = static_cast<long long>(px.pg.max_pages) * px.pg.page.div;
-  KeyRows k;
-  k.n = static_cast<int>(min(static_cast<long long>(max(px.pg.seqlens[b], 0)), cap));
-  k.off = k.n - nq;
+  k.n = static_cast<int>(min(static_cast<long long>(max(len, 0)), cap));
+  k.off = k.n - sr.n;
   k.hi = px.causal ? k.off : kNoLimit;
-  return k;
 }
-__device__ __forceinline__ KeyRows key_rows(const PagedArgs<false>&, int, int nq) {
-  return {nq, 0, 0};
+template <bool PACKED>
+__device__ __forceinline__ void rows_of(const PagedArgs<false>&, const int* __restrict__ cu, int b,
+                                        int N, int total, SeqRows& sr, KeyRows& k) {
+  sr = seq_rows_t<PACKED>(cu, b, N, total);
+  k = {sr.n, 0, 0};
 }
 // KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of nq, paged keys.
 __device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nq, int window, int& lo,
@@ -111,32 +119,39 @@ __device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nq, int
 
 // One warp's loads of 128-key tiles of a paged cache.  Lane i handles boxes i, i + 32, ...
 struct PagedTile {
-  int id[4], row[4];               // page (-1: absent; past the keys: -2) and first row
-  uint32_t smem_mask;              // ring of 8 key masks of 128 bits
+  int id[4], row[4];               // page id as the table has it, and first row in the page
+  int past;                        // bit i: box lane + 32 i lies past the keys
 };
 constexpr int kMaskSlots = 8;
+// Starts the tile's table loads.  Nothing here uses what they return: the warp would stand
+// still for a load's latency instead of issuing the tile before this one.
 __device__ __forceinline__ void paged_fetch(const PagedArgs<true>& px, int b, const KeyRows& k,
                                             int krow, int lane, PagedTile& t) {
   const int n_box = BN >> px.box_log2;
+  t.past = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int bx = lane + 32 * i, key = krow + (bx << px.box_log2);
-    t.id[i] = -2;
+    t.id[i] = -1;
     t.row[i] = 0;
     if (bx < n_box && key < k.n) {
       const int p = static_cast<int>(px.pg.page.quot(key));
       t.row[i] = key - p * static_cast<int>(px.pg.page.div);
-      const int id = px.pg.table[b * px.pg.table_stride + p];
-      t.id[i] = id >= 0 && id < px.pg.pages ? id : -1;
+      t.id[i] = px.pg.table[b * px.pg.table_stride + p];
+    } else {
+      t.past |= 1 << i;
     }
   }
 }
-// Keys of the tile that exist, as a bit mask, to slot `slot` of the ring (all lanes call).
+__device__ __forceinline__ bool paged_in_pool(const PagedArgs<true>& px, int id) {
+  return id >= 0 && id < px.pg.pages;
+}
+// Keys of the tile that exist, as 128 bits, to the ring slot at `slot` (all lanes call).
 __device__ __forceinline__ void paged_mask(const PagedArgs<true>& px, int lane, const PagedTile& t,
-                                           int slot) {
-  uint32_t have = 0;
+                                           uint32_t slot) {
+  uint32_t have = t.past;                        // keys past the end are masked by their index
 #pragma unroll
-  for (int i = 0; i < 4; ++i) have |= (t.id[i] != -1 ? 1u : 0u) << i;
+  for (int i = 0; i < 4; ++i) have |= (paged_in_pool(px, t.id[i]) ? 1u : 0u) << i;
   uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
   if (__any_sync(0xffffffffu, have != 15u)) {
 #pragma unroll
@@ -147,7 +162,7 @@ __device__ __forceinline__ void paged_mask(const PagedArgs<true>& px, int lane, 
     }
   }
   if (lane == 0)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t.smem_mask + slot * 16),
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot),
                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                  : "memory");
 }
@@ -161,7 +176,7 @@ __device__ __forceinline__ void paged_load(const PagedArgs<true>& px, const CUte
   for (int i = 0; i < 4; ++i) {
     const int bx = lane + 32 * i;
     if (bx < n_box) {
-      const int w = t.id[i] >= 0 ? t.id[i] : px.pg.pages;   // past the pool: zeros
+      const int w = paged_in_pool(px, t.id[i]) ? t.id[i] : px.pg.pages;   // past the pool: zeros
 #pragma unroll
       for (int c = 0; c < C::NCHUNK; ++c)
         tma_load_4d(dst + c * C::CHUNK_BYTES + (bx << px.box_log2) * C::SW, map, bar, c * C::ATOM,
@@ -218,13 +233,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   // Rows of this (batch, head): dense (B, H, N, d) maps are (d, N, B*H), a row at
   // (row, flat head); packed sequences (total, H, d) have maps (d, H, total), a row at
   // (head within the batch, first token + row), and their own length Nr.
-  const SeqRows sr = seq_rows_t<PACKED>(cu_seqlens, bh / H, N, total);
+  SeqRows sr;
+  KeyRows kr;
+  rows_of<PACKED>(px, cu_seqlens, bh / H, N, total, sr, kr);
   const int Nr = sr.n;
   const int hq = sr.packed ? bh % H : bh, hk = sr.packed ? (bh % H) / group : bkv;
   auto cy = [&](int r, int head) { return sr.y(r, head); };
   auto cz = [&](int r, int head) { return sr.z(r, head); };
   const int row0 = qblk * (NT * BM);
-  const KeyRows kr = key_rows(px, bh / H, Nr);
   const int Nk = PAGED ? kr.n : Nr;             // keys
   const int nkv = (Nr + BN - 1) / BN;
   // KV tiles [lo_t[t], n_t[t]) of Q tile t: up to the diagonal when causal; with a
@@ -268,6 +284,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto B_OF = [&](int t) { return 5 + 4 * C::STAGES + t; };
   const int B_DONE = 7 + 4 * C::STAGES;
 
+  PagedTile first_tile;
+  if constexpr (PAGED)                          // its latency passes under the set-up
+    if (warp == 0) paged_fetch(px, bh / H, kr, j0 * BN, lane, first_tile);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBARS; ++i) mbar_init(bar(i), 1);
     for (int t = 0; t < NT; ++t) mbar_init(bar(B_PF(t)), 128);
@@ -300,9 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         c * C::ATOM, cy(row0 + t * BM, hq), cz(row0 + t * BM, hq));
       }
       bool ok = true;
-      PagedTile next;
-      next.smem_mask = sb + C::MASK_OFF;
-      paged_fetch(px, bh / H, kr, j0 * BN, lane, next);
+      PagedTile next = first_tile;
       int j = 0;
       for (; j < n_stream; ++j) {
         const int s = j % C::STAGES;
@@ -312,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!(ok = mbar_wait_warp(bar(B_KE(s)), ph ^ 1, ctl))) break;
         // the slot's last readers were the softmax threads of tile j - 8: they are done,
         // since S(j - 2), whose K tile has just been released, waited for their P
-        paged_mask(px, lane, cur, j % kMaskSlots);
+        paged_mask(px, lane, cur, sb + C::MASK_OFF + (j % kMaskSlots) * 16);
         if (lane == 0) mbar_arrive_expect_tx(bar(B_KF(s)), C::TILE_BYTES);
         __syncwarp();
         paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), hk, lane, cur);
@@ -673,12 +690,11 @@ __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int w
   const BlockPos bp = block_pos(n_qt, id);
   t.bh = bp.bh;
   const int qt = n_qt - 1 - bp.rank;            // causal: the last query tiles have the most work
-  t.sr = seq_rows_t<PACKED>(cu_seqlens, t.bh / H, N, total);
+  rows_of<PACKED>(px, cu_seqlens, t.bh / H, N, total, t.sr, t.kr);
   const int Nr = t.sr.n;
   t.hq = t.sr.packed ? t.bh % H : t.bh;
   t.hk = t.sr.packed ? (t.bh % H) / group : t.bh / group;
   t.row0 = qt * BM;
-  t.kr = key_rows(px, t.bh / H, Nr);
   if constexpr (PAGED) {
     int hi;
     paged_tiles(t.kr, t.row0, Nr, window, t.lo, hi);
@@ -809,7 +825,6 @@ __global__ void __launch_bounds__(one::THREADS, 2)
           }
           ++kq;
           PagedTile next;
-          next.smem_mask = sb + C1::MASK_OFF;
           if constexpr (PAGED) paged_fetch(px, t.bh / H, t.kr, t.lo * BN, lane, next);
           for (int j = 0; j < t.nt; ++j, ++g) {
             const int st = g % STAGES;
@@ -822,7 +837,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
             // the mask slot's last readers were the softmax threads of step g - 8: they are
             // done, since S(g - STAGES), whose K tile has just been released, came two steps
             // or more after theirs
-            if constexpr (PAGED) paged_mask(px, lane, cur, g % kMaskSlots);
+            if constexpr (PAGED) paged_mask(px, lane, cur, sb + C1::MASK_OFF + (g % kMaskSlots) * 16);
             if (lead) mbar_arrive_expect_tx(bar(B_KF(st)), C1::TILE_BYTES);
             if constexpr (PAGED) {
               __syncwarp();
