@@ -109,7 +109,9 @@ def load_library(path: str | None = None):
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_fp8.argtypes = [vp, pc, vp, vp, vp, sz, i, i, i, i, i, f, f, f, i, vp]
     lib.fa_decode_paged_fp8.restype = i
-    lib.fa_fwd_paged.argtypes = [vp, pc, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, vp]
+    lib.fa_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.fa_fwd_paged_workspace_size.restype = sz
+    lib.fa_fwd_paged.argtypes = [vp, pc, vp, vp, vp, sz, vp, i, i, i, i, i, i, i, i, f, i, vp]
     lib.fa_fwd_paged.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -690,14 +692,19 @@ def decode_paged_fp8(q, k_cache8, v_cache8, page_table, cache_seqlens, k_scale: 
                          scale, window, out, lse, workspace)
 
 
+def fwd_paged_workspace_size(B: int, total: int, max_seqlen: int, H: int, Hkv: int, d: int) -> int:
+    return int(load_library().fa_fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d))
+
+
 def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_seqlen: int,
               causal: bool = True, scale: float | None = None, window: int = 0, out=None,
-              lse=None):
+              lse=None, workspace=None):
     """O, L of packed new tokens over a paged cache (see ``append_paged``): q (total, H, d), the
     rows of sequence b at cu_seqlens[b] .. cu_seqlens[b+1]-1 (int32, B+1 entries), its last
     positions: causal row i of nq sees keys up to cache_seqlens[b] - nq + i, with ``window`` > 0
     of those the last ``window``.  max_seqlen bounds every nq.  L is (H, total) fp32; a row
-    without keys gets O = 0, L = -inf."""
+    without keys gets O = 0, L = -inf.  ``workspace``: an optional CUDA tensor of at least
+    ``fwd_paged_workspace_size`` bytes; calls that may overlap need one each."""
     import torch
     dev = _one_device(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens)
     shape, dtype = q.shape, q.dtype
@@ -720,8 +727,19 @@ def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_se
     elif lse.shape != (H, total) or lse.dtype != torch.float32 or not lse.is_contiguous() \
             or lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 (H, total) on q's device")
-    _check(_on_device(dev, load_library().fa_fwd_paged, q.data_ptr(), pc, out.data_ptr(),
-                      lse.data_ptr(), cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d,
+    lib = load_library()
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be contiguous, on q's device")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = lib.fa_fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d)
+        if ws_bytes:                             # torch's allocator, as for out and lse
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    _check(_on_device(dev, lib.fa_fwd_paged, q.data_ptr(), pc, out.data_ptr(),
+                      lse.data_ptr(), ws, ws_bytes, cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d,
                       int(causal), window, 1.0 / math.sqrt(d) if scale is None else scale,
                       _dtype_code(q)), "fa_fwd_paged")
     return out, lse

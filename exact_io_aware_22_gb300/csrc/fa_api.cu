@@ -155,9 +155,11 @@ fa_status make_map(CUtensorMap* m, const void* base, int d, int N, long long BH,
 }
 
 // 3-D map (d, Hx, total) over packed sequences (total, Hx, d): box = one head of one
-// 128-row tile of one swizzle width, laid out in shared memory as make_map's tile.
+// 128-row tile of one swizzle width, laid out in shared memory as make_map's tile (or
+// box_heads heads of as many fewer rows, heads fastest).
 // Rows >= total read as zeros.
-fa_status make_map_packed(CUtensorMap* m, const void* base, int d, int Hx, int total, bool bf16) {
+fa_status make_map_packed(CUtensorMap* m, const void* base, int d, int Hx, int total, bool bf16,
+                          int box_heads = 1) {
   EncodeTiledFn enc;
   fa_status st = get_encoder(&enc);
   if (st != FA_OK) return st;
@@ -166,7 +168,8 @@ fa_status make_map_packed(CUtensorMap* m, const void* base, int d, int Hx, int t
                         static_cast<cuuint64_t>(total)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                            static_cast<cuuint64_t>(Hx) * static_cast<cuuint64_t>(d) * 2};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(ti.box_cols), 1, 128};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(ti.box_cols), static_cast<cuuint32_t>(box_heads),
+                       static_cast<cuuint32_t>(128 / box_heads)};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                    const_cast<void*>(base), dims, strides, box, estr,
@@ -992,16 +995,27 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
+// Bytes of fa_fwd_paged's workspace: each range's O and L of every row, in fp32.
+size_t fwd_paged_ws(int splits, int total, int H, int d) {
+  return splits > 1 ? static_cast<size_t>(splits) * total * H * (d + 1) * sizeof(float) : 0;
+}
+
 fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, float* L,
-                         const int* cu_seqlens, int B, int total, int max_seqlen, int H, int Hkv,
-                         int d, int causal, int window, float scale, fa_dtype dtype, void* stream) {
+                         void* workspace, size_t workspace_bytes, const int* cu_seqlens, int B,
+                         int total, int max_seqlen, int H, int Hkv, int d, int causal, int window,
+                         float scale, fa_dtype dtype, void* stream) {
   fa_status st = check_common(B, H, max_seqlen, d, causal, scale, static_cast<int>(dtype));
   if (st != FA_OK) return st;
   if ((st = check_heads(H, Hkv)) != FA_OK) return st;
   if ((st = check_packed(cu_seqlens, total)) != FA_OK) return st;
   if (window < 0 || (window > 0 && !causal) || !Q || !O || !L) return FA_ERR_INVALID_VALUE;
-  if (max_seqlen > (1 << 29)) return FA_ERR_UNSUPPORTED;
-  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4)) return FA_ERR_MISALIGNED;
+  const int pack = fa::fwd_paged_pack(H / Hkv);
+  if (static_cast<long long>(max_seqlen) << pack > (1 << 29) || B > 65535) return FA_ERR_UNSUPPORTED;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4) || (workspace && !aligned(workspace, 16)))
+    return FA_ERR_MISALIGNED;
+  const int splits = fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d);
+  const size_t need = fwd_paged_ws(splits, total, H, d);
+  if (need && workspace && workspace_bytes < need) return FA_ERR_INVALID_VALUE;
   fa::FwdArgs a;
   std::memset(&a, 0, sizeof(a));
   if ((st = check_paged(cache, Hkv, d, 2, &a.pg)) != FA_OK) return st;
@@ -1012,15 +1026,19 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   const size_t insz[6] = {qb, pb, pb,
                           static_cast<size_t>((B - 1) * c.table_stride + c.max_pages) * 4,
                           static_cast<size_t>(B) * 4, (static_cast<size_t>(B) + 1) * 4};
+  const bool ws_in = need && workspace;
   for (int j = 0; j < 6; ++j)
-    if (overlap(O, qb, ins[j], insz[j]) || overlap(L, lb, ins[j], insz[j]))
+    if (overlap(O, qb, ins[j], insz[j]) || overlap(L, lb, ins[j], insz[j]) ||
+        (ws_in && overlap(workspace, need, ins[j], insz[j])))
       return FA_ERR_INVALID_VALUE;
   if (overlap(O, qb, L, lb)) return FA_ERR_INVALID_VALUE;
+  if (ws_in && (overlap(workspace, need, O, qb) || overlap(workspace, need, L, lb)))
+    return FA_ERR_INVALID_VALUE;
   const bool bf16 = dtype == FA_BF16;
   const int lg = box_rows_log2(c.page_size, 128);
   const CUtensorMapDataType type =
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if ((st = make_map_packed(&a.tmQ, Q, d, H, total, bf16)) != FA_OK) return st;
+  if ((st = make_map_packed(&a.tmQ, Q, d, H, total, bf16, 1 << pack)) != FA_OK) return st;
   if ((st = make_map_paged(&a.tmK, c.K, c, Hkv, d, type, 2, 1u << lg)) != FA_OK) return st;
   if ((st = make_map_paged(&a.tmV, c.V, c, Hkv, d, type, 2, 1u << lg)) != FA_OK) return st;
   if ((st = ctl_for_launch(&a.ctl)) != FA_OK) return st;
@@ -1030,12 +1048,26 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   a.O = O;
   a.L = L;
   a.N = max_seqlen;
-  a.BH = B * H;
   a.group = H / Hkv;
   a.window = window < (1 << 30) ? window : 0;   // no cache holds more keys
   a.box_log2 = lg;
+  a.B = B;
+  a.pack = pack;
+  a.n_split = splits;
   a.c_log2 = scale * 1.4426950408889634f;
-  cudaError_t e = fa::launch_fwd_paged(a, d, bf16, causal != 0, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ws = workspace;
+  if (need && !ws) {
+    cudaError_t e = cudaMallocAsync(&ws, need, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  a.part = static_cast<float*>(ws);
+  a.part_l = a.part + static_cast<size_t>(splits) * total * H * d;
+  cudaError_t e = fa::launch_fwd_paged(a, d, bf16, causal != 0, s);
+  if (need && !workspace) {
+    cudaError_t e2 = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = e2;
+  }
   if (e == cudaErrorInvalidConfiguration) return FA_ERR_UNSUPPORTED;
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
@@ -1089,12 +1121,20 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
                            dtype, stream, true, k_scale, v_scale);
 }
 
+size_t fa_fwd_paged_workspace_size(int B, int total, int max_seqlen, int H, int Hkv, int d) {
+  if (check_common(B, H, max_seqlen, d, 1, 1.f, FA_FP16) != FA_OK || check_heads(H, Hkv) != FA_OK ||
+      total < 1)
+    return 0;
+  return fwd_paged_ws(fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d), total, H, d);
+}
+
 fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
-                       const int* cu_seqlens, int B, int total, int max_seqlen, int H, int Hkv,
-                       int d, int causal, int window, float scale, fa_dtype dtype, void* stream) {
+                       void* workspace, size_t workspace_bytes, const int* cu_seqlens, int B,
+                       int total, int max_seqlen, int H, int Hkv, int d, int causal, int window,
+                       float scale, fa_dtype dtype, void* stream) {
   if (!cu_seqlens) return FA_ERR_INVALID_VALUE;
-  return fwd_paged_impl(Q, cache, O, L, cu_seqlens, B, total, max_seqlen, H, Hkv, d, causal, window,
-                        scale, dtype, stream);
+  return fwd_paged_impl(Q, cache, O, L, workspace, workspace_bytes, cu_seqlens, B, total, max_seqlen,
+                        H, Hkv, d, causal, window, scale, dtype, stream);
 }
 
 }  // extern "C"

@@ -31,6 +31,12 @@
 // ahead and loads them; a 128-row tile is laid out in shared memory as one box would be.
 // Boxes of absent pages read as zeros and their keys are masked; V rows past the last key,
 // which may hold anything, are cleared before the product that reads them (0 x NaN).
+// A query tile of a paged instance holds the rows of 2^pack heads that share a K/V head, heads
+// fastest: the tile of a few new tokens is better filled, K and V pass once for those heads,
+// and less of a tile lies beyond the diagonal.  Where there are fewer query tiles than the
+// GPU runs at once, the KV tiles of each are cut into up to n_split ranges of equal length
+// for as many CTAs, whose results, each normalised with its own L, fwd_paged_merge_kernel
+// joins by their weights 2^(L_s - L).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -83,6 +89,10 @@ template <>
 struct PagedArgs<true> {
   PagedView pg;
   int box_log2, causal;
+  int pack;                        // log2 of the heads in a query tile
+  int n_split;                     // KV ranges per query tile (1: no workspace)
+  float* part;                     // [n_split][total * H][D] results of the ranges
+  float* part_l;                   // [n_split][total * H] their logsumexp (natural log)
 };
 // Keys of a sequence with nq query rows: query row i is at key position i + off and sees keys
 // up to i + hi (all of them unless causal) and from i + off - window + 1.
@@ -109,12 +119,34 @@ __device__ __forceinline__ void rows_of(const PagedArgs<false>&, const int* __re
   sr = seq_rows_t<PACKED>(cu, b, N, total);
   k = {sr.n, 0, 0};
 }
-// KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of nq, paged keys.
-__device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nq, int window, int& lo,
-                                            int& hi) {
-  const int last = min(r + BM - 1, nq - 1) + k.hi;
-  hi = last < 0 ? 0 : min((k.n + BN - 1) / BN, last / BN + 1);
-  lo = min(max(0, r + k.off - window + 1) / BN, hi);
+// KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of a sequence's nr; row i is
+// a head of query i >> pack.
+__device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nr, int window, int pack,
+                                            int& lo, int& hi) {
+  const int last = (min(r + BM - 1, nr - 1) >> pack) + k.hi;
+  hi = r >= nr || last < 0 ? 0 : min((k.n + BN - 1) / BN, last / BN + 1);
+  lo = min(max(0, (r >> pack) + k.off - window + 1) / BN, hi);
+}
+// How the KV tiles [lo, hi) of `TILES` query tiles from row r are cut: ranges of `per` tiles,
+// `used` of them (at least one).
+struct SplitRange {
+  int lo, hi, per, used;
+};
+template <int TILES>
+__device__ __forceinline__ SplitRange split_range(const KeyRows& k, int r, int nr, int window,
+                                                  int pack, int n_split) {
+  SplitRange s;
+  paged_tiles(k, r, nr, window, pack, s.lo, s.hi);
+#pragma unroll
+  for (int t = 1; t < TILES; ++t) {
+    int lo, hi;
+    paged_tiles(k, r + t * BM, nr, window, pack, lo, hi);
+    if (hi > s.hi) s.hi = hi;                    // lo rises with the row
+  }
+  // two tiles at least: the join costs about as much as one
+  s.per = max((s.hi - s.lo + n_split - 1) / n_split, n_split > 1 ? 2 : 1);
+  s.used = max((s.hi - s.lo + s.per - 1) / s.per, 1);
+  return s;
 }
 
 // One warp's loads of 128-key tiles of a paged cache.  Lane i handles boxes i, i + 32, ...
@@ -227,7 +259,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (PACKED) grid_dep_wait();        // the offsets may come from earlier work
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const BlockPos bp = block_pos(n_qblk);
-  const int bh = bp.bh;
+  // paged: bp.bh counts (sequence, block of packed heads, KV range)
+  int bh = bp.bh, split = 0, pack = 0;
+  if constexpr (PAGED) {
+    split = bp.bh % px.n_split;
+    bh = bp.bh / px.n_split;                    // sequence, block of heads
+    pack = px.pack;
+    H >>= pack;                                 // blocks of heads per sequence
+  }
   const int qblk = n_qblk - 1 - bp.rank;        // causal: the last query tiles have the most work
   const int bkv = bh / group;                   // the K/V head of this query head (b-major heads)
   // Rows of this (batch, head): dense (B, H, N, d) maps are (d, N, B*H), a row at
@@ -236,8 +275,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   SeqRows sr;
   KeyRows kr;
   rows_of<PACKED>(px, cu_seqlens, bh / H, N, total, sr, kr);
-  const int Nr = sr.n;
-  const int hq = sr.packed ? bh % H : bh, hk = sr.packed ? (bh % H) / group : bkv;
+  const int Nr = sr.n << pack;
+  // paged: hq is the first of the tile's heads
+  const int hq = sr.packed ? (bh % H) << pack : bh, hk = sr.packed ? hq / group : bkv;
   auto cy = [&](int r, int head) { return sr.y(r, head); };
   auto cz = [&](int r, int head) { return sr.z(r, head); };
   const int row0 = qblk * (NT * BM);
@@ -251,21 +291,46 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int r = row0 + t * BM;
     if (r >= Nr) n_t[t] = 0;
     else if (PAGED) {
-      paged_tiles(kr, r, Nr, window, lo_t[t], n_t[t]);
+      paged_tiles(kr, r, Nr, window, pack, lo_t[t], n_t[t]);
       continue;
     } else if (CAUSAL) n_t[t] = min(nkv, min(r + BM - 1, Nr - 1) / BN + 1);
     else n_t[t] = nkv;
     lo_t[t] = WINDOW ? max(0, r - window + 1) / BN : 0;
   }
-  const int j0 = lo_t[0];                       // the stream starts at tile 0's first KV tile
-  const int n_max = max(n_t[0], n_t[1]);
+  int j0 = lo_t[0];                             // the stream starts at tile 0's first KV tile
+  int n_max = max(n_t[0], n_t[1]);
+  bool shared = false;                          // this CTA has one of several KV ranges
+  if constexpr (PAGED) {
+    const SplitRange sp = split_range<NT>(kr, row0, Nr, window, pack, px.n_split);
+    if (split >= sp.used) return;
+    shared = sp.used > 1;
+    j0 = sp.lo + split * sp.per;
+    n_max = min(j0 + sp.per, sp.hi);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      lo_t[t] = min(max(lo_t[t], j0), n_max);
+      n_t[t] = min(max(n_t[t], j0), n_max);
+    }
+  }
   const int n_stream = n_max - j0;              // KV tiles loaded, j0 .. n_max - 1
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  // row `grow` sees no key: O = 0, L = -inf
+  // paged: where row `grow` lies in O and in L, or in its range's part of the workspace
+  auto row_at = [&](int grow) -> size_t {
+    return static_cast<size_t>(sr.base + (grow >> pack)) * (H << pack) + hq + (grow & ((1 << pack) - 1));
+  };
+  auto lse_at = [&](int grow) -> float* {
+    if constexpr (PAGED)
+      if (shared) return px.part_l + static_cast<size_t>(split) * total * (H << pack) + row_at(grow);
+    return Lout + static_cast<size_t>(hq + (grow & ((1 << pack) - 1))) * total + sr.base +
+           (grow >> pack);
+  };
+  // row `grow` sees no key here: O = 0, L = -inf (a range's O is not read where its L is -inf)
   auto empty_row = [&](int grow) {
-    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + sr.off(grow, hq, H, N, D));
-    for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    Lout[static_cast<size_t>(hq) * total + sr.base + grow] = -INFINITY;
+    if (!shared) {
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at(grow) * D);
+      for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    *lse_at(grow) = -INFINITY;
   };
   if (n_stream <= 0) {                          // query tiles past the end of a packed sequence
     if constexpr (PAGED)                        // or before the first key
@@ -316,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = 0; t < NT; ++t)
           for (int c = 0; c < C::NCHUNK; ++c)
             tma_load_3d(sb + C::Q_OFF + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ, bar(B_QF),
-                        c * C::ATOM, cy(row0 + t * BM, hq), cz(row0 + t * BM, hq));
+                        c * C::ATOM, hq, sr.base + ((row0 + t * BM) >> pack));
       }
       bool ok = true;
       PagedTile next = first_tile;
@@ -469,7 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tO = tmem + lane_off + C::O_COL + t * D;
     const int nt = n_t[t] - lo_t[t];             // this tile's KV tiles, from lo_t[t]
     const int tile_row0 = row0 + t * BM;
-    const int lo_key = WINDOW ? grow + kr.off - window + 1 : 0;   // first allowed key
+    const int qi = grow >> pack;                 // query of the row (paged tiles pack heads)
+    const int lo_key = WINDOW ? qi + kr.off - window + 1 : 0;   // first allowed key
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -487,10 +553,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int kbase = (lo_t[t] + j) * BN;
       // masks: causal on the diagonal tile, key padding on the last tile, and with a
       // window the tiles reaching left of some row's first allowed key
-      const bool need_mask = (CAUSAL && kbase + BN - 1 > tile_row0 + kr.hi) || (kbase + BN > Nk) ||
-                             (WINDOW && kbase < tile_row0 + kr.off + BM - window);
+      const bool need_mask =
+          (CAUSAL && kbase + BN - 1 > (tile_row0 >> pack) + kr.hi) || (kbase + BN > Nk) ||
+          (WINDOW && kbase < ((tile_row0 + BM - 1) >> pack) + 1 + kr.off - window);
       if (need_mask) {
-        const int lim = CAUSAL ? min(grow + kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
+        const int lim = CAUSAL ? min(qi + kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr[c] = __float_as_uint(-INFINITY);
@@ -557,12 +624,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool none = PAGED && l_run == 0.f;
       const float inv_l = none ? 0.f : 1.f / l_run;
       const bool valid = grow < Nr;
-      T* orow = reinterpret_cast<T*>(Out) + sr.off(grow, hq, H, N, D);
+      T* orow = reinterpret_cast<T*>(Out) + (PAGED ? row_at(grow) * D : sr.off(grow, hq, H, N, D));
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * cc, o);
         tmem_ld_wait_regs(o);
+        if constexpr (PAGED) {
+          if (shared) {
+            if (valid) {
+              float4* dst = reinterpret_cast<float4*>(
+                  px.part + (static_cast<size_t>(split) * total * (H << pack) + row_at(grow)) * D + 32 * cc);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(
+                    __uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
+                    __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+            }
+            continue;
+          }
+        }
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -576,8 +657,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (valid)
-        Lout[sr.packed ? static_cast<size_t>(hq) * total + sr.base + grow
-                       : static_cast<size_t>(bh) * N + grow] =
+        (PAGED ? *lse_at(grow)
+               : Lout[sr.packed ? static_cast<size_t>(hq) * total + sr.base + grow
+                                : static_cast<size_t>(bh) * N + grow]) =
             none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
     } else if (PAGED && nt <= 0 && grow < Nr) {
       empty_row(grow);
@@ -601,6 +683,10 @@ PagedArgs<PAGED> paged_args(const FwdArgs& a) {
     px.pg = a.pg;
     px.box_log2 = a.box_log2;
     px.causal = a.causal;
+    px.pack = a.pack;
+    px.n_split = a.n_split;
+    px.part = a.part;
+    px.part_l = a.part_l;
   }
   return px;
 }
@@ -614,7 +700,7 @@ cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int n_qblk = (a.N + NT * BM - 1) / (NT * BM);
+  const int n_qblk = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + NT * BM - 1) / (NT * BM));
   const long long grid = static_cast<long long>(n_qblk) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
@@ -681,6 +767,9 @@ struct Tile1 {
   int bh, hq, hk, row0, lo, nt;
   SeqRows sr;
   KeyRows kr;
+  int nr;                                        // rows of the sequence (queries x packed heads)
+  int split;                                     // paged: its KV range, if it has one of several
+  bool shared;
 };
 template <bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
 __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int window,
@@ -689,18 +778,31 @@ __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int w
   Tile1 t;
   const BlockPos bp = block_pos(n_qt, id);
   t.bh = bp.bh;
+  t.split = 0;
+  t.shared = false;
   const int qt = n_qt - 1 - bp.rank;            // causal: the last query tiles have the most work
-  rows_of<PACKED>(px, cu_seqlens, t.bh / H, N, total, t.sr, t.kr);
-  const int Nr = t.sr.n;
-  t.hq = t.sr.packed ? t.bh % H : t.bh;
-  t.hk = t.sr.packed ? (t.bh % H) / group : t.bh / group;
   t.row0 = qt * BM;
-  if constexpr (PAGED) {
-    int hi;
-    paged_tiles(t.kr, t.row0, Nr, window, t.lo, hi);
-    t.nt = t.row0 >= Nr ? 0 : hi - t.lo;
+  if constexpr (PAGED) {                         // bp.bh: sequence, block of heads, KV range
+    const int hb = H >> px.pack;
+    t.split = bp.bh % px.n_split;
+    t.bh = bp.bh / px.n_split;
+    const int b = t.bh / hb;
+    rows_of<PACKED>(px, cu_seqlens, b, N, total, t.sr, t.kr);
+    t.nr = t.sr.n << px.pack;
+    t.hq = (t.bh % hb) << px.pack;               // the first of the tile's heads
+    t.hk = t.hq / group;
+    t.bh = b * H + t.hq;
+    const SplitRange sp = split_range<1>(t.kr, t.row0, t.nr, window, px.pack, px.n_split);
+    t.shared = sp.used > 1;
+    t.lo = sp.lo + t.split * sp.per;
+    t.nt = max(min(sp.per, sp.hi - t.lo), 0);
+    if (t.split >= sp.used) t.nr = t.nt = 0;     // nothing to do or to write
     return t;
   }
+  rows_of<PACKED>(px, cu_seqlens, t.bh / H, N, total, t.sr, t.kr);
+  const int Nr = t.nr = t.sr.n;
+  t.hq = t.sr.packed ? t.bh % H : t.bh;
+  t.hk = t.sr.packed ? (t.bh % H) / group : t.bh / group;
   // up to the diagonal when causal; with a sliding window of W keys, from the tile
   // holding key (first row - W + 1); none for a tile past the end of a packed sequence
   const int nkv = (Nr + BN - 1) / BN;
@@ -730,6 +832,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int pack = 0;
+  if constexpr (PAGED) pack = px.pack;
   auto tile_of = [&](int id) {
     return one::tile1<CAUSAL, WINDOW, PACKED, PAGED>(id, n_qt, N, group, window, cu_seqlens, H,
                                                      total, px);
@@ -821,7 +925,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
             mbar_arrive_expect_tx(bar(B_QF(qb)), C1::TILE_BYTES);
             for (int c = 0; c < C::NCHUNK; ++c)
               tma_load_3d(sb + C1::Q_OFF + qb * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ,
-                          bar(B_QF(qb)), c * C::ATOM, t.sr.y(t.row0, t.hq), t.sr.z(t.row0, t.hq));
+                          bar(B_QF(qb)), c * C::ATOM, t.sr.y(t.row0, t.hq),
+                          PAGED ? t.sr.base + (t.row0 >> pack) : t.sr.z(t.row0, t.hq));
           }
           ++kq;
           PagedTile next;
@@ -969,18 +1074,28 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (lane == 0) mbar_arrive(bar(B_TE(k & 1)));
       if (tile < 0) break;
       const one::Tile1 t = tile_of(tile);
-      const int Nr = t.sr.n, Nk = PAGED ? t.kr.n : Nr;   // query rows, keys
+      const int Nr = t.nr, Nk = PAGED ? t.kr.n : Nr;   // query rows, keys
       const int grow = t.row0 + rit;             // query row
+      const int qi = grow >> pack;               // its query (paged tiles pack heads)
+      // paged: where a row lies in O, and in L or its range's part of the workspace
+      auto row_at = [&](int r) -> size_t {
+        return static_cast<size_t>(t.sr.base + (r >> pack)) * H + t.hq + (r & ((1 << pack) - 1));
+      };
+      auto lse_at = [&](int r) -> float* {
+        if constexpr (PAGED)
+          if (t.shared) return px.part_l + static_cast<size_t>(t.split) * total * H + row_at(r);
+        return Lout + static_cast<size_t>(t.hq + (r & ((1 << pack) - 1))) * total + t.sr.base +
+               (r >> pack);
+      };
       if (t.nt == 0) {
         if (PAGED && grow < Nr) {                // a row before the first key: O = 0, L = -inf
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(Out) +
-                                                t.sr.off(grow, t.hq, H, N, D));
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(Out) + row_at(grow) * D);
           for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-          Lout[static_cast<size_t>(t.hq) * total + t.sr.base + grow] = -INFINITY;
+          *lse_at(grow) = -INFINITY;
         }
         continue;
       }
-      const int lo_key = WINDOW ? grow + t.kr.off - window + 1 : 0;   // first allowed key
+      const int lo_key = WINDOW ? qi + t.kr.off - window + 1 : 0;   // first allowed key
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < t.nt; ++j, ++g) {
         if (!(ok = mbar_wait_warp(bar(B_SF), g & 1, ctl))) break;
@@ -999,10 +1114,11 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         const int kbase = (t.lo + j) * BN;
         // masks: causal on the diagonal tile, key padding on the last tile, and with a
         // window the tiles reaching left of some row's first allowed key
-        const bool need_mask = (CAUSAL && kbase + BN - 1 > t.row0 + t.kr.hi) || (kbase + BN > Nk) ||
-                               (WINDOW && kbase < t.row0 + t.kr.off + BM - window);
+        const bool need_mask =
+            (CAUSAL && kbase + BN - 1 > (t.row0 >> pack) + t.kr.hi) || (kbase + BN > Nk) ||
+            (WINDOW && kbase < ((t.row0 + BM - 1) >> pack) + 1 + t.kr.off - window);
         if (need_mask) {
-          const int lim = CAUSAL ? min(grow + t.kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
+          const int lim = CAUSAL ? min(qi + t.kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr_[c] = __float_as_uint(-INFINITY);
@@ -1097,6 +1213,20 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         uint32_t o[32];
         tmem_ld32(tO + 32 * cc, o);
         tmem_ld_wait_regs(o);
+        if constexpr (PAGED) {
+          if (t.shared) {
+            if (valid) {
+              float4* dst = reinterpret_cast<float4*>(
+                  px.part + (static_cast<size_t>(t.split) * total * H + row_at(grow)) * D + 32 * cc);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(
+                    __uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
+                    __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+            }
+            continue;
+          }
+        }
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -1109,9 +1239,11 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       }
       tc_fence_before();                         // O read before the next tile's p_full
       if (valid)
-        Lout[t.sr.packed ? static_cast<size_t>(t.hq) * total + t.sr.base + grow
-                         : static_cast<size_t>(t.bh) * N + grow] =
+        (PAGED ? *lse_at(grow)
+               : Lout[t.sr.packed ? static_cast<size_t>(t.hq) * total + t.sr.base + grow
+                                  : static_cast<size_t>(t.bh) * N + grow]) =
             none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+      if (PAGED && t.shared) continue;           // nothing staged
       __syncwarp();
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       constexpr int RPI = 32 / CPR;              // rows per store instruction
@@ -1120,7 +1252,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         const int r = i * RPI + lane / CPR, c = lane % CPR;   // row within the warp, chunk
         const int orow_g = t.row0 + (warp & 3) * 32 + r;
         if (orow_g < Nr) {
-          T* dst = reinterpret_cast<T*>(Out) + t.sr.off(orow_g, t.hq, H, N, D) + 8 * c;
+          T* dst = reinterpret_cast<T*>(Out) +
+                   (PAGED ? row_at(orow_g) * D : t.sr.off(orow_g, t.hq, H, N, D)) + 8 * c;
           *reinterpret_cast<uint4*>(dst) = stage[r * CPR + (c ^ (r % CPR))];
         }
       }
@@ -1143,7 +1276,7 @@ cudaError_t launch_fwd1_t(const FwdArgs& a, cudaStream_t st) {
   auto kern = fwd1_kernel<D, BF16, CAUSAL, WINDOW, PACKED, PAGED>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int n_qt = (a.N + BM - 1) / BM;
+  const int n_qt = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + BM - 1) / BM);
   const long long grid = static_cast<long long>(n_qt) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
@@ -1189,20 +1322,108 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int d, bool bf16, bool causal, bool w
               : launch_fwd_b<false>(a, d, causal, window, packed, st);
 }
 
+// Joins the KV ranges of a query tile: one warp per (query, head) of a sequence, which is
+// left alone where its tile was not cut.  TILES: query tiles of 128 rows that are cut together.
+constexpr int MERGE_THREADS = 128;
+template <int D, bool BF16, int TILES>
+__global__ void __launch_bounds__(MERGE_THREADS)
+    fwd_paged_merge_kernel(void* Out, float* Lout, const int* cu_seqlens, int N, int H, int total,
+                           int window, const PagedArgs<true> px) {
+  grid_dep_wait();                               // the ranges' results
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  SeqRows sr;
+  KeyRows kr;
+  rows_of<true>(px, cu_seqlens, b, N, total, sr, kr);
+  const long long i = static_cast<long long>(blockIdx.x) * (MERGE_THREADS / 32) + (threadIdx.x >> 5);
+  if (i >= static_cast<long long>(sr.n) * H) return;
+  const int q = static_cast<int>(i / H), h = static_cast<int>(i % H);
+  // the row in its block of packed heads, and the first row of its tiles
+  const int row = (q << px.pack) + (h & ((1 << px.pack) - 1));
+  const SplitRange sp = split_range<TILES>(kr, row / (TILES * BM) * (TILES * BM), sr.n << px.pack,
+                                           window, px.pack, px.n_split);
+  if (sp.used <= 1) return;
+  const size_t rows = static_cast<size_t>(total) * H;
+  const size_t at = static_cast<size_t>(sr.base + q) * H + h;
+  float l_max = -INFINITY;
+  for (int s = lane; s < sp.used; s += 32) l_max = fmaxf(l_max, px.part_l[s * rows + at]);
+#pragma unroll
+  for (int w = 16; w >= 1; w /= 2) l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, w));
+  float sum = 0.f, acc[D / 32] = {};
+#pragma unroll 4
+  for (int s = 0; s < sp.used; ++s) {
+    const float ls = px.part_l[s * rows + at];
+    if (ls == -INFINITY) continue;               // no key in this range: nothing was written
+    const float w = ex2((ls - l_max) * 1.4426950408889634f);
+    sum += w;
+    const float* src = px.part + (s * rows + at) * D + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(src[e], w, acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  T* dst = static_cast<T*>(Out) + at * D + lane * (D / 32);
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) {
+    if constexpr (BF16) dst[e] = __float2bfloat16_rn(acc[e] * inv);
+    else dst[e] = __float2half_rn(acc[e] * inv);
+  }
+  if (lane == 0)
+    Lout[static_cast<size_t>(h) * total + sr.base + q] =
+        sum == 0.f ? -INFINITY : l_max + log2f(sum) * 0.69314718055994531f;
+}
+
 // Queries packed, keys in pages: one instance per head dim and type, its masks at run time
 // (no window: one that reaches past every key).
+template <int D, bool BF16>
+cudaError_t launch_fwd_paged_t(const FwdArgs& a, cudaStream_t st) {
+  cudaError_t e;
+  if constexpr (D == 128) e = launch_fwd_t<D, BF16, true, true, true, true>(a, st);
+  else e = launch_fwd1_t<D, BF16, true, true, true, true>(a, st);
+  if (e != cudaSuccess || a.n_split == 1) return e;
+  const long long warps = static_cast<long long>(a.N) * a.H;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps * 32 + MERGE_THREADS - 1) / MERGE_THREADS),
+                     static_cast<unsigned>(a.B));
+  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fwd_paged_merge_kernel<D, BF16, D == 128 ? NT : 1>, a.O, a.L,
+                            a.cu_seqlens, a.N, a.H, a.total, a.window, paged_args<true>(a));
+}
+
 template <bool BF16>
 cudaError_t launch_fwd_paged_b(const FwdArgs& a, int d, cudaStream_t st) {
-  if (d == 32) return launch_fwd1_t<32, BF16, true, true, true, true>(a, st);
-  if (d == 64) return launch_fwd1_t<64, BF16, true, true, true, true>(a, st);
-  if (d == 128) return launch_fwd_t<128, BF16, true, true, true, true>(a, st);
+  if (d == 32) return launch_fwd_paged_t<32, BF16>(a, st);
+  if (d == 64) return launch_fwd_paged_t<64, BF16>(a, st);
+  if (d == 128) return launch_fwd_paged_t<128, BF16>(a, st);
   return cudaErrorInvalidValue;
+}
+
+int fwd_paged_pack(int group) {
+  int p = 0;
+  while (p < 7 && group % (2 << p) == 0) ++p;
+  return p;
+}
+
+// Ranges per query tile: none where the tiles fill half the GPU or more (152 SMs; two CTAs
+// each at d <= 64), else as many as fill it once.
+int fwd_paged_splits(int B, int H, int Hkv, int max_seqlen, int d) {
+  const int pack = fwd_paged_pack(H / Hkv), rows = d == 128 ? NT * BM : BM;
+  const long long tiles = static_cast<long long>(B) * (H >> pack) *
+                          (((static_cast<long long>(max_seqlen) << pack) + rows - 1) / rows);
+  const long long slots = d == 128 ? 152 : 304;
+  return tiles * 2 > slots ? 1 : static_cast<int>(slots / tiles);
 }
 
 cudaError_t launch_fwd_paged(const FwdArgs& args, int d, bool bf16, bool causal, cudaStream_t st) {
   FwdArgs a = args;
   a.causal = causal;
   if (!causal || a.window == 0) a.window = kNoLimit;
+  a.BH = a.B * (a.H >> a.pack) * a.n_split;
   return bf16 ? launch_fwd_paged_b<true>(a, d, st) : launch_fwd_paged_b<false>(a, d, st);
 }
 

@@ -109,11 +109,19 @@ struct FwdArgs {
   PagedView pg;
   int box_log2;
   int causal;
+  int B;
+  int pack;                    // log2 of the heads that share a query tile (0 elsewhere)
+  int n_split;                 // KV ranges per query tile
+  float* part;                 // workspace of the ranges, n_split > 1: results, then their L
+  float* part_l;
   float c_log2;                // scale * log2(e)
   KernelCtl ctl;
 };
 cudaError_t launch_fwd(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st);
 cudaError_t launch_fwd_paged(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st);
+// log2 of the heads packed in a query tile, and KV ranges per query tile, of a paged call.
+int fwd_paged_pack(int group);
+int fwd_paged_splits(int B, int H, int Hkv, int max_seqlen, int d);
 
 struct BwdArgs {
   CUtensorMap tmQ, tmK, tmV, tmO, tmdO;

@@ -405,6 +405,12 @@ FWD = [
     ((200, 17), (300, 15), 4, 1, 64, "fp16", 8, dict(causal=False, layout="pair")),
     ((700,), (0,), 2, 2, 64, "bf16", 64, dict(qmul=4.0)),
     ((300,), (400,), 2, 2, 128, "bf16", 64, dict(scale=1.3)),
+    # keys split over the CTAs, heads packed: 4, 8, 128 and 2 of 6, odd rows
+    ((5,), (6000,), 4, 1, 128, "bf16", 64, {}),
+    ((5, 70, 1), (3000, 0, 700), 16, 2, 128, "fp16", 16, dict(window=900)),
+    ((3, 2), (2500, 300), 128, 1, 64, "bf16", 32, {}),
+    ((33, 7), (2000, 100), 6, 1, 64, "fp16", 16, dict(pad=(2, 3))),
+    ((9, 130), (3000, 700), 12, 2, 32, "bf16", 16, dict(causal=False)),
 ]
 
 
@@ -445,11 +451,13 @@ def test_fwd_offsets_that_break_the_rules_touch_nothing_outside():
 
 def test_fwd_repeats_and_replays_bit_for_bit():
     fa = fa_()
-    for d in (128, 64):
+    # 333 rows: tiles enough at 128 heads, keys split at 4
+    for d, H in ((128, 4), (64, 4), (128, 128), (64, 128)):
         pool = pu.Pool((700, 400, 33), 2, d, 16, "bf16")
         kc, vc, tb, sl = pool.cuda()
         cu = torch.tensor([0, 300, 310, 333], dtype=torch.int32, device="cuda")
-        q = torch.randn(333, 4, d, device="cuda").bfloat16()
+        q = torch.randn(333, H, d, device="cuda").bfloat16()
+        assert (fa.fwd_paged_workspace_size(3, 333, 300, H, 2, d) > 0) == (H == 4)
         want = fa.fwd_paged(q, kc, vc, tb, sl, cu, 300)
         o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
         graph = torch.cuda.CUDAGraph()

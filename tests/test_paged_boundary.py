@@ -150,12 +150,12 @@ def test_append_fp8_rejects(lib, kw, code):
 
 
 def fwd(lib, pc=None, **kw):
-    a = dict(Q=5 * M, O=6 * M, L=7 * M, cu=8 * M, B=3, total=40, max_len=20, H=8, Hkv=2, d=128,
-             causal=1, window=0, scale=0.1, dtype=1)
+    a = dict(Q=5 * M, O=6 * M, L=7 * M, cu=8 * M, ws=0, ws_bytes=0, B=3, total=40, max_len=20, H=8,
+             Hkv=2, d=128, causal=1, window=0, scale=0.1, dtype=1)
     a.update(kw)
     pc = cache() if pc is None else pc
-    return lib.fa_fwd_paged(a["Q"], ctypes.byref(pc) if pc else None, a["O"], a["L"], a["cu"], a["B"],
-                            a["total"], a["max_len"], a["H"], a["Hkv"], a["d"], a["causal"],
+    return lib.fa_fwd_paged(a["Q"], ctypes.byref(pc) if pc else None, a["O"], a["L"], a["ws"],
+                            a["ws_bytes"], a["cu"], a["B"], a["total"], a["max_len"], a["H"], a["Hkv"], a["d"], a["causal"],
                             a["window"], a["scale"], a["dtype"], None)
 
 
@@ -173,9 +173,23 @@ def test_fwd_cache_rejects(lib, kw, code):
     (dict(cu=8 * M + 2), MISALIGNED), (dict(L=7 * M + 1), MISALIGNED), (dict(O=5 * M + 4096), INVALID),
     (dict(O=M), INVALID), (dict(L=2 * M + 64), INVALID), (dict(O=3 * M), INVALID),
     (dict(L=4 * M), INVALID), (dict(L=8 * M), INVALID), (dict(L=6 * M + 64), INVALID),
+    (dict(max_len=(1 << 27) + 1), UNSUPPORTED), (dict(B=65536), UNSUPPORTED),
+    (dict(ws=11 * M, ws_bytes=64), INVALID), (dict(ws=11 * M + 8, ws_bytes=1 << 30), MISALIGNED),
+    (dict(ws=6 * M, ws_bytes=1 << 30), INVALID), (dict(ws=2 * M, ws_bytes=1 << 30), INVALID),
 ])
 def test_fwd_rejects(lib, kw, code):
     assert fwd(lib, **kw) == code
+
+
+def test_fwd_workspace_size(lib):
+    f = lib.fa_fwd_paged_workspace_size
+    # 3 sequences x 2 blocks of 4 packed heads x 1 tile of 256 rows: 152 // 6 = 25 ranges of
+    # 40 x 8 rows of 128 columns and a logsumexp, in fp32
+    assert f(3, 40, 20, 8, 2, 128) == 25 * 40 * 8 * 129 * 4
+    # at d = 64 tiles of 128 rows, two CTAs on each SM
+    assert f(3, 120, 40, 8, 2, 64) == (304 // 12) * 120 * 8 * 65 * 4
+    assert f(4, 4096, 1024, 32, 8, 128) == 0                  # tiles enough
+    assert f(3, 40, 20, 8, 3, 128) == 0 and f(3, 0, 20, 8, 2, 128) == 0
 
 
 def test_fwd_without_cache_rejects(lib):
