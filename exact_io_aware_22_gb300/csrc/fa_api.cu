@@ -992,6 +992,7 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
     cudaError_t e2 = cudaFreeAsync(ws, s);
     if (e == cudaSuccess) e = e2;
   }
+  if (e == cudaErrorInvalidConfiguration) return FA_ERR_UNSUPPORTED;
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

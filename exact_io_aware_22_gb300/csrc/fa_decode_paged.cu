@@ -24,6 +24,8 @@
 // the row that goes on in the next one (slot 1).  Ranges are equal in cost: a row of u units
 // counts 2u + 1, since beginning and ending a row takes about as long as half a unit.  Unit i
 // of a row then sits at the row's position 2i + 1, and a CTA has the units at its positions.
+// Where the table (or the window) bounds every row to a few units, each row has a CTA of its
+// own instead: nothing to scan, nothing to join.
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -174,7 +176,7 @@ template <int D, bool BF16, bool C8, int NT>
 __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     decode_paged_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const void* Q, void* O, float* L,
-                        uint8_t* ws, int B, int H, int Hkv, int window, int box_log2, float c_log2,
+                        uint8_t* ws, int B, int H, int Hkv, int window, int direct, int box_log2, float c_log2,
                         float o_scale, const PagedView pg, KernelCtl ctl) {
   using G = Geom<D, C8>;
   constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT, STAGES = stages_of(NT);
@@ -212,72 +214,90 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
   // CTA = (range, part of the head group); the range's rows are (sequence, K/V head)
   const int grp = H / Hkv, n_rg = (grp + RG - 1) / RG, rg = blockIdx.x % n_rg;
   const int nrow = min(RG, grp - rg * RG);       // heads of this part
-  const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);                // sequences per thread
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    if (b < B) mine += row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * Hkv;
-  }
-  int incl = mine;
-#pragma unroll
-  for (int w = 1; w < 32; w *= 2) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, w);
-    if (lane >= w) incl += o;
-  }
-  volatile int* sc = reinterpret_cast<volatile int*>(smem_raw + (scan - raw));   // [4] sums, [4] start
-  if (lane == 31) sc[warp] = incl;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < DP_WARPS; ++w) {
-    if (w < warp) before += sc[w];
-    total += sc[w];
-  }
-  incl += before;
-  const int cta = blockIdx.x / n_rg, n_cta = gridDim.x / n_rg;   // range index, ranges
-  const int per_cta = max((total - 1) / n_cta + 1, 2);          // positions per CTA
-  const int x0 = static_cast<int>(min(static_cast<long long>(cta) * per_cta,
-                                      static_cast<long long>(total)));
-  const int x1 = x0 + min(per_cta, total - x0);
-  if (x0 < x1 && incl > x0 && incl - mine <= x0) {              // one thread holds position x0
-    int at = incl - mine;
-    for (int i = 0; i < per; ++i) {
-      const int b = threadIdx.x * per + i;
-      const int n = b < B ? row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * Hkv : 0;
-      if (at + n > x0) {
-        sc[4] = b;
-        sc[5] = at;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-
-  // rows of sequences without keys: O = 0, L = -inf
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    if (pg.seqlens[b] > 0) continue;
-    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(O) + static_cast<size_t>(b) * H * D);
-    for (int i = threadIdx.x; i < H * D / 2; i += 32 * DP_WARPS) o[i] = 0u;
-    for (int i = threadIdx.x; i < H; i += 32 * DP_WARPS) L[static_cast<size_t>(b) * H + i] = -INFINITY;
-  }
+  // rows of this part of the head group without keys: O = 0, L = -inf
+  auto empty_heads = [&](int b, int h_first, int n_heads) {
+    const size_t at = static_cast<size_t>(b) * H + h_first;
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(O) + at * D);
+    for (int i = threadIdx.x; i < n_heads * (D / 2); i += 32 * DP_WARPS) o[i] = 0u;
+    for (int i = threadIdx.x; i < n_heads; i += 32 * DP_WARPS) L[at + i] = -INFINITY;
+  };
+  const int cta = blockIdx.x / n_rg;             // range index (direct: row)
   Header* hdr = reinterpret_cast<Header*>(ws);
   float* part = reinterpret_cast<float*>(ws + hdr_bytes(NT));
-  if (x0 >= x1) {
-    if (threadIdx.x == 0) hdr[blockIdx.x].row = -1;
-    return;
-  }
-
   Cursor cur;
-  cur.b = sc[4];
-  cur.s = seq_keys<KEYS, G::UNIT>(pg, cur.b, window);
-  {
+  if (direct) {
+    cur.b = cta / Hkv;
+    cur.r = cta % Hkv;
+    cur.s = seq_keys<KEYS, G::UNIT>(pg, cur.b, window);
+    cur.u = cur.left = 0;
+    cur.ue = cur.s.units;
+    if (cur.ue == 0) {
+      empty_heads(cur.b, cur.r * grp + rg * RG, nrow);
+      return;
+    }
+  } else {
+    const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);                // sequences per thread
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      if (b < B) mine += row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * Hkv;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int w = 1; w < 32; w *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, w);
+      if (lane >= w) incl += o;
+    }
+    volatile int* sc = reinterpret_cast<volatile int*>(smem_raw + (scan - raw));   // [4] sums, [2] start
+    if (lane == 31) sc[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < DP_WARPS; ++w) {
+      if (w < warp) before += sc[w];
+      total += sc[w];
+    }
+    incl += before;
+    const int n_cta = gridDim.x / n_rg;
+    const int per_cta = max((total - 1) / n_cta + 1, 2);          // positions per CTA
+    const int x0 = static_cast<int>(min(static_cast<long long>(cta) * per_cta,
+                                        static_cast<long long>(total)));
+    const int x1 = x0 + min(per_cta, total - x0);
+    if (x0 < x1 && incl > x0 && incl - mine <= x0) {              // one thread holds position x0
+      int at = incl - mine;
+      for (int i = 0; i < per; ++i) {
+        const int b = threadIdx.x * per + i;
+        const int n = b < B ? row_cost(seq_keys<KEYS, G::UNIT>(pg, b, window).units) * Hkv : 0;
+        if (at + n > x0) {
+          sc[4] = b;
+          sc[5] = at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    for (int b = blockIdx.x; b < B; b += gridDim.x)
+      if (pg.seqlens[b] <= 0) empty_heads(b, 0, H);
+    if (x0 >= x1) {
+      if (threadIdx.x == 0) hdr[blockIdx.x].row = -1;
+      return;
+    }
+    cur.b = sc[4];
+    cur.s = seq_keys<KEYS, G::UNIT>(pg, cur.b, window);
     const int w = row_cost(cur.s.units), x = (x0 - sc[5]) % w, take = min(w - x, x1 - x0);
     cur.r = (x0 - sc[5]) / w;
     cur.u = x / 2;
     cur.ue = min(cur.s.units, (x + take) / 2);
     cur.left = x1 - x0 - take;
+    Header h = {-1, 0, 0};
+    if (cur.u > 0 && cur.u < cur.ue) {           // its unit 0 lies in an earlier CTA
+      h.row = cur.b * Hkv + cur.r;
+      h.c0 = (x0 - x + 1) / per_cta;
+      h.c1 = (x0 - x + 2 * cur.s.units - 1) / per_cta;
+    }
+    if (threadIdx.x == 0) hdr[blockIdx.x] = h;
   }
   // to the range's units of the next row that has some; false at its end
   auto next_row = [&](Cursor& x) -> bool {
@@ -297,16 +317,6 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     } while (x.u == x.ue);
     return true;
   };
-  {
-    const int row0 = x0 - (x0 - sc[5]) % row_cost(cur.s.units);   // the first row's position
-    Header h = {-1, 0, 0};
-    if (cur.u > 0 && cur.u < cur.ue) {           // its unit 0 lies in an earlier CTA
-      h.row = cur.b * Hkv + cur.r;
-      h.c0 = (row0 + 1) / per_cta;
-      h.c1 = (row0 + 2 * cur.s.units - 1) / per_cta;
-    }
-    if (threadIdx.x == 0) hdr[blockIdx.x] = h;
-  }
   if (cur.u == cur.ue && !next_row(cur)) return;  // only positions without a unit
 
   // ---------------------------------------------------------------- this warp's ring
@@ -836,6 +846,17 @@ __global__ void __launch_bounds__(DP_MERGE_THREADS)
 // Column blocks of a CTA's products: two when a group has more than 8 heads.
 int n_blocks(int H, int Hkv) { return H / Hkv > 8 ? 2 : 1; }
 
+// Whether each of `rows` rows of at most `units` units gets a CTA of its own.  Measured with
+// 32/8 heads, d = 128, bf16, lengths up to 64 `units`, rows cut against whole (us):
+//   8 units     1 sequence 7.7 / 7.7     8: 9.4 / 9.4     32: 16.8 / 13.0   256: 71.8 / 63.3
+//   16 units    1: 8.2 / 11.5            16: 16.6 / 17.4  32: 24.5 / 21.2   256: 127 / 115
+//   32 units    16: 24.5 / 30.1          64: 67.4 / 68.3  128: 123 / 119    256: 239 / 222
+// Longer rows are cut however many there are: one that is much longer than the others would
+// keep one CTA busy after all the rest.
+bool rows_direct(long long units, long long rows, int slots) {
+  return units <= 8 || (units <= 16 && rows >= 152) || (units <= 32 && rows >= 2 * slots);
+}
+
 template <int D, bool BF16, bool C8, int NT>
 cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   auto kern = decode_paged_kernel<D, BF16, C8, NT>;
@@ -843,17 +864,23 @@ cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const long long cap = static_cast<long long>(a.pg.max_pages) * a.pg.page.div;
-  const long long most =                         // positions, two per range at least
-      a.B * decode_paged_cost(a.Hkv, D, C8, a.window > 0 && a.window < cap ? a.window : cap) / 2;
+  const long long longest = a.window > 0 && a.window < cap ? a.window : cap;
+  const long long cost = decode_paged_cost(a.Hkv, D, C8, longest), most = a.B * cost / 2;
   const int n_rg = (a.H / a.Hkv + 8 * NT - 1) / (8 * NT);
-  const long long fit = grid_of(NT) / n_rg, ranges = most < fit ? (most > 1 ? most : 1) : fit;
+  const bool direct = rows_direct((cost / a.Hkv - 1) / 2, static_cast<long long>(a.B) * a.Hkv * n_rg,
+                                  grid_of(NT));
+  // at least two positions per range, ranges no more than run at once
+  const long long fit = grid_of(NT) / n_rg;
+  const long long ranges = direct ? static_cast<long long>(a.B) * a.Hkv
+                                  : most < fit ? (most > 1 ? most : 1) : fit;
+  if (ranges * n_rg > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(ranges * n_rg);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   trace_begin(TR_DEC_SPLIT, st);
   e = launch_dependent(kern, grid, 32 * DP_WARPS, smem, st, a.tmK, a.tmV, a.Q, a.O, a.L, ws, a.B,
-                       a.H, a.Hkv, a.window, a.box_log2, a.c_log2, a.o_scale, a.pg, a.ctl);
+                       a.H, a.Hkv, a.window, static_cast<int>(direct), a.box_log2, a.c_log2, a.o_scale, a.pg, a.ctl);
   trace_end(TR_DEC_SPLIT, st);
-  if (e != cudaSuccess || ranges == 1) return e;   // no row is cut
+  if (e != cudaSuccess || direct || ranges == 1) return e;   // no row is cut
   trace_begin(TR_DEC_MERGE, st);
   e = launch_dependent(decode_paged_merge_kernel<D, BF16>, grid, DP_MERGE_THREADS, 0, st,
                        static_cast<const uint8_t*>(ws), a.O, a.L, a.H, a.Hkv, NT, a.o_scale);

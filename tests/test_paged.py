@@ -91,6 +91,16 @@ def test_decode_long_split(cache):
     run_decode((20011, 3), 4, 1, 128, "bf16", 64, cache)
 
 
+@pytest.mark.parametrize("cache", ["16", "e4m3"])
+@pytest.mark.parametrize("B,n", [(3, 500), (60, 1000), (330, 1500)])
+def test_decode_whole_rows(B, n, cache):
+    # short rows, and more rows than run at once: a CTA for each; some empty
+    lens = [int(x) for x in pu.np_rng(B).integers(0, n, B)]
+    lens[B // 2] = 0
+    H, Hkv = (12, 3) if B < 300 else (3, 3)
+    run_decode(lens, H, Hkv, 128, "bf16", 32, cache, window=0 if B != 60 else 400)
+
+
 def test_decode_wide_table():
     # a table much wider than the lengths: the split follows the lengths
     run_decode((300, 1000), 8, 2, 128, "bf16", 16, width=4096)
