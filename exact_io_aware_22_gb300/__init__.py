@@ -11,6 +11,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -474,16 +475,17 @@ def decode_fp8(q, k_cache8, v_cache8, cache_seqlens, k_scale: float, v_scale: fl
 
 
 # The calls on paged caches are made once per layer and generated token, so what they do on
-# the host counts: each looks at every tensor once and asks torch for the raw stream handle
-# (a Stream object takes longer to make than the rest of the call).
+# the host counts: each looks at every tensor once, asks torch for the raw stream handle and
+# takes workspaces from torch's allocator without making a tensor of them (making a Stream or
+# a tensor between two launches costs 2 and 7 us on the GB300's host).
 def _one_device(*ts) -> int:
     """Index of the one CUDA device of all tensors."""
     dev = ts[0].get_device()
+    if dev < 0 or not ts[0].is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
         if t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
+            raise ValueError("all tensors must be CUDA tensors on one device")
     return dev
 
 
@@ -494,6 +496,29 @@ def _on_device(dev: int, fn, *args) -> int:
         return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
         return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _with_workspace(dev: int, workspace, need: int, fn, head, tail) -> int:
+    """fn(*head, workspace, its bytes, *tail, stream): the caller's workspace, or `need` bytes
+    from torch's allocator, given back once the call has enqueued its work (they are then
+    reused by later work of the same stream only; inside a capture they belong to the graph)."""
+    import torch
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be contiguous, on q's device")
+        return _on_device(dev, fn, *head, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), *tail)
+    if need == 0:
+        return _on_device(dev, fn, *head, None, 0, *tail)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _with_workspace(dev, None, need, fn, head, tail)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+    try:
+        return fn(*head, ws, need, *tail, stream)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
 
 
 def _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B: int, d: int):
@@ -627,6 +652,7 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda")
     return torch.cat([a.cos(), a.sin()], 1).float()
 
 
+@functools.lru_cache(maxsize=None)
 def decode_paged_workspace_size(H: int, Hkv: int, d: int) -> int:
     return int(load_library().fa_decode_paged_workspace_size(H, Hkv, d))
 
@@ -651,21 +677,12 @@ def _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scales, scale,
             or lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 (B, H) on q's device")
     lib = load_library()
-    if workspace is None:
-        # torch's allocator, as for out and lse: capturable, and safe to reuse on this stream
-        workspace = torch.empty(lib.fa_decode_paged_workspace_size(H, Hkv, d), dtype=torch.uint8,
-                                device=q.device)
-        ws_bytes = workspace.numel()
-    else:
-        if not workspace.is_contiguous() or workspace.get_device() != dev:
-            raise ValueError("workspace must be contiguous, on q's device")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    args = (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws_bytes, B, H,
-            Hkv, d, window, 1.0 / math.sqrt(d) if scale is None else scale)
-    if scales:
-        st = _on_device(dev, lib.fa_decode_paged_fp8, *args, *scales, _dtype_code(q))
-    else:
-        st = _on_device(dev, lib.fa_decode_paged, *args, _dtype_code(q))
+    st = _with_workspace(
+        dev, workspace, decode_paged_workspace_size(H, Hkv, d) if workspace is None else 0,
+        lib.fa_decode_paged_fp8 if scales else lib.fa_decode_paged,
+        (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
+        (B, H, Hkv, d, window, 1.0 / math.sqrt(d) if scale is None else scale) + scales
+        + (_dtype_code(q),))
     if st:
         _check(st, "fa_decode_paged_fp8" if scales else "fa_decode_paged")
     return out, lse
@@ -679,7 +696,7 @@ def decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scale: float | 
     of pages with an id outside [0, pages) are not attended; a row without keys gets O = 0,
     L = -inf.  ``workspace``: an optional CUDA tensor of at least
     ``decode_paged_workspace_size(H, Hkv, d)`` bytes; calls that may overlap need one each."""
-    return _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, None, scale, window, out,
+    return _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, (), scale, window, out,
                          lse, workspace)
 
 
@@ -692,6 +709,7 @@ def decode_paged_fp8(q, k_cache8, v_cache8, page_table, cache_seqlens, k_scale: 
                          scale, window, out, lse, workspace)
 
 
+@functools.lru_cache(maxsize=1024)
 def fwd_paged_workspace_size(B: int, total: int, max_seqlen: int, H: int, Hkv: int, d: int) -> int:
     return int(load_library().fa_fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d))
 
@@ -727,21 +745,14 @@ def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_se
     elif lse.shape != (H, total) or lse.dtype != torch.float32 or not lse.is_contiguous() \
             or lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 (H, total) on q's device")
-    lib = load_library()
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.get_device() != dev:
-            raise ValueError("workspace must be contiguous, on q's device")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    else:
-        ws_bytes = lib.fa_fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d)
-        if ws_bytes:                             # torch's allocator, as for out and lse
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            ws = workspace.data_ptr()
-    _check(_on_device(dev, lib.fa_fwd_paged, q.data_ptr(), pc, out.data_ptr(),
-                      lse.data_ptr(), ws, ws_bytes, cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d,
-                      int(causal), window, 1.0 / math.sqrt(d) if scale is None else scale,
-                      _dtype_code(q)), "fa_fwd_paged")
+    need = fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d) if workspace is None else 0
+    st = _with_workspace(
+        dev, workspace, need, load_library().fa_fwd_paged,
+        (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
+        (cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d, int(causal), window,
+         1.0 / math.sqrt(d) if scale is None else scale, _dtype_code(q)))
+    if st:
+        _check(st, "fa_fwd_paged")
     return out, lse
 
 
