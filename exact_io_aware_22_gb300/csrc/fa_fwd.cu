@@ -216,14 +216,38 @@ __device__ __forceinline__ void paged_load(const PagedArgs<true>& px, const CUte
     }
   }
 }
-// Masks the scores of absent keys; mask: the tile's slot of the ring.
-__device__ __forceinline__ void paged_holes(uint32_t mask, uint32_t (&s)[BN]) {
+// Which keys a row of a paged query tile may attend, [lo, lim), and where a KV tile needs
+// masks at all: above `full` for the tile's first row, below `past` for its last.
+struct RowKeys {
+  int lo, lim, past, full;
+};
+__device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row, int pack,
+                                            int window) {
+  RowKeys r;
+  r.lim = min((row >> pack) + k.hi + 1, k.n);
+  r.lo = (row >> pack) + k.off - window + 1;
+  r.full = min((row0 >> pack) + k.hi + 1, k.n);
+  r.past = ((row0 + BM - 1) >> pack) + k.off - window + 1;
+  return r;
+}
+// Masks a row's scores with the keys kbase .. kbase + BN - 1: those outside [lo, lim) and those
+// of absent pages (slot: the tile's mask in the ring).  One block for all of them, entered for
+// few tiles: separate ones cost the unmasked tiles more (1 x 8192, 32 heads, d = 128: 393
+// against 371 us).
+__device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_t slot,
+                                            uint32_t (&s)[BN]) {
   uint32_t w[4];
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(mask)
+               : "r"(slot)
                : "memory");
-  if ((w[0] & w[1] & w[2] & w[3]) == ~0u) return;
+  if (kbase + BN <= r.full && kbase >= r.past && (w[0] & w[1] & w[2] & w[3]) == ~0u) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int hi = r.lim - kbase - 32 * i, lo = r.lo - kbase - 32 * i;   // bits [lo, hi) stay
+    if (hi < 32) w[i] &= hi > 0 ? (1u << hi) - 1u : 0u;
+    if (lo > 0) w[i] &= lo < 32 ? ~0u << lo : 0u;
+  }
 #pragma unroll
   for (int c = 0; c < BN; ++c)
     if (!((w[c / 32] >> (c % 32)) & 1u)) s[c] = __float_as_uint(-INFINITY);
@@ -534,8 +558,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tO = tmem + lane_off + C::O_COL + t * D;
     const int nt = n_t[t] - lo_t[t];             // this tile's KV tiles, from lo_t[t]
     const int tile_row0 = row0 + t * BM;
-    const int qi = grow >> pack;                 // query of the row (paged tiles pack heads)
-    const int lo_key = WINDOW ? qi + kr.off - window + 1 : 0;   // first allowed key
+    const int lo_key = WINDOW ? grow - window + 1 : 0;   // first allowed key
+    const RowKeys rk = row_keys(kr, tile_row0, grow, pack, window);   // paged
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -553,18 +577,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int kbase = (lo_t[t] + j) * BN;
       // masks: causal on the diagonal tile, key padding on the last tile, and with a
       // window the tiles reaching left of some row's first allowed key
-      const bool need_mask =
-          (CAUSAL && kbase + BN - 1 > (tile_row0 >> pack) + kr.hi) || (kbase + BN > Nk) ||
-          (WINDOW && kbase < ((tile_row0 + BM - 1) >> pack) + 1 + kr.off - window);
-      if (need_mask) {
-        const int lim = CAUSAL ? min(qi + kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
+      const bool need_mask = (CAUSAL && kbase + BN - 1 > tile_row0) || (kbase + BN > Nr) ||
+                             (WINDOW && kbase < tile_row0 + BM - window);
+      if (PAGED) {
+        paged_masks(rk, kbase, sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, sr);
+      } else if (need_mask) {
+        const int lim = CAUSAL ? min(grow + 1, Nr) : Nr;   // keys in [lo_key, lim) are allowed
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr[c] = __float_as_uint(-INFINITY);
       }
       if constexpr (PAGED) {
         const int jj = lo_t[t] + j - j0;         // stream position
-        paged_holes(sb + C::MASK_OFF + (jj % kMaskSlots) * 16, sr);
         if (kbase + BN > Nk) {                   // the last tile's V rows past the keys
           if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
           if (kbase + rit >= Nk) clear_row<D>(sb + C::V_OFF + (jj % C::STAGES) * C::TILE_BYTES, rit);
@@ -753,8 +777,9 @@ struct Cfg1 {
   static constexpr int CLC_OFF = (BAR_OFF + NBARS * 8 + 15) / 16 * 16;   // 16-byte response
   static constexpr int SLOT_OFF = CLC_OFF + 16;             // TMEM base, tile slots[2]
   static constexpr int SMEM_BYTES = SLOT_OFF + 16;
-  static constexpr int MASK_OFF = SLOT_OFF + 16;            // paged: key masks
-  static constexpr int PAGED_SMEM_BYTES = MASK_OFF + 8 * 16;
+  static constexpr int MASK_OFF = SLOT_OFF + 16;            // paged: key masks, two Tile1
+  static constexpr int INFO_OFF = MASK_OFF + 8 * 16;
+  static constexpr int PAGED_SMEM_BYTES = INFO_OFF + 2 * 64;
   static constexpr int TMEM_COLS = 256;
   static constexpr uint32_t S_COL = 0, P_COL = 128, O_COL = 192;
   // two CTAs per SM, each with the 1 KiB the system reserves per CTA
@@ -771,6 +796,7 @@ struct Tile1 {
   int split;                                     // paged: its KV range, if it has one of several
   bool shared;
 };
+static_assert(sizeof(Tile1) <= 64, "a slot of the paged kernel's tile ring");
 template <bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
 __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int window,
                                        const int* __restrict__ cu_seqlens, int H, int total,
@@ -877,6 +903,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sg + C1::SLOT_OFF);
   grid_dep_wait();                              // inputs written, outputs free to overwrite
 
+  auto info = [&](int b) -> one::Tile1* {
+    return reinterpret_cast<one::Tile1*>(sg + C1::INFO_OFF + 64 * b);
+  };
   // Consumers read tile k from slot k & 1; the last tile published is -1.
   auto next_tile = [&](int k, bool& ok) -> int {
     if (!(ok = mbar_wait(bar(B_TF(k & 1)), (k >> 1) & 1, ctl))) return -1;
@@ -898,6 +927,13 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       int n_req = 0;                               // requests made
       for (int k = 0; ok; ++k) {
         if (!(ok = wait(bar(B_TE(k & 1)), ((k >> 1) & 1) ^ 1))) break;
+        // paged: the tile's description goes with it, so that its look-ups (lengths, and
+        // divisions) happen once and not in every role
+        one::Tile1 t;
+        if constexpr (PAGED) {
+          if (tile >= 0) t = tile_of(tile);
+          if (lead && tile >= 0) *info(k & 1) = t;
+        }
         if (lead) {
           slot[k & 1] = tile;
           mbar_arrive(bar(B_TF(k & 1)));        // release: the slot write is seen with the phase
@@ -916,7 +952,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
           pending = true;
           ++n_req;
         };
-        const one::Tile1 t = tile_of(tile);
+        if constexpr (!PAGED) t = tile_of(tile);
         if (t.nt <= 0) request();
         if (t.nt > 0) {
           const int qb = kq & 1;
@@ -1017,9 +1053,11 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       for (int k = 0; ok; ++k) {
         const int tile = next_tile(k, ok);
         if (!ok) break;
+        one::Tile1 t;
+        if constexpr (PAGED) t.nt = info(k & 1)->nt;
         mbar_arrive(bar(B_TE(k & 1)));
         if (tile < 0) break;
-        const one::Tile1 t = tile_of(tile);
+        if constexpr (!PAGED) t = tile_of(tile);
         if (t.nt == 0) continue;
         const int qb = kq & 1;
         if (!(ok = mbar_wait(bar(B_QF(qb)), (kq >> 1) & 1, ctl))) break;
@@ -1071,13 +1109,41 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_TE(k & 1)));
+      // paged: the tile's slot is read again by the epilogue and given back after it
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_TE(k & 1)));
+      };
+      if (!PAGED || tile < 0) release();
       if (tile < 0) break;
-      const one::Tile1 t = tile_of(tile);
-      const int Nr = t.nr, Nk = PAGED ? t.kr.n : Nr;   // query rows, keys
+      one::Tile1 t;
+      RowKeys rk;
+      int Nr = 0, Nk = 0, lo_key = 0;            // query rows, keys, first allowed key
+      if constexpr (PAGED) {
+        const one::Tile1* ti = info(k & 1);
+        t.nt = ti->nt;
+        t.lo = ti->lo;
+        t.row0 = ti->row0;
+        KeyRows kr;
+        kr.n = Nk = ti->kr.n;
+        kr.off = ti->kr.off;
+        kr.hi = ti->kr.hi;
+        rk = row_keys(kr, t.row0, t.row0 + rit, pack, window);
+      } else {
+        t = tile_of(tile);
+        Nr = Nk = t.sr.n;
+        lo_key = WINDOW ? t.row0 + rit - window + 1 : 0;
+      }
       const int grow = t.row0 + rit;             // query row
-      const int qi = grow >> pack;               // its query (paged tiles pack heads)
       // paged: where a row lies in O, and in L or its range's part of the workspace
+      auto load_place = [&]() {
+        const one::Tile1* ti = info(k & 1);
+        t.sr.base = ti->sr.base;
+        t.hq = ti->hq;
+        t.split = ti->split;
+        t.shared = ti->shared;
+        Nr = ti->nr;
+      };
       auto row_at = [&](int r) -> size_t {
         return static_cast<size_t>(t.sr.base + (r >> pack)) * H + t.hq + (r & ((1 << pack) - 1));
       };
@@ -1088,14 +1154,17 @@ __global__ void __launch_bounds__(one::THREADS, 2)
                (r >> pack);
       };
       if (t.nt == 0) {
-        if (PAGED && grow < Nr) {                // a row before the first key: O = 0, L = -inf
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(Out) + row_at(grow) * D);
-          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-          *lse_at(grow) = -INFINITY;
+        if constexpr (PAGED) {
+          load_place();
+          if (grow < Nr) {                       // a row before the first key: O = 0, L = -inf
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(Out) + row_at(grow) * D);
+            for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+            *lse_at(grow) = -INFINITY;
+          }
+          release();
         }
         continue;
       }
-      const int lo_key = WINDOW ? qi + t.kr.off - window + 1 : 0;   // first allowed key
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < t.nt; ++j, ++g) {
         if (!(ok = mbar_wait_warp(bar(B_SF), g & 1, ctl))) break;
@@ -1114,17 +1183,17 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         const int kbase = (t.lo + j) * BN;
         // masks: causal on the diagonal tile, key padding on the last tile, and with a
         // window the tiles reaching left of some row's first allowed key
-        const bool need_mask =
-            (CAUSAL && kbase + BN - 1 > (t.row0 >> pack) + t.kr.hi) || (kbase + BN > Nk) ||
-            (WINDOW && kbase < ((t.row0 + BM - 1) >> pack) + 1 + t.kr.off - window);
-        if (need_mask) {
-          const int lim = CAUSAL ? min(qi + t.kr.hi + 1, Nk) : Nk;   // keys in [lo_key, lim) are allowed
+        const bool need_mask = (CAUSAL && kbase + BN - 1 > t.row0) || (kbase + BN > Nr) ||
+                               (WINDOW && kbase < t.row0 + BM - window);
+        if (PAGED) {
+          paged_masks(rk, kbase, sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
+        } else if (need_mask) {
+          const int lim = CAUSAL ? min(grow + 1, Nr) : Nr;   // keys in [lo_key, lim) are allowed
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr_[c] = __float_as_uint(-INFINITY);
         }
         if constexpr (PAGED) {
-          paged_holes(sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
           if (kbase + BN > Nk) {                 // the last tile's V rows past the keys
             const int st = g % STAGES;
             if (!(ok = mbar_wait_warp(bar(B_VF(st)), (g / STAGES) & 1, ctl))) break;
@@ -1198,6 +1267,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (!(ok = mbar_wait_warp(bar(B_OF), kq & 1, ctl))) break;
       ++kq;
       tc_fence_after();
+      if constexpr (PAGED) load_place();
       // a row whose keys are all masked (paged only): l = 0 and acc = 0
       const bool none = PAGED && l_run == 0.f;
       const float inv_l = none ? 0.f : 1.f / l_run;
@@ -1243,7 +1313,10 @@ __global__ void __launch_bounds__(one::THREADS, 2)
                : Lout[t.sr.packed ? static_cast<size_t>(t.hq) * total + t.sr.base + grow
                                   : static_cast<size_t>(t.bh) * N + grow]) =
             none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
-      if (PAGED && t.shared) continue;           // nothing staged
+      if (PAGED && t.shared) {                   // nothing staged
+        release();
+        continue;
+      }
       __syncwarp();
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       constexpr int RPI = 32 / CPR;              // rows per store instruction
@@ -1257,6 +1330,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
           *reinterpret_cast<uint4*>(dst) = stage[r * CPR + (c ^ (r % CPR))];
         }
       }
+      if constexpr (PAGED) release();
       __syncwarp();                              // staging rows free for the next tile
     }
   }
