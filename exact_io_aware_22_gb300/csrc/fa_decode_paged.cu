@@ -181,6 +181,9 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
   using G = Geom<D, C8>;
   constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT, STAGES = stages_of(NT);
   constexpr bool MB = BF16 && !C8;               // operands of the products: bf16 or f16
+  // A state's m is the maximum less SH: p <= 2^(SH + 8) = 2^15 where P is f16, so that the
+  // small p of a long context, which add up, stay clear of f16's subnormals.
+  constexpr float SH = MB ? 0.f : 7.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;         // fragment row, column pair
   extern __shared__ uint8_t smem_raw[];
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
       }
       // Running maximum, moved only when some score of the warp exceeds it by 2^8 (then
       // every lane of a head takes the head's new maximum): numerator and denominator carry
-      // the same m, so a stale one changes nothing, and p <= 2^8.
+      // the same m, so a stale one changes nothing, and p <= 2^(SH + 8).
       bool rise = false;
       float mx[NT][2];
 #pragma unroll
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) v = fmax3(v, s[mt][nt][e], s[mt][nt][2 + e]);
           mx[nt][e] = v * cs[nt][e];
-          rise |= mx[nt][e] > m[nt][e] + 8.0f;
+          rise |= mx[nt][e] > m[nt][e] + (SH + 8.0f);
         }
       if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            const float mn = fmaxf(m[nt][e], v), al = weight(m[nt][e], mn);
+            const float mn = fmaxf(m[nt][e], v - SH), al = weight(m[nt][e], mn);
             m[nt][e] = mn;
             l[nt][e] *= al;
 #pragma unroll

@@ -1108,7 +1108,6 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       int tile = next_tile(k, ok);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      __syncwarp();
       // paged: the tile's slot is read again by the epilogue and given back after it
       auto release = [&]() {
         __syncwarp();

@@ -279,7 +279,7 @@ typedef struct fa_paged_cache {
  *   positions    device int32 [T] to look angles up by, or NULL: key positions.
  *   A token whose angle position lies outside the table, or whose page is absent, is left out
  *   (its query too for the former), and fa_device_status then reports FA_ERR_INVALID_VALUE.
- *   Where two new tokens fall on one cache row, one of them stays.
+ *   Two new tokens must not fall on one cache row: it would hold pieces of both.
  *   Arithmetic in fp32, one rounding.
  *   Errors: as for the cache, FA_ERR_INVALID_VALUE for NULL K or V, one of Q and Qout alone,
  *   B, T or Hkv < 1, H not a multiple of Hkv, T != B without cu_seqlens, strides below a
@@ -387,7 +387,9 @@ fa_status fa_trace_enable(int on);
 
 /* Name of trace kind `kind` (0: forward kernel, 1: backward pre-pass, 2:
  * backward dK/dV kernel, 3: backward dQ kernel, 4: decode split kernel, 5:
- * decode merge kernel, 6: FP8 forward kernel); NULL when out of range. */
+ * decode merge kernel, 6: FP8 forward kernel); NULL when out of range.  The calls on
+ * paged caches count under the kinds of their dense counterparts (0, 4, 5); fa_append_paged's
+ * kernel and the join of fa_fwd_paged's key ranges are not traced. */
 const char* fa_trace_kind_name(int kind);
 
 /* Waits for the recorded events of kind `kind`, then writes the summed GPU

@@ -591,6 +591,79 @@ def test_generation_step_by_step(cache):
             pu.check_rows(o[b:b + 1], lse[b:b + 1], ref, dtype)
 
 
+@pytest.mark.parametrize("cache", ["16", "e4m3"])
+def test_pool_past_32_bit_offsets(cache):
+    """Pages whose elements lie more than 2^32 from the pool's start: appended to, decoded from
+    and attended by many tokens, beside the same work on a small pool."""
+    fa = fa_()
+    Hkv, page, d, H = 2, 64, 128, 8
+    P = (1 << 32) // (Hkv * page * d) + 64
+    t = torch.uint8 if cache == "e4m3" else torch.bfloat16
+    big = [torch.empty(P, Hkv, page, d, dtype=t, device="cuda") for _ in range(2)]
+    small = [torch.zeros(8, Hkv, page, d, dtype=t, device="cuda") for _ in range(2)]
+    far = torch.arange(P - 8, P, dtype=torch.int32, device="cuda").flip(0).view(2, 4)
+    near = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    sl = torch.tensor([250, 100], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 250, 350], dtype=torch.int32, device="cuda")
+    k, v, q = (torch.randn(350, n, d, device="cuda").bfloat16() for n in (Hkv, Hkv, H))
+    cs = fa.rope_table(256, d)
+    got = []
+    for (kc, vc), tb in ((big, far), (small, near)):
+        if cache == "e4m3":
+            qo = fa.append_paged_fp8(k, v, kc, vc, tb, sl, 0.01, 0.01, cu_seqlens=cu, cos_sin=cs, q=q)
+            o = fa.decode_paged_fp8(qo[[249, 349]], kc, vc, tb, sl, 0.01, 0.01)
+        else:
+            qo = fa.append_paged(k, v, kc, vc, tb, sl, cu_seqlens=cu, cos_sin=cs, q=q)
+            o = fa.decode_paged(qo[[249, 349]], kc, vc, tb, sl)
+            o += fa.fwd_paged(qo, kc, vc, tb, sl, cu, 250)
+        got.append((qo,) + o)
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert got[0][1].isfinite().all()
+
+
+def test_tables_and_lengths_seen_through_strides():
+    # a table that is a slice of a wider one
+    fa = fa_()
+    pool = pu.Pool((300, 120, 33), 2, 64, 16, "fp16")
+    kc, vc, tb, sl = pool.cuda()
+    wide = torch.full((3, tb.shape[1] + 9), -5, dtype=torch.int32, device="cuda")
+    wide[:, 4:4 + tb.shape[1]] = tb
+    q = torch.randn(3, 8, 64, device="cuda").half()
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    a, b = (fa.decode_paged(q, kc, vc, x, sl) + fa.fwd_paged(q, kc, vc, x, sl, cu, 1)
+            for x in (tb, wide[:, 4:4 + tb.shape[1]]))
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_decode_many_small_weights_add_up():
+    """One key far above 100000 others whose weights are about 2^-26 each: together 0.2 % of the
+    sum, which f16 weights of at most 1 would lose."""
+    fa = fa_()
+    for cache in ("16", "e4m3"):
+        n, d = 100000, 128
+        pages = -(-n // 64)
+        t = torch.float16
+        kc = torch.zeros(pages, 1, 64, d, dtype=t, device="cuda")
+        vc = torch.zeros(pages, 1, 64, d, dtype=t, device="cuda")
+        kc[0, 0, 0] = 1.0
+        vc[1:] = 1.0
+        q = torch.full((1, 1, d), 18.0 / d, dtype=t, device="cuda")
+        tb = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+        sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+        if cache == "e4m3":
+            kc, vc = (x.to(torch.float8_e4m3fn) for x in (kc, vc))
+            o, _ = fa.decode_paged_fp8(q, kc, vc, tb, sl, 1.0, 1.0, scale=1.0)
+        else:
+            o, _ = fa.decode_paged(q, kc, vc, tb, sl, scale=1.0)
+        ok()
+        s = float(q.double().sum())
+        want = (n - 64) / (math.exp(s) + n - 1)
+        # the output's rounding, and each weight's: 2^-26 2^7 is f16's 2^-19, a multiple of 2^-24
+        assert abs(float(o[0, 0, 0]) / want - 1) <= 2.0 ** -11 + 2.0 ** -10
+
+
 def test_calls_on_two_streams():
     fa = fa_()
     pool = pu.Pool((3000, 2000), 2, 128, 64, "bf16")
