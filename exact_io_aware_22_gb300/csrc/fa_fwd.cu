@@ -23,20 +23,6 @@
 // more than RESCALE_LOG2 (log2 units), so the O rescale (TMEM load-multiply-
 // store) is skipped on almost every tile.  The result is still exact algebra:
 // numerator and denominator carry the same stale m, and every p <= 2^8.
-//
-// PAGED instances (fa_fwd_paged) take packed queries and the keys of a paged cache: the
-// queries of a sequence are its last positions, so a query row sees keys up to its own
-// index plus (keys - queries).  Their producer is a whole warp: each lane looks up the pages
-// of its boxes (the largest power of two of rows that divides the page size) one tile
-// ahead and loads them; a 128-row tile is laid out in shared memory as one box would be.
-// Boxes of absent pages read as zeros and their keys are masked; V rows past the last key,
-// which may hold anything, are cleared before the product that reads them (0 x NaN).
-// A query tile of a paged instance holds the rows of 2^pack heads that share a K/V head, heads
-// fastest: the tile of a few new tokens is better filled, K and V pass once for those heads,
-// and less of a tile lies beyond the diagonal.  Where there are fewer query tiles than the
-// GPU runs at once, the KV tiles of each are cut into up to n_split ranges of equal length
-// for as many CTAs, whose results, each normalised with its own L, fwd_paged_merge_kernel
-// joins by their weights 2^(L_s - L).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -67,8 +53,6 @@ struct Cfg {
   static constexpr int NBARS = 1 + 4 * STAGES + 7;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SMEM_BYTES = SLOT_OFF + 16 + 1024;   // + alignment slack
-  static constexpr int MASK_OFF = (SLOT_OFF + 16 + 15) / 16 * 16;   // paged: key masks
-  static constexpr int PAGED_SMEM_BYTES = MASK_OFF + 8 * 16 + 1024;
   static constexpr int TMEM_COLS = 512;
   static constexpr int S_COL = 0;                           // S_t at t * 128
   static constexpr int O_COL = 256;                         // O_t at 256 + t * D
@@ -82,197 +66,13 @@ __device__ __forceinline__ uint32_t kmajor_koff(int kk) {
   return (e / C::ATOM) * C::CHUNK_BYTES + (e % C::ATOM) * 2;
 }
 
-// What a PAGED kernel gets besides the packed ones' arguments (nothing in the others).
-template <bool PAGED>
-struct PagedArgs {};
-template <>
-struct PagedArgs<true> {
-  PagedView pg;
-  int box_log2, causal;
-  int pack;                        // log2 of the heads in a query tile
-  int n_split;                     // KV ranges per query tile (1: no workspace)
-  float* part;                     // [n_split][total * H][D] results of the ranges
-  float* part_l;                   // [n_split][total * H] their logsumexp (natural log)
-};
-// Keys of a sequence with nq query rows: query row i is at key position i + off and sees keys
-// up to i + hi (all of them unless causal) and from i + off - window + 1.
-struct KeyRows {
-  int n, off, hi;
-};
-constexpr int kNoLimit = 1 << 30;
-// Query and key rows of sequence b; paged: the three loads go out together.
-template <bool PACKED>
-__device__ __forceinline__ void rows_of(const PagedArgs<true>& px, const int* cu, int b, int N,
-                                        int total, SeqRows& sr, KeyRows& k) {
-  static_assert(PACKED, "paged queries are packed");
-  const int c0 = cu[b], c1 = cu[b + 1], len = px.pg.seqlens[b];
-  const int a = min(max(c0, 0), total), e = min(max(c1, a), total);
-  sr = {a, min(e - a, N), true};
-  const long long cap = static_cast<long long>(px.pg.max_pages) * px.pg.page.div;
-  k.n = static_cast<int>(min(static_cast<long long>(max(len, 0)), cap));
-  k.off = k.n - sr.n;
-  k.hi = px.causal ? k.off : kNoLimit;
-}
-template <bool PACKED>
-__device__ __forceinline__ void rows_of(const PagedArgs<false>&, const int* __restrict__ cu, int b,
-                                        int N, int total, SeqRows& sr, KeyRows& k) {
-  sr = seq_rows_t<PACKED>(cu, b, N, total);
-  k = {sr.n, 0, 0};
-}
-// KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of a sequence's nr; row i is
-// a head of query i >> pack.
-__device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nr, int window, int pack,
-                                            int& lo, int& hi) {
-  const int last = (min(r + BM - 1, nr - 1) >> pack) + k.hi;
-  hi = r >= nr || last < 0 ? 0 : min((k.n + BN - 1) / BN, last / BN + 1);
-  lo = min(max(0, (r >> pack) + k.off - window + 1) / BN, hi);
-}
-// How the KV tiles [lo, hi) of `TILES` query tiles from row r are cut: ranges of `per` tiles,
-// `used` of them (at least one).
-struct SplitRange {
-  int lo, hi, per, used;
-};
-template <int TILES>
-__device__ __forceinline__ SplitRange split_range(const KeyRows& k, int r, int nr, int window,
-                                                  int pack, int n_split) {
-  SplitRange s;
-  paged_tiles(k, r, nr, window, pack, s.lo, s.hi);
-#pragma unroll
-  for (int t = 1; t < TILES; ++t) {
-    int lo, hi;
-    paged_tiles(k, r + t * BM, nr, window, pack, lo, hi);
-    if (hi > s.hi) s.hi = hi;                    // lo rises with the row
-  }
-  // two tiles at least: the join costs about as much as one
-  s.per = max((s.hi - s.lo + n_split - 1) / n_split, n_split > 1 ? 2 : 1);
-  s.used = max((s.hi - s.lo + s.per - 1) / s.per, 1);
-  return s;
-}
-
-// One warp's loads of 128-key tiles of a paged cache.  Lane i handles boxes i, i + 32, ...
-struct PagedTile {
-  int id[4], row[4];               // page id as the table has it, and first row in the page
-  int past;                        // bit i: box lane + 32 i lies past the keys
-};
-constexpr int kMaskSlots = 8;
-// Starts the tile's table loads.  Nothing here uses what they return: the warp would stand
-// still for a load's latency instead of issuing the tile before this one.
-__device__ __forceinline__ void paged_fetch(const PagedArgs<true>& px, int b, const KeyRows& k,
-                                            int krow, int lane, PagedTile& t) {
-  const int n_box = BN >> px.box_log2;
-  t.past = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int bx = lane + 32 * i, key = krow + (bx << px.box_log2);
-    t.id[i] = -1;
-    t.row[i] = 0;
-    if (bx < n_box && key < k.n) {
-      const int p = static_cast<int>(px.pg.page.quot(key));
-      t.row[i] = key - p * static_cast<int>(px.pg.page.div);
-      t.id[i] = px.pg.table[b * px.pg.table_stride + p];
-    } else {
-      t.past |= 1 << i;
-    }
-  }
-}
-__device__ __forceinline__ bool paged_in_pool(const PagedArgs<true>& px, int id) {
-  return id >= 0 && id < px.pg.pages;
-}
-// Keys of the tile that exist, as 128 bits, to the ring slot at `slot` (all lanes call).
-__device__ __forceinline__ void paged_mask(const PagedArgs<true>& px, int lane, const PagedTile& t,
-                                           uint32_t slot) {
-  uint32_t have = t.past;                        // keys past the end are masked by their index
-#pragma unroll
-  for (int i = 0; i < 4; ++i) have |= (paged_in_pool(px, t.id[i]) ? 1u : 0u) << i;
-  uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-  if (__any_sync(0xffffffffu, have != 15u)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int bx = (32 * i + lane) >> px.box_log2;      // the box of key 32 i + lane
-      const uint32_t h = __shfl_sync(0xffffffffu, have, bx & 31);
-      w[i] = __ballot_sync(0xffffffffu, (h >> (bx >> 5)) & 1u);
-    }
-  }
-  if (lane == 0)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot),
-                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                 : "memory");
-}
-template <int D>
-__device__ __forceinline__ void paged_load(const PagedArgs<true>& px, const CUtensorMap* map,
-                                           uint32_t dst, uint32_t bar, int hk, int lane,
-                                           const PagedTile& t) {
-  using C = Cfg<D>;
-  const int n_box = BN >> px.box_log2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int bx = lane + 32 * i;
-    if (bx < n_box) {
-      const int w = paged_in_pool(px, t.id[i]) ? t.id[i] : px.pg.pages;   // past the pool: zeros
-#pragma unroll
-      for (int c = 0; c < C::NCHUNK; ++c)
-        tma_load_4d(dst + c * C::CHUNK_BYTES + (bx << px.box_log2) * C::SW, map, bar, c * C::ATOM,
-                    t.row[i], hk, w);
-    }
-  }
-}
-// Which keys a row of a paged query tile may attend, [lo, lim), and where a KV tile needs
-// masks at all: above `full` for the tile's first row, below `past` for its last.
-struct RowKeys {
-  int lo, lim, past, full;
-};
-__device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row, int pack,
-                                            int window) {
-  RowKeys r;
-  r.lim = min((row >> pack) + k.hi + 1, k.n);
-  r.lo = (row >> pack) + k.off - window + 1;
-  r.full = min((row0 >> pack) + k.hi + 1, k.n);
-  r.past = ((row0 + BM - 1) >> pack) + k.off - window + 1;
-  return r;
-}
-// Masks a row's scores with the keys kbase .. kbase + BN - 1: those outside [lo, lim) and those
-// of absent pages (slot: the tile's mask in the ring).  One block for all of them, entered for
-// few tiles: separate ones cost the unmasked tiles more (1 x 8192, 32 heads, d = 128: 393
-// against 371 us).
-__device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_t slot,
-                                            uint32_t (&s)[BN]) {
-  uint32_t w[4];
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(slot)
-               : "memory");
-  if (kbase + BN <= r.full && kbase >= r.past && (w[0] & w[1] & w[2] & w[3]) == ~0u) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int hi = r.lim - kbase - 32 * i, lo = r.lo - kbase - 32 * i;   // bits [lo, hi) stay
-    if (hi < 32) w[i] &= hi > 0 ? (1u << hi) - 1u : 0u;
-    if (lo > 0) w[i] &= lo < 32 ? ~0u << lo : 0u;
-  }
-#pragma unroll
-  for (int c = 0; c < BN; ++c)
-    if (!((w[c / 32] >> (c % 32)) & 1u)) s[c] = __float_as_uint(-INFINITY);
-}
-// Clears row r of a V tile (all its columns, so the swizzle does not matter).
-template <int D>
-__device__ __forceinline__ void clear_row(uint32_t tile, int r) {
-  using C = Cfg<D>;
-#pragma unroll
-  for (int c = 0; c < C::NCHUNK; ++c)
-#pragma unroll
-    for (int i = 0; i < C::SW / 16; ++i)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                       tile + c * C::CHUNK_BYTES + r * C::SW + 16 * i),
-                   "r"(0u)
-                   : "memory");
-}
-
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
 __global__ void __launch_bounds__(THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, void* __restrict__ Out,
                float* __restrict__ Lout, int N, int n_qblk, int group, int window,
                const int* __restrict__ cu_seqlens, int H, int total, float c_log2,
-               KernelCtl ctl, const PagedArgs<PAGED> px) {
+               KernelCtl ctl) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -283,29 +83,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (PACKED) grid_dep_wait();        // the offsets may come from earlier work
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const BlockPos bp = block_pos(n_qblk);
-  // paged: bp.bh counts (sequence, block of packed heads, KV range)
-  int bh = bp.bh, split = 0, pack = 0;
-  if constexpr (PAGED) {
-    split = bp.bh % px.n_split;
-    bh = bp.bh / px.n_split;                    // sequence, block of heads
-    pack = px.pack;
-    H >>= pack;                                 // blocks of heads per sequence
-  }
+  const int bh = bp.bh;
   const int qblk = n_qblk - 1 - bp.rank;        // causal: the last query tiles have the most work
   const int bkv = bh / group;                   // the K/V head of this query head (b-major heads)
   // Rows of this (batch, head): dense (B, H, N, d) maps are (d, N, B*H), a row at
   // (row, flat head); packed sequences (total, H, d) have maps (d, H, total), a row at
   // (head within the batch, first token + row), and their own length Nr.
-  SeqRows sr;
-  KeyRows kr;
-  rows_of<PACKED>(px, cu_seqlens, bh / H, N, total, sr, kr);
-  const int Nr = sr.n << pack;
-  // paged: hq is the first of the tile's heads
-  const int hq = sr.packed ? (bh % H) << pack : bh, hk = sr.packed ? hq / group : bkv;
+  const SeqRows sr = seq_rows_t<PACKED>(cu_seqlens, bh / H, N, total);
+  const int Nr = sr.n;
+  const int hq = sr.packed ? bh % H : bh, hk = sr.packed ? (bh % H) / group : bkv;
   auto cy = [&](int r, int head) { return sr.y(r, head); };
   auto cz = [&](int r, int head) { return sr.z(r, head); };
   const int row0 = qblk * (NT * BM);
-  const int Nk = PAGED ? kr.n : Nr;             // keys
   const int nkv = (Nr + BN - 1) / BN;
   // KV tiles [lo_t[t], n_t[t]) of Q tile t: up to the diagonal when causal; with a
   // sliding window of W keys, from the tile holding key (first row - W + 1)
@@ -314,53 +103,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int t = 0; t < NT; ++t) {
     const int r = row0 + t * BM;
     if (r >= Nr) n_t[t] = 0;
-    else if (PAGED) {
-      paged_tiles(kr, r, Nr, window, pack, lo_t[t], n_t[t]);
-      continue;
-    } else if (CAUSAL) n_t[t] = min(nkv, min(r + BM - 1, Nr - 1) / BN + 1);
+    else if (CAUSAL) n_t[t] = min(nkv, min(r + BM - 1, Nr - 1) / BN + 1);
     else n_t[t] = nkv;
     lo_t[t] = WINDOW ? max(0, r - window + 1) / BN : 0;
   }
-  int j0 = lo_t[0];                             // the stream starts at tile 0's first KV tile
-  int n_max = max(n_t[0], n_t[1]);
-  bool shared = false;                          // this CTA has one of several KV ranges
-  if constexpr (PAGED) {
-    const SplitRange sp = split_range<NT>(kr, row0, Nr, window, pack, px.n_split);
-    if (split >= sp.used) return;
-    shared = sp.used > 1;
-    j0 = sp.lo + split * sp.per;
-    n_max = min(j0 + sp.per, sp.hi);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      lo_t[t] = min(max(lo_t[t], j0), n_max);
-      n_t[t] = min(max(n_t[t], j0), n_max);
-    }
-  }
+  const int j0 = lo_t[0];                       // the stream starts at tile 0's first KV tile
+  const int n_max = max(n_t[0], n_t[1]);
   const int n_stream = n_max - j0;              // KV tiles loaded, j0 .. n_max - 1
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  // paged: where row `grow` lies in O and in L, or in its range's part of the workspace
-  auto row_at = [&](int grow) -> size_t {
-    return static_cast<size_t>(sr.base + (grow >> pack)) * (H << pack) + hq + (grow & ((1 << pack) - 1));
-  };
-  auto lse_at = [&](int grow) -> float* {
-    if constexpr (PAGED)
-      if (shared) return px.part_l + static_cast<size_t>(split) * total * (H << pack) + row_at(grow);
-    return Lout + static_cast<size_t>(hq + (grow & ((1 << pack) - 1))) * total + sr.base +
-           (grow >> pack);
-  };
-  // row `grow` sees no key here: O = 0, L = -inf (a range's O is not read where its L is -inf)
-  auto empty_row = [&](int grow) {
-    if (!shared) {
-      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at(grow) * D);
-      for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    *lse_at(grow) = -INFINITY;
-  };
-  if (n_stream <= 0) {                          // query tiles past the end of a packed sequence
-    if constexpr (PAGED)                        // or before the first key
-      for (int r = row0 + threadIdx.x; r < min(row0 + NT * BM, Nr); r += THREADS) empty_row(r);
-    return;
-  }
+  if (n_stream <= 0) return;                    // query tiles past the end of a packed sequence
 
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8 * i; };
   const int B_QF = 0;
@@ -373,9 +123,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto B_OF = [&](int t) { return 5 + 4 * C::STAGES + t; };
   const int B_DONE = 7 + 4 * C::STAGES;
 
-  PagedTile first_tile;
-  if constexpr (PAGED)                          // its latency passes under the set-up
-    if (warp == 0) paged_fetch(px, bh / H, kr, j0 * BN, lane, first_tile);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBARS; ++i) mbar_init(bar(i), 1);
     for (int t = 0; t < NT; ++t) mbar_init(bar(B_PF(t)), 128);
@@ -399,44 +146,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     regs_dec<kRegsLow>();                          // warpgroup 0 (TMA, MMA issue): few registers
     // ------------------------------------------------------------ producer
-    if constexpr (PAGED) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(B_QF), NT * C::TILE_BYTES);
-        for (int t = 0; t < NT; ++t)
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_3d(sb + C::Q_OFF + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ, bar(B_QF),
-                        c * C::ATOM, hq, sr.base + ((row0 + t * BM) >> pack));
-      }
-      bool ok = true;
-      PagedTile next = first_tile;
-      int j = 0;
-      for (; j < n_stream; ++j) {
-        const int s = j % C::STAGES;
-        const uint32_t ph = (j / C::STAGES) & 1;
-        const PagedTile cur = next;
-        if (j + 1 < n_stream) paged_fetch(px, bh / H, kr, (j0 + j + 1) * BN, lane, next);
-        if (!(ok = mbar_wait_warp(bar(B_KE(s)), ph ^ 1, ctl))) break;
-        // the slot's last readers were the softmax threads of tile j - 8: they are done,
-        // since S(j - 2), whose K tile has just been released, waited for their P
-        paged_mask(px, lane, cur, sb + C::MASK_OFF + (j % kMaskSlots) * 16);
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_KF(s)), C::TILE_BYTES);
-        __syncwarp();
-        paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), hk, lane, cur);
-        if (!(ok = mbar_wait_warp(bar(B_VE(s)), ph ^ 1, ctl))) { ++j; break; }
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_VF(s)), C::TILE_BYTES);
-        __syncwarp();
-        paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), hk, lane, cur);
-      }
-      if (!ok) {                                // as below: wait for the copies in flight
-        mbar_wait_warp(bar(B_QF), 0, ctl);
-        for (int jj = max(0, j - C::STAGES); jj < j; ++jj) {
-          const int s = jj % C::STAGES;
-          const uint32_t ph = (jj / C::STAGES) & 1;
-          mbar_wait_warp(bar(B_KF(s)), ph, ctl);
-          mbar_wait_warp(bar(B_VF(s)), ph, ctl);
-        }
-      }
-    } else if (lane == 0 && n_stream > 0) {
+    if (lane == 0 && n_stream > 0) {
       bool ok = true;
       mbar_arrive_expect_tx(bar(B_QF), NT * C::TILE_BYTES);
       for (int t = 0; t < NT; ++t)
@@ -559,7 +269,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int nt = n_t[t] - lo_t[t];             // this tile's KV tiles, from lo_t[t]
     const int tile_row0 = row0 + t * BM;
     const int lo_key = WINDOW ? grow - window + 1 : 0;   // first allowed key
-    const RowKeys rk = row_keys(kr, tile_row0, grow, pack, window);   // paged
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -579,21 +288,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       // window the tiles reaching left of some row's first allowed key
       const bool need_mask = (CAUSAL && kbase + BN - 1 > tile_row0) || (kbase + BN > Nr) ||
                              (WINDOW && kbase < tile_row0 + BM - window);
-      if (PAGED) {
-        paged_masks(rk, kbase, sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, sr);
-      } else if (need_mask) {
+      if (need_mask) {
         const int lim = CAUSAL ? min(grow + 1, Nr) : Nr;   // keys in [lo_key, lim) are allowed
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr[c] = __float_as_uint(-INFINITY);
-      }
-      if constexpr (PAGED) {
-        const int jj = lo_t[t] + j - j0;         // stream position
-        if (kbase + BN > Nk) {                   // the last tile's V rows past the keys
-          if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
-          if (kbase + rit >= Nk) clear_row<D>(sb + C::V_OFF + (jj % C::STAGES) * C::TILE_BYTES, rit);
-          fence_proxy_async_smem();              // before this thread's arrival on p_full
-        }
       }
       // row maximum: four independent chains of 3-input max
       const float mx = row_max128(sr);
@@ -644,30 +343,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (ok && nt > 0 && mbar_wait_warp(bar(B_OF(t)), 0, ctl)) {
       tc_fence_after();
-      // a row whose keys are all masked (paged only): l = 0 and acc = 0
-      const bool none = PAGED && l_run == 0.f;
-      const float inv_l = none ? 0.f : 1.f / l_run;
+      const float inv_l = 1.f / l_run;
       const bool valid = grow < Nr;
-      T* orow = reinterpret_cast<T*>(Out) + (PAGED ? row_at(grow) * D : sr.off(grow, hq, H, N, D));
+      using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+      T* orow = reinterpret_cast<T*>(Out) + sr.off(grow, hq, H, N, D);
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * cc, o);
         tmem_ld_wait_regs(o);
-        if constexpr (PAGED) {
-          if (shared) {
-            if (valid) {
-              float4* dst = reinterpret_cast<float4*>(
-                  px.part + (static_cast<size_t>(split) * total * (H << pack) + row_at(grow)) * D + 32 * cc);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(
-                    __uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
-                    __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
-            }
-            continue;
-          }
-        }
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -681,12 +365,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (valid)
-        (PAGED ? *lse_at(grow)
-               : Lout[sr.packed ? static_cast<size_t>(hq) * total + sr.base + grow
-                                : static_cast<size_t>(bh) * N + grow]) =
-            none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
-    } else if (PAGED && nt <= 0 && grow < Nr) {
-      empty_row(grow);
+        Lout[sr.packed ? static_cast<size_t>(hq) * total + sr.base + grow
+                       : static_cast<size_t>(bh) * N + grow] =
+            (m_run + log2f(l_run)) * 0.69314718055994531f;
     }
   } else {
     regs_dec<kRegsLow>();                          // warps 2 and 3: idle
@@ -700,37 +381,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <bool PAGED>
-PagedArgs<PAGED> paged_args(const FwdArgs& a) {
-  PagedArgs<PAGED> px;
-  if constexpr (PAGED) {
-    px.pg = a.pg;
-    px.box_log2 = a.box_log2;
-    px.causal = a.causal;
-    px.pack = a.pack;
-    px.n_split = a.n_split;
-    px.part = a.part;
-    px.part_l = a.part_l;
-  }
-  return px;
-}
-
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED = false>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
 cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
-  constexpr int smem = PAGED ? C::PAGED_SMEM_BYTES : C::SMEM_BYTES;
-  auto kern = fwd_kernel<D, BF16, CAUSAL, WINDOW, PACKED, PAGED>;
+  auto kern = fwd_kernel<D, BF16, CAUSAL, WINDOW, PACKED>;
   cudaError_t e = check_split_regs(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
-  e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
+  e = ensure_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int n_qblk = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + NT * BM - 1) / (NT * BM));
+  const int n_qblk = (a.N + NT * BM - 1) / (NT * BM);
   const long long grid = static_cast<long long>(n_qblk) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
-  e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, smem, st, a.tmQ,
+  e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, C::SMEM_BYTES, st, a.tmQ,
                        a.tmK, a.tmV, a.O, a.L, a.N, n_qblk, a.group, a.window, a.cu_seqlens, a.H,
-                       a.total, a.c_log2, a.ctl, paged_args<PAGED>(a));
+                       a.total, a.c_log2, a.ctl);
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -777,13 +442,10 @@ struct Cfg1 {
   static constexpr int CLC_OFF = (BAR_OFF + NBARS * 8 + 15) / 16 * 16;   // 16-byte response
   static constexpr int SLOT_OFF = CLC_OFF + 16;             // TMEM base, tile slots[2]
   static constexpr int SMEM_BYTES = SLOT_OFF + 16;
-  static constexpr int MASK_OFF = SLOT_OFF + 16;            // paged: key masks, two Tile1
-  static constexpr int INFO_OFF = MASK_OFF + 8 * 16;
-  static constexpr int PAGED_SMEM_BYTES = INFO_OFF + 2 * 64;
   static constexpr int TMEM_COLS = 256;
   static constexpr uint32_t S_COL = 0, P_COL = 128, O_COL = 192;
   // two CTAs per SM, each with the 1 KiB the system reserves per CTA
-  static_assert(2 * (PAGED_SMEM_BYTES + 1024) <= 233472, "two CTAs per SM must fit");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM must fit");
   static_assert(O_COL + D <= TMEM_COLS, "TMEM layout");
 };
 
@@ -791,44 +453,19 @@ struct Cfg1 {
 struct Tile1 {
   int bh, hq, hk, row0, lo, nt;
   SeqRows sr;
-  KeyRows kr;
-  int nr;                                        // rows of the sequence (queries x packed heads)
-  int split;                                     // paged: its KV range, if it has one of several
-  bool shared;
 };
-static_assert(sizeof(Tile1) <= 64, "a slot of the paged kernel's tile ring");
-template <bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
+template <bool CAUSAL, bool WINDOW, bool PACKED>
 __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int window,
-                                       const int* __restrict__ cu_seqlens, int H, int total,
-                                       const PagedArgs<PAGED>& px) {
+                                       const int* __restrict__ cu_seqlens, int H, int total) {
   Tile1 t;
   const BlockPos bp = block_pos(n_qt, id);
   t.bh = bp.bh;
-  t.split = 0;
-  t.shared = false;
   const int qt = n_qt - 1 - bp.rank;            // causal: the last query tiles have the most work
-  t.row0 = qt * BM;
-  if constexpr (PAGED) {                         // bp.bh: sequence, block of heads, KV range
-    const int hb = H >> px.pack;
-    t.split = bp.bh % px.n_split;
-    t.bh = bp.bh / px.n_split;
-    const int b = t.bh / hb;
-    rows_of<PACKED>(px, cu_seqlens, b, N, total, t.sr, t.kr);
-    t.nr = t.sr.n << px.pack;
-    t.hq = (t.bh % hb) << px.pack;               // the first of the tile's heads
-    t.hk = t.hq / group;
-    t.bh = b * H + t.hq;
-    const SplitRange sp = split_range<1>(t.kr, t.row0, t.nr, window, px.pack, px.n_split);
-    t.shared = sp.used > 1;
-    t.lo = sp.lo + t.split * sp.per;
-    t.nt = max(min(sp.per, sp.hi - t.lo), 0);
-    if (t.split >= sp.used) t.nr = t.nt = 0;     // nothing to do or to write
-    return t;
-  }
-  rows_of<PACKED>(px, cu_seqlens, t.bh / H, N, total, t.sr, t.kr);
-  const int Nr = t.nr = t.sr.n;
+  t.sr = seq_rows_t<PACKED>(cu_seqlens, t.bh / H, N, total);
+  const int Nr = t.sr.n;
   t.hq = t.sr.packed ? t.bh % H : t.bh;
   t.hk = t.sr.packed ? (t.bh % H) / group : t.bh / group;
+  t.row0 = qt * BM;
   // up to the diagonal when causal; with a sliding window of W keys, from the tile
   // holding key (first row - W + 1); none for a tile past the end of a packed sequence
   const int nkv = (Nr + BN - 1) / BN;
@@ -839,13 +476,13 @@ __device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, int w
 }
 }  // namespace one
 
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
 __global__ void __launch_bounds__(one::THREADS, 2)
     fwd1_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, void* __restrict__ Out,
                 float* __restrict__ Lout, int N, int n_qt, int group, int window,
                 const int* __restrict__ cu_seqlens, int H, int total, float c_log2,
-                KernelCtl ctl, const PagedArgs<PAGED> px) {
+                KernelCtl ctl) {
   using C = Cfg<D>;
   using C1 = one::Cfg1<D>;
   constexpr int STAGES = C1::STAGES;
@@ -858,11 +495,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int pack = 0;
-  if constexpr (PAGED) pack = px.pack;
   auto tile_of = [&](int id) {
-    return one::tile1<CAUSAL, WINDOW, PACKED, PAGED>(id, n_qt, N, group, window, cu_seqlens, H,
-                                                     total, px);
+    return one::tile1<CAUSAL, WINDOW, PACKED>(id, n_qt, N, group, window, cu_seqlens, H, total);
   };
 
   auto bar = [&](int i) -> uint32_t { return sb + C1::BAR_OFF + 8 * i; };
@@ -903,9 +537,6 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sg + C1::SLOT_OFF);
   grid_dep_wait();                              // inputs written, outputs free to overwrite
 
-  auto info = [&](int b) -> one::Tile1* {
-    return reinterpret_cast<one::Tile1*>(sg + C1::INFO_OFF + 64 * b);
-  };
   // Consumers read tile k from slot k & 1; the last tile published is -1.
   auto next_tile = [&](int k, bool& ok) -> int {
     if (!(ok = mbar_wait(bar(B_TF(k & 1)), (k >> 1) & 1, ctl))) return -1;
@@ -914,30 +545,16 @@ __global__ void __launch_bounds__(one::THREADS, 2)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer, scheduler
-    // one thread; for paged keys the whole warp, whose first lane does what is done once
-    if (PAGED || lane == 0) {
-      const bool lead = !PAGED || lane == 0;
-      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-        return PAGED ? mbar_wait_warp(b, parity, ctl) : mbar_wait(b, parity, ctl);
-      };
+    if (lane == 0) {
       bool ok = true;
       int tile = static_cast<int>(blockIdx.x);
       int g = 0, kq = 0, nk = 0, nv = 0;         // steps, Q tiles, K and V tiles loaded
       bool pending = false;                       // a request for the next tile is out
       int n_req = 0;                               // requests made
       for (int k = 0; ok; ++k) {
-        if (!(ok = wait(bar(B_TE(k & 1)), ((k >> 1) & 1) ^ 1))) break;
-        // paged: the tile's description goes with it, so that its look-ups (lengths, and
-        // divisions) happen once and not in every role
-        one::Tile1 t;
-        if constexpr (PAGED) {
-          if (tile >= 0) t = tile_of(tile);
-          if (lead && tile >= 0) *info(k & 1) = t;
-        }
-        if (lead) {
-          slot[k & 1] = tile;
-          mbar_arrive(bar(B_TF(k & 1)));        // release: the slot write is seen with the phase
-        }
+        if (!(ok = mbar_wait(bar(B_TE(k & 1)), ((k >> 1) & 1) ^ 1, ctl))) break;
+        slot[k & 1] = tile;
+        mbar_arrive(bar(B_TF(k & 1)));          // release: the slot write is seen with the phase
         if (tile < 0) break;
         // ask for the next tile together with this tile's last loads: early enough that
         // the answer is there when they complete, late enough that a CTA takes a tile
@@ -945,81 +562,55 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         // CTAs that still had most of a long tile ahead, and took tiles from CTAs that had
         // not started yet when all would have fit at once)
         auto request = [&]() {
-          if (lead) {
-            mbar_arrive_expect_tx(bar(B_CLC), 16);
-            clc_try_cancel(clc_resp, bar(B_CLC));
-          }
+          mbar_arrive_expect_tx(bar(B_CLC), 16);
+          clc_try_cancel(clc_resp, bar(B_CLC));
           pending = true;
           ++n_req;
         };
-        if constexpr (!PAGED) t = tile_of(tile);
+        const one::Tile1 t = tile_of(tile);
         if (t.nt <= 0) request();
         if (t.nt > 0) {
           const int qb = kq & 1;
-          if (!(ok = wait(bar(B_QE(qb)), ((kq >> 1) & 1) ^ 1))) break;
-          if (lead) {
-            mbar_arrive_expect_tx(bar(B_QF(qb)), C1::TILE_BYTES);
-            for (int c = 0; c < C::NCHUNK; ++c)
-              tma_load_3d(sb + C1::Q_OFF + qb * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ,
-                          bar(B_QF(qb)), c * C::ATOM, t.sr.y(t.row0, t.hq),
-                          PAGED ? t.sr.base + (t.row0 >> pack) : t.sr.z(t.row0, t.hq));
-          }
+          if (!(ok = mbar_wait(bar(B_QE(qb)), ((kq >> 1) & 1) ^ 1, ctl))) break;
+          mbar_arrive_expect_tx(bar(B_QF(qb)), C1::TILE_BYTES);
+          for (int c = 0; c < C::NCHUNK; ++c)
+            tma_load_3d(sb + C1::Q_OFF + qb * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ,
+                        bar(B_QF(qb)), c * C::ATOM, t.sr.y(t.row0, t.hq), t.sr.z(t.row0, t.hq));
           ++kq;
-          PagedTile next;
-          if constexpr (PAGED) paged_fetch(px, t.bh / H, t.kr, t.lo * BN, lane, next);
           for (int j = 0; j < t.nt; ++j, ++g) {
             const int st = g % STAGES;
             const uint32_t ph = (g / STAGES) & 1;
             const int krow = (t.lo + j) * BN;
-            const PagedTile cur = next;
-            if constexpr (PAGED)
-              if (j + 1 < t.nt) paged_fetch(px, t.bh / H, t.kr, krow + BN, lane, next);
-            if (!(ok = wait(bar(B_KE(st)), ph ^ 1))) break;
-            // the mask slot's last readers were the softmax threads of step g - 8: they are
-            // done, since S(g - STAGES), whose K tile has just been released, came two steps
-            // or more after theirs
-            if constexpr (PAGED) paged_mask(px, lane, cur, sb + C1::MASK_OFF + (g % kMaskSlots) * 16);
-            if (lead) mbar_arrive_expect_tx(bar(B_KF(st)), C1::TILE_BYTES);
-            if constexpr (PAGED) {
-              __syncwarp();
-              paged_load<D>(px, &tmK, sb + C1::K_OFF + st * C1::TILE_BYTES, bar(B_KF(st)), t.hk,
-                            lane, cur);
-            } else {
-              for (int c = 0; c < C::NCHUNK; ++c)
-                tma_load_3d(sb + C1::K_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmK,
-                            bar(B_KF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
-            }
+            if (!(ok = mbar_wait(bar(B_KE(st)), ph ^ 1, ctl))) break;
+            mbar_arrive_expect_tx(bar(B_KF(st)), C1::TILE_BYTES);
+            for (int c = 0; c < C::NCHUNK; ++c)
+              tma_load_3d(sb + C1::K_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmK,
+                          bar(B_KF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
             ++nk;
-            if (!(ok = wait(bar(B_VE(st)), ph ^ 1))) break;
-            if (lead) mbar_arrive_expect_tx(bar(B_VF(st)), C1::TILE_BYTES);
-            if constexpr (PAGED) {
-              __syncwarp();
-              paged_load<D>(px, &tmV, sb + C1::V_OFF + st * C1::TILE_BYTES, bar(B_VF(st)), t.hk,
-                            lane, cur);
-            } else {
-              for (int c = 0; c < C::NCHUNK; ++c)
-                tma_load_3d(sb + C1::V_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmV,
-                            bar(B_VF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
-            }
+            if (!(ok = mbar_wait(bar(B_VE(st)), ph ^ 1, ctl))) break;
+            mbar_arrive_expect_tx(bar(B_VF(st)), C1::TILE_BYTES);
+            for (int c = 0; c < C::NCHUNK; ++c)
+              tma_load_3d(sb + C1::V_OFF + st * C1::TILE_BYTES + c * C::CHUNK_BYTES, &tmV,
+                          bar(B_VF(st)), c * C::ATOM, t.sr.y(krow, t.hk), t.sr.z(krow, t.hk));
             ++nv;
             if (j + 1 == t.nt) request();
           }
           if (!ok) break;
         }
         // the next tile: a CTA that had not started, if any was left
-        if (!(ok = wait(bar(B_CLC), k & 1))) break;
+        if (!(ok = mbar_wait(bar(B_CLC), k & 1, ctl))) break;
         pending = false;
         tile = clc_result(clc_resp);
       }
       if (!ok) {
-        if (pending) wait(bar(B_CLC), (n_req - 1) & 1);   // the response lands in smem
+        if (pending) mbar_wait(bar(B_CLC), (n_req - 1) & 1, ctl);   // the response lands in smem
         // drain: wait (bounded) for the copies this thread may still have in flight, so
         // no bulk copy lands in shared memory after the CTA has gone
-        for (int i = max(0, kq - 2); i < kq; ++i) wait(bar(B_QF(i & 1)), (i >> 1) & 1);
+        for (int i = max(0, kq - 2); i < kq; ++i) mbar_wait(bar(B_QF(i & 1)), (i >> 1) & 1, ctl);
         for (int i = max(0, nk - STAGES); i < nk; ++i)
-          wait(bar(B_KF(i % STAGES)), (i / STAGES) & 1);
+          mbar_wait(bar(B_KF(i % STAGES)), (i / STAGES) & 1, ctl);
         for (int i = max(0, nv - STAGES); i < nv; ++i)
-          wait(bar(B_VF(i % STAGES)), (i / STAGES) & 1);
+          mbar_wait(bar(B_VF(i % STAGES)), (i / STAGES) & 1, ctl);
       }
     }
     __syncwarp();
@@ -1053,11 +644,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       for (int k = 0; ok; ++k) {
         const int tile = next_tile(k, ok);
         if (!ok) break;
-        one::Tile1 t;
-        if constexpr (PAGED) t.nt = info(k & 1)->nt;
         mbar_arrive(bar(B_TE(k & 1)));
         if (tile < 0) break;
-        if constexpr (!PAGED) t = tile_of(tile);
+        const one::Tile1 t = tile_of(tile);
         if (t.nt == 0) continue;
         const int qb = kq & 1;
         if (!(ok = mbar_wait(bar(B_QF(qb)), (kq >> 1) & 1, ctl))) break;
@@ -1108,62 +697,14 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       int tile = next_tile(k, ok);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      // paged: the tile's slot is read again by the epilogue and given back after it
-      auto release = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_TE(k & 1)));
-      };
-      if (!PAGED || tile < 0) release();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_TE(k & 1)));
       if (tile < 0) break;
-      one::Tile1 t;
-      RowKeys rk;
-      int Nr = 0, Nk = 0, lo_key = 0;            // query rows, keys, first allowed key
-      if constexpr (PAGED) {
-        const one::Tile1* ti = info(k & 1);
-        t.nt = ti->nt;
-        t.lo = ti->lo;
-        t.row0 = ti->row0;
-        KeyRows kr;
-        kr.n = Nk = ti->kr.n;
-        kr.off = ti->kr.off;
-        kr.hi = ti->kr.hi;
-        rk = row_keys(kr, t.row0, t.row0 + rit, pack, window);
-      } else {
-        t = tile_of(tile);
-        Nr = Nk = t.sr.n;
-        lo_key = WINDOW ? t.row0 + rit - window + 1 : 0;
-      }
+      const one::Tile1 t = tile_of(tile);
+      if (t.nt == 0) continue;
+      const int Nr = t.sr.n;
       const int grow = t.row0 + rit;             // query row
-      // paged: where a row lies in O, and in L or its range's part of the workspace
-      auto load_place = [&]() {
-        const one::Tile1* ti = info(k & 1);
-        t.sr.base = ti->sr.base;
-        t.hq = ti->hq;
-        t.split = ti->split;
-        t.shared = ti->shared;
-        Nr = ti->nr;
-      };
-      auto row_at = [&](int r) -> size_t {
-        return static_cast<size_t>(t.sr.base + (r >> pack)) * H + t.hq + (r & ((1 << pack) - 1));
-      };
-      auto lse_at = [&](int r) -> float* {
-        if constexpr (PAGED)
-          if (t.shared) return px.part_l + static_cast<size_t>(t.split) * total * H + row_at(r);
-        return Lout + static_cast<size_t>(t.hq + (r & ((1 << pack) - 1))) * total + t.sr.base +
-               (r >> pack);
-      };
-      if (t.nt == 0) {
-        if constexpr (PAGED) {
-          load_place();
-          if (grow < Nr) {                       // a row before the first key: O = 0, L = -inf
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(Out) + row_at(grow) * D);
-            for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-            *lse_at(grow) = -INFINITY;
-          }
-          release();
-        }
-        continue;
-      }
+      const int lo_key = WINDOW ? grow - window + 1 : 0;   // first allowed key
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < t.nt; ++j, ++g) {
         if (!(ok = mbar_wait_warp(bar(B_SF), g & 1, ctl))) break;
@@ -1184,21 +725,11 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         // window the tiles reaching left of some row's first allowed key
         const bool need_mask = (CAUSAL && kbase + BN - 1 > t.row0) || (kbase + BN > Nr) ||
                                (WINDOW && kbase < t.row0 + BM - window);
-        if (PAGED) {
-          paged_masks(rk, kbase, sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
-        } else if (need_mask) {
+        if (need_mask) {
           const int lim = CAUSAL ? min(grow + 1, Nr) : Nr;   // keys in [lo_key, lim) are allowed
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (kbase + c >= lim || (WINDOW && kbase + c < lo_key)) sr_[c] = __float_as_uint(-INFINITY);
-        }
-        if constexpr (PAGED) {
-          if (kbase + BN > Nk) {                 // the last tile's V rows past the keys
-            const int st = g % STAGES;
-            if (!(ok = mbar_wait_warp(bar(B_VF(st)), (g / STAGES) & 1, ctl))) break;
-            if (kbase + rit >= Nk) clear_row<D>(sb + C1::V_OFF + st * C1::TILE_BYTES, rit);
-            fence_proxy_async_smem();            // before this thread's arrival on p_full
-          }
         }
         const float mx = row_max128(sr_);
         const float m_tile = mx * c_log2;
@@ -1266,10 +797,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (!(ok = mbar_wait_warp(bar(B_OF), kq & 1, ctl))) break;
       ++kq;
       tc_fence_after();
-      if constexpr (PAGED) load_place();
-      // a row whose keys are all masked (paged only): l = 0 and acc = 0
-      const bool none = PAGED && l_run == 0.f;
-      const float inv_l = none ? 0.f : 1.f / l_run;
+      const float inv_l = 1.f / l_run;
       const bool valid = grow < Nr;
       // Each thread writes its row of O (16-bit) to this warp's 32 staging rows in shared
       // memory, 16-byte chunk c of row r at chunk c ^ (r mod CPR), so the eight lanes of
@@ -1282,20 +810,6 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         uint32_t o[32];
         tmem_ld32(tO + 32 * cc, o);
         tmem_ld_wait_regs(o);
-        if constexpr (PAGED) {
-          if (t.shared) {
-            if (valid) {
-              float4* dst = reinterpret_cast<float4*>(
-                  px.part + (static_cast<size_t>(t.split) * total * H + row_at(grow)) * D + 32 * cc);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(
-                    __uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
-                    __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
-            }
-            continue;
-          }
-        }
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -1308,14 +822,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       }
       tc_fence_before();                         // O read before the next tile's p_full
       if (valid)
-        (PAGED ? *lse_at(grow)
-               : Lout[t.sr.packed ? static_cast<size_t>(t.hq) * total + t.sr.base + grow
-                                  : static_cast<size_t>(t.bh) * N + grow]) =
-            none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
-      if (PAGED && t.shared) {                   // nothing staged
-        release();
-        continue;
-      }
+        Lout[t.sr.packed ? static_cast<size_t>(t.hq) * total + t.sr.base + grow
+                         : static_cast<size_t>(t.bh) * N + grow] =
+            (m_run + log2f(l_run)) * 0.69314718055994531f;
       __syncwarp();
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       constexpr int RPI = 32 / CPR;              // rows per store instruction
@@ -1324,12 +833,10 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         const int r = i * RPI + lane / CPR, c = lane % CPR;   // row within the warp, chunk
         const int orow_g = t.row0 + (warp & 3) * 32 + r;
         if (orow_g < Nr) {
-          T* dst = reinterpret_cast<T*>(Out) +
-                   (PAGED ? row_at(orow_g) * D : t.sr.off(orow_g, t.hq, H, N, D)) + 8 * c;
+          T* dst = reinterpret_cast<T*>(Out) + t.sr.off(orow_g, t.hq, H, N, D) + 8 * c;
           *reinterpret_cast<uint4*>(dst) = stage[r * CPR + (c ^ (r % CPR))];
         }
       }
-      if constexpr (PAGED) release();
       __syncwarp();                              // staging rows free for the next tile
     }
   }
@@ -1342,20 +849,19 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   }
 }
 
-template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED, bool PAGED = false>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW, bool PACKED>
 cudaError_t launch_fwd1_t(const FwdArgs& a, cudaStream_t st) {
   using C1 = one::Cfg1<D>;
-  constexpr int smem = PAGED ? C1::PAGED_SMEM_BYTES : C1::SMEM_BYTES;
-  auto kern = fwd1_kernel<D, BF16, CAUSAL, WINDOW, PACKED, PAGED>;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
+  auto kern = fwd1_kernel<D, BF16, CAUSAL, WINDOW, PACKED>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), C1::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int n_qt = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + BM - 1) / BM);
+  const int n_qt = (a.N + BM - 1) / BM;
   const long long grid = static_cast<long long>(n_qt) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
-  e = launch_dependent(kern, static_cast<unsigned>(grid), one::THREADS, smem, st, a.tmQ,
+  e = launch_dependent(kern, static_cast<unsigned>(grid), one::THREADS, C1::SMEM_BYTES, st, a.tmQ,
                        a.tmK, a.tmV, a.O, a.L, a.N, n_qt, a.group, a.window, a.cu_seqlens, a.H,
-                       a.total, a.c_log2, a.ctl, paged_args<PAGED>(a));
+                       a.total, a.c_log2, a.ctl);
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1393,111 +899,6 @@ cudaError_t launch_fwd_d(const FwdArgs& a, int d, bool bf16, bool causal, bool w
                          cudaStream_t st) {
   return bf16 ? launch_fwd_b<true>(a, d, causal, window, packed, st)
               : launch_fwd_b<false>(a, d, causal, window, packed, st);
-}
-
-// Joins the KV ranges of a query tile: one warp per (query, head) of a sequence, which is
-// left alone where its tile was not cut.  TILES: query tiles of 128 rows that are cut together.
-constexpr int MERGE_THREADS = 128;
-template <int D, bool BF16, int TILES>
-__global__ void __launch_bounds__(MERGE_THREADS)
-    fwd_paged_merge_kernel(void* Out, float* Lout, const int* cu_seqlens, int N, int H, int total,
-                           int window, const PagedArgs<true> px) {
-  grid_dep_wait();                               // the ranges' results
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  SeqRows sr;
-  KeyRows kr;
-  rows_of<true>(px, cu_seqlens, b, N, total, sr, kr);
-  const long long i = static_cast<long long>(blockIdx.x) * (MERGE_THREADS / 32) + (threadIdx.x >> 5);
-  if (i >= static_cast<long long>(sr.n) * H) return;
-  const int q = static_cast<int>(i / H), h = static_cast<int>(i % H);
-  // the row in its block of packed heads, and the first row of its tiles
-  const int row = (q << px.pack) + (h & ((1 << px.pack) - 1));
-  const SplitRange sp = split_range<TILES>(kr, row / (TILES * BM) * (TILES * BM), sr.n << px.pack,
-                                           window, px.pack, px.n_split);
-  if (sp.used <= 1) return;
-  const size_t rows = static_cast<size_t>(total) * H;
-  const size_t at = static_cast<size_t>(sr.base + q) * H + h;
-  float l_max = -INFINITY;
-  for (int s = lane; s < sp.used; s += 32) l_max = fmaxf(l_max, px.part_l[s * rows + at]);
-#pragma unroll
-  for (int w = 16; w >= 1; w /= 2) l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, w));
-  float sum = 0.f, acc[D / 32] = {};
-#pragma unroll 4
-  for (int s = 0; s < sp.used; ++s) {
-    const float ls = px.part_l[s * rows + at];
-    if (ls == -INFINITY) continue;               // no key in this range: nothing was written
-    const float w = ex2((ls - l_max) * 1.4426950408889634f);
-    sum += w;
-    const float* src = px.part + (s * rows + at) * D + lane * (D / 32);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(src[e], w, acc[e]);
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  T* dst = static_cast<T*>(Out) + at * D + lane * (D / 32);
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    if constexpr (BF16) dst[e] = __float2bfloat16_rn(acc[e] * inv);
-    else dst[e] = __float2half_rn(acc[e] * inv);
-  }
-  if (lane == 0)
-    Lout[static_cast<size_t>(h) * total + sr.base + q] =
-        sum == 0.f ? -INFINITY : l_max + log2f(sum) * 0.69314718055994531f;
-}
-
-// Queries packed, keys in pages: one instance per head dim and type, its masks at run time
-// (no window: one that reaches past every key).
-template <int D, bool BF16>
-cudaError_t launch_fwd_paged_t(const FwdArgs& a, cudaStream_t st) {
-  cudaError_t e;
-  if constexpr (D == 128) e = launch_fwd_t<D, BF16, true, true, true, true>(a, st);
-  else e = launch_fwd1_t<D, BF16, true, true, true, true>(a, st);
-  if (e != cudaSuccess || a.n_split == 1) return e;
-  const long long warps = static_cast<long long>(a.N) * a.H;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps * 32 + MERGE_THREADS - 1) / MERGE_THREADS),
-                     static_cast<unsigned>(a.B));
-  cfg.blockDim = dim3(MERGE_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fwd_paged_merge_kernel<D, BF16, D == 128 ? NT : 1>, a.O, a.L,
-                            a.cu_seqlens, a.N, a.H, a.total, a.window, paged_args<true>(a));
-}
-
-template <bool BF16>
-cudaError_t launch_fwd_paged_b(const FwdArgs& a, int d, cudaStream_t st) {
-  if (d == 32) return launch_fwd_paged_t<32, BF16>(a, st);
-  if (d == 64) return launch_fwd_paged_t<64, BF16>(a, st);
-  if (d == 128) return launch_fwd_paged_t<128, BF16>(a, st);
-  return cudaErrorInvalidValue;
-}
-
-int fwd_paged_pack(int group) {
-  int p = 0;
-  while (p < 7 && group % (2 << p) == 0) ++p;
-  return p;
-}
-
-// Ranges per query tile: none where the tiles fill half the GPU or more (152 SMs; two CTAs
-// each at d <= 64), else as many as fill it once.
-int fwd_paged_splits(int B, int H, int Hkv, int max_seqlen, int d) {
-  const int pack = fwd_paged_pack(H / Hkv), rows = d == 128 ? NT * BM : BM;
-  const long long tiles = static_cast<long long>(B) * (H >> pack) *
-                          (((static_cast<long long>(max_seqlen) << pack) + rows - 1) / rows);
-  const long long slots = d == 128 ? 152 : 304;
-  return tiles * 2 > slots ? 1 : static_cast<int>(slots / tiles);
-}
-
-cudaError_t launch_fwd_paged(const FwdArgs& args, int d, bool bf16, bool causal, cudaStream_t st) {
-  FwdArgs a = args;
-  a.causal = causal;
-  if (!causal || a.window == 0) a.window = kNoLimit;
-  a.BH = a.B * (a.H >> a.pack) * a.n_split;
-  return bf16 ? launch_fwd_paged_b<true>(a, d, st) : launch_fwd_paged_b<false>(a, d, st);
 }
 
 cudaError_t launch_fwd(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st) {
