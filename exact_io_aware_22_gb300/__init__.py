@@ -16,7 +16,9 @@ import math
 import os
 
 __all__ = ["fwd", "bwd", "bwd_workspace_size", "device_status", "set_wait_limit_ns",
-           "selftest_timeout", "trace_enable", "trace_read", "FAError", "library_path", "load_library", "STATUS"]
+           "selftest_timeout", "trace_enable", "trace_read", "FAError", "library_path", "load_library", "STATUS",
+           "append_paged", "append_paged_fp8", "decode_paged", "decode_paged_fp8",
+           "decode_paged_workspace_size", "fwd_paged", "fwd_paged_workspace_size", "rope_table"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libfa_gb300.so")
