@@ -372,13 +372,30 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
   };
 #pragma unroll
   for (int st = 0; st < STAGES; ++st) okm[st] = 0;
-  fetch();
+  {
+    // the first stages' look-ups go out together
+    int id0[STAGES], row0[STAGES], hk0[STAGES];
+    bool has0[STAGES];
 #pragma unroll
-  for (int st = 0; st < STAGES; ++st) {
-    if (p_has) {
-      issue(st);
+    for (int st = 0; st < STAGES; ++st) {
       fetch();
+      id0[st] = pid;
+      row0[st] = prow;
+      hk0[st] = phk;
+      has0[st] = p_has;
     }
+    fetch();
+    const int id1 = pid, row1 = prow, hk1 = phk;
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) {
+      pid = id0[st];
+      prow = row0[st];
+      phk = hk0[st];
+      if (has0[st]) issue(st);
+    }
+    pid = id1;
+    prow = row1;
+    phk = hk1;
   }
 
   // shared-memory byte offsets of this lane's ldmatrix rows: lane i gives row i % 8 of block

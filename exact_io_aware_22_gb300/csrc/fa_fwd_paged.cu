@@ -1177,17 +1177,31 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   for (int s = lane; s < sp.used; s += 32) l_max = fmaxf(l_max, px.part_l[s * rows + at]);
 #pragma unroll
   for (int w = 16; w >= 1; w /= 2) l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, w));
-  float sum = 0.f, acc[D / 32] = {};
-#pragma unroll 4
-  for (int s = 0; s < sp.used; ++s) {
-    const float ls = px.part_l[s * rows + at];
-    if (ls == -INFINITY) continue;               // no key in this range: nothing was written
-    const float w = ex2((ls - l_max) * 1.4426950408889634f);
-    sum += w;
-    const float* src = px.part + (s * rows + at) * D + lane * (D / 32);
+  // weights of 32 ranges at a time, one per lane; their rows in batches of 8 loads that do not
+  // wait for one another (a range without keys has weight 0 and left nothing to read)
+  constexpr int E = D / 32;
+  float sum = 0.f, acc[E] = {};
+  for (int s0 = 0; s0 < sp.used; s0 += 32) {
+    const float ls = s0 + lane < sp.used ? px.part_l[(s0 + lane) * rows + at] : -INFINITY;
+    const float wl = ls == -INFINITY ? 0.f : ex2((ls - l_max) * 1.4426950408889634f);
+    sum += wl;
+    for (int k0 = 0; k0 < min(32, sp.used - s0); k0 += 8) {
+      float v[8][E], w[8];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(src[e], w, acc[e]);
+      for (int k = 0; k < 8; ++k) {
+        w[k] = __shfl_sync(0xffffffffu, wl, k0 + k);
+        const float* src = px.part + ((s0 + k0 + k) * rows + at) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = w[k] > 0.f ? src[e] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[k][e], w[k], acc[e]);
+    }
   }
+#pragma unroll
+  for (int w = 16; w >= 1; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   T* dst = static_cast<T*>(Out) + at * D + lane * (D / 32);
