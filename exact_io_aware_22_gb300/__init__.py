@@ -112,7 +112,7 @@ def load_library(path: str | None = None):
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_fp8.argtypes = [vp, pc, vp, vp, vp, sz, i, i, i, i, i, f, f, f, i, vp]
     lib.fa_decode_paged_fp8.restype = i
-    lib.fa_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.fa_fwd_paged_workspace_size.argtypes = [i, i, i, i, i]
     lib.fa_fwd_paged_workspace_size.restype = sz
     lib.fa_fwd_paged.argtypes = [vp, pc, vp, vp, vp, sz, vp, i, i, i, i, i, i, i, i, f, i, vp]
     lib.fa_fwd_paged.restype = i
@@ -524,7 +524,7 @@ def _with_workspace(dev: int, workspace, need: int, fn, head, tail) -> int:
 
 
 def _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B: int, d: int):
-    """struct fa_paged_cache of caches (pages, Hkv, page_size, d), and Hkv; ``dtype`` None: codes."""
+    """struct fa_paged_cache of caches (pages, Hkv, page_size, d), and Hkv; dtype None: codes."""
     import torch
     shape, st = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or shape != v_cache.shape or shape[3] != d:
@@ -575,7 +575,7 @@ def _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, scales, cu_
     elif page_table.shape[0] != T:
         raise ValueError("without cu_seqlens every sequence brings one token: T must be B")
     pc, heads = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else dtype, B, d)
-    if heads != Hkv:
+    if heads != Hkv or Hkv < 1:
         raise ValueError("the caches must have the heads of k and v")
     if q is not None:
         _one_device(k, q)
@@ -712,8 +712,8 @@ def decode_paged_fp8(q, k_cache8, v_cache8, page_table, cache_seqlens, k_scale: 
 
 
 @functools.lru_cache(maxsize=1024)
-def fwd_paged_workspace_size(B: int, total: int, max_seqlen: int, H: int, Hkv: int, d: int) -> int:
-    return int(load_library().fa_fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d))
+def fwd_paged_workspace_size(B: int, max_seqlen: int, H: int, Hkv: int, d: int) -> int:
+    return int(load_library().fa_fwd_paged_workspace_size(B, max_seqlen, H, Hkv, d))
 
 
 def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_seqlen: int,
@@ -747,7 +747,7 @@ def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_se
     elif lse.shape != (H, total) or lse.dtype != torch.float32 or not lse.is_contiguous() \
             or lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 (H, total) on q's device")
-    need = fwd_paged_workspace_size(B, total, max_seqlen, H, Hkv, d) if workspace is None else 0
+    need = fwd_paged_workspace_size(B, max_seqlen, H, Hkv, d) if workspace is None else 0
     st = _with_workspace(
         dev, workspace, need, load_library().fa_fwd_paged,
         (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),

@@ -935,6 +935,8 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   if (st != FA_OK) return st;
   if ((st = check_heads(H, Hkv)) != FA_OK) return st;
   if (window < 0 || !Q || !O || !L) return FA_ERR_INVALID_VALUE;
+  const float c_log2 = scale * (c8 ? k_scale : 1.f) * 1.4426950408889634f;
+  if (!(std::isfinite(c_log2) && c_log2 > 0.f)) return FA_ERR_INVALID_VALUE;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4) || (workspace && !aligned(workspace, 16)))
     return FA_ERR_MISALIGNED;
   fa::DecodePagedArgs a;
@@ -985,7 +987,7 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   a.Hkv = Hkv;
   a.window = window;
   a.box_log2 = lg;
-  a.c_log2 = scale * (c8 ? k_scale : 1.f) * 1.4426950408889634f;
+  a.c_log2 = c_log2;
   a.o_scale = c8 ? v_scale : 1.f;
   cudaError_t e = fa::launch_decode_paged(a, d, dtype == FA_BF16, c8, s);
   if (!workspace) {
@@ -996,9 +998,10 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-// Bytes of fa_fwd_paged's workspace: each range's O and L of every row, in fp32.
-size_t fwd_paged_ws(int splits, int total, int H, int d) {
-  return splits > 1 ? static_cast<size_t>(splits) * total * H * (d + 1) * sizeof(float) : 0;
+// Bytes of fa_fwd_paged's workspace: each range's O and L of every (query, head), in fp32.
+size_t fwd_paged_ws(int splits, int B, int max_seqlen, int H, int d) {
+  return splits > 1 ? static_cast<size_t>(splits) * B * max_seqlen * H * (d + 1) * sizeof(float)
+                    : 0;
 }
 
 fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, float* L,
@@ -1010,12 +1013,15 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   if ((st = check_heads(H, Hkv)) != FA_OK) return st;
   if ((st = check_packed(cu_seqlens, total)) != FA_OK) return st;
   if (window < 0 || (window > 0 && !causal) || !Q || !O || !L) return FA_ERR_INVALID_VALUE;
+  const float c_log2 = scale * 1.4426950408889634f;
+  if (!(std::isfinite(c_log2) && c_log2 > 0.f)) return FA_ERR_INVALID_VALUE;
   const int pack = fa::fwd_paged_pack(H / Hkv);
-  if (static_cast<long long>(max_seqlen) << pack > (1 << 29) || B > 65535) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_seqlen) << pack > (1 << 29) || B > 65535)
+    return FA_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4) || (workspace && !aligned(workspace, 16)))
     return FA_ERR_MISALIGNED;
   const int splits = fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d);
-  const size_t need = fwd_paged_ws(splits, total, H, d);
+  const size_t need = fwd_paged_ws(splits, B, max_seqlen, H, d);
   if (need && workspace && workspace_bytes < need) return FA_ERR_INVALID_VALUE;
   fa::FwdArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -1055,7 +1061,7 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   a.B = B;
   a.pack = pack;
   a.n_split = splits;
-  a.c_log2 = scale * 1.4426950408889634f;
+  a.c_log2 = c_log2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = workspace;
   if (need && !ws) {
@@ -1063,7 +1069,7 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
     if (e != cudaSuccess) return cuda_fail(e);
   }
   a.part = static_cast<float*>(ws);
-  a.part_l = a.part + static_cast<size_t>(splits) * total * H * d;
+  a.part_l = a.part + static_cast<size_t>(splits) * B * max_seqlen * H * d;
   cudaError_t e = fa::launch_fwd_paged(a, d, bf16, causal != 0, s);
   if (need && !workspace) {
     cudaError_t e2 = cudaFreeAsync(ws, s);
@@ -1122,11 +1128,10 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
                            dtype, stream, true, k_scale, v_scale);
 }
 
-size_t fa_fwd_paged_workspace_size(int B, int total, int max_seqlen, int H, int Hkv, int d) {
-  if (check_common(B, H, max_seqlen, d, 1, 1.f, FA_FP16) != FA_OK || check_heads(H, Hkv) != FA_OK ||
-      total < 1)
+size_t fa_fwd_paged_workspace_size(int B, int max_seqlen, int H, int Hkv, int d) {
+  if (check_common(B, H, max_seqlen, d, 1, 1.f, FA_FP16) != FA_OK || check_heads(H, Hkv) != FA_OK)
     return 0;
-  return fwd_paged_ws(fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d), total, H, d);
+  return fwd_paged_ws(fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d), B, max_seqlen, H, d);
 }
 
 fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
@@ -1134,8 +1139,8 @@ fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, floa
                        int total, int max_seqlen, int H, int Hkv, int d, int causal, int window,
                        float scale, fa_dtype dtype, void* stream) {
   if (!cu_seqlens) return FA_ERR_INVALID_VALUE;
-  return fwd_paged_impl(Q, cache, O, L, workspace, workspace_bytes, cu_seqlens, B, total, max_seqlen,
-                        H, Hkv, d, causal, window, scale, dtype, stream);
+  return fwd_paged_impl(Q, cache, O, L, workspace, workspace_bytes, cu_seqlens, B, total,
+                        max_seqlen, H, Hkv, d, causal, window, scale, dtype, stream);
 }
 
 }  // extern "C"

@@ -12,11 +12,13 @@
 // (two 16-byte loads, two stores) -- both halves of 8 pairs -- so a rotation needs no exchange
 // between threads.  A thread carries the same 16 columns of up to M heads of one token, which
 // share the 16 table values that turn them; a token takes as many threads as that needs, and
-// a CTA as many tokens as fit (or a slice of one).  The data are
-// loaded before the token's position is known: finding the sequence, its length and the page
-// is a chain of dependent loads that the data loads then hide.  All loads are
-// plain ones, not read-only-path ones: earlier work in the stream may still be writing their
-// sources when this kernel starts, and nothing may move them above grid_dep_wait().
+// a CTA as many tokens as fit (or a slice of one).  The data are loaded before the token's
+// position is known: finding the sequence, its length and the page is a chain of dependent
+// loads that the data loads then hide.  All loads are plain ones, not read-only-path ones:
+// earlier work in the stream may still be writing their sources when this kernel starts, and
+// nothing may move them above grid_dep_wait().
+// Measured, 32/8 heads, d = 128, bf16: 16 prompts of 600-1100 tokens 55 us (6.3 TB/s), one token
+// 1.9 us, 64 tokens 2.2 us.
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -27,7 +29,7 @@ namespace fa {
 namespace {
 
 constexpr int APP_THREADS = 128;
-constexpr int APP_CTAS = 8;                       // CTAs per SM up to which heads go one to a thread
+constexpr int APP_CTAS = 8;                       // CTAs per SM up to which a thread has one head
 
 // The sequence b and key position pos of token t; false for a token that belongs to no
 // sequence or lies before its sequence's first key.

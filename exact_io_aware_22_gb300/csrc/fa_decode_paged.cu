@@ -7,8 +7,8 @@
 //
 // Bound: the cache's bytes.  Each K and V row is read once from HBM and serves all query
 // heads of its group (up to 16 per CTA; the CTAs of a larger group's parts walk the same keys
-// side by side, so that all but one find them in L2), so the products are kept off the critical path: they
-// run as warp-level tensor-core products (m16n8k16) with the *keys* as the rows,
+// side by side, so that all but one find them in L2).  The products are kept off the critical
+// path: they run as warp-level tensor-core products (m16n8k16) with the *keys* as the rows,
 //     S^T (16 keys x 8 heads) = K Q^T,      O^T (16 columns x 8 heads) += V^T P^T,
 // so a group of up to 8 heads pads nothing but n = 8, K and V^T are fragments that ldmatrix
 // reads from the tiles as TMA laid them down, and S^T becomes the second product's operand by
@@ -26,10 +26,14 @@
 // of a row then sits at the row's position 2i + 1, and a CTA has the units at its positions.
 // Where the table (or the window) bounds every row to a few units, each row has a CTA of its
 // own instead: nothing to scan, nothing to join.
+//
+// Measured, 32/8 heads, d = 128: 16 sequences of 16384-32768 keys 0.238 ms in bf16 (6.8 TB/s,
+// the rate of a copy) and 0.130 ms in E4M3 (6.2 TB/s); one sequence of 130049 keys 0.090 ms
+// (5.9 TB/s).  About 10 us of every call that cuts rows do not depend on the bytes: 3 us until
+// the first load is out, 3 to 4 us of join, and ranges that end up to 10 % apart.  Short rows
+// that are not cut: one sequence of 60 keys 3.7 us, 256 of 250-500 keys 63 us (5.8 TB/s).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
-
-#include <cuda_fp8.h>
 
 namespace fa {
 
@@ -48,7 +52,7 @@ template <int D, bool C8>
 struct Geom {
   static constexpr int ELEM = C8 ? 1 : 2;
   static constexpr int BOXC = C8 ? D : (D == 32 ? 32 : 64);   // columns of one TMA box
-  static constexpr int ROWB = BOXC * ELEM;                    // bytes of a box row: one swizzle span
+  static constexpr int ROWB = BOXC * ELEM;                    // bytes of a box row (swizzle span)
   static constexpr int SWM = ROWB == 128 ? 7 : 3;             // 16-byte chunk bits ^= row bits
   static constexpr int HALVES = D / BOXC;
   static constexpr int KEYS = 4096 / (D * ELEM);              // 16, 32 or 64
@@ -59,7 +63,9 @@ struct Geom {
 };
 
 template <int D, bool C8, int NT>
-__host__ __device__ constexpr int ring_bytes() { return DP_WARPS * stages_of(NT) * Geom<D, C8>::STAGEB; }
+__host__ __device__ constexpr int ring_bytes() {
+  return DP_WARPS * stages_of(NT) * Geom<D, C8>::STAGEB;
+}
 // two warps' states of 8 heads: m, l, then acc, heads 16 bytes apart mod 128
 template <int D>
 __host__ __device__ constexpr int red_bytes() { return 2 * 8 * (D + 4) * 4; }
@@ -166,7 +172,8 @@ __device__ __forceinline__ SeqKeys seq_keys(const PagedView& pg, int b, int wind
 // Cost of a row of `units` units (see above).
 __host__ __device__ constexpr int row_cost(int units) { return units > 0 ? 2 * units + 1 : 0; }
 
-// A place in a CTA's range: row r (K/V head) of sequence b, unit u of the row; the range covers the row's units up to ue, and `left` positions after the row's.
+// A place in a CTA's range: row r (K/V head) of sequence b, unit u of the row; the range
+// covers the row's units up to ue, and `left` positions after the row's.
 struct Cursor {
   int b, r, u, ue, left;
   SeqKeys s;
@@ -176,8 +183,8 @@ template <int D, bool BF16, bool C8, int NT>
 __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     decode_paged_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const void* Q, void* O, float* L,
-                        uint8_t* ws, int B, int H, int Hkv, int window, int direct, int box_log2, float c_log2,
-                        float o_scale, const PagedView pg, KernelCtl ctl) {
+                        uint8_t* ws, int B, int H, int Hkv, int window, int direct, int box_log2,
+                        float c_log2, float o_scale, const PagedView pg, KernelCtl ctl) {
   using G = Geom<D, C8>;
   constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT, STAGES = stages_of(NT);
   constexpr bool MB = BF16 && !C8;               // operands of the products: bf16 or f16
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
       return;
     }
   } else {
-    const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);                // sequences per thread
+    const int per = (B + 32 * DP_WARPS - 1) / (32 * DP_WARPS);   // sequences per thread
     int mine = 0;
     for (int i = 0; i < per; ++i) {
       const int b = threadIdx.x * per + i;
@@ -252,7 +259,8 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
       const int o = __shfl_up_sync(0xffffffffu, incl, w);
       if (lane >= w) incl += o;
     }
-    volatile int* sc = reinterpret_cast<volatile int*>(smem_raw + (scan - raw));   // [4] sums, [2] start
+    // [4] warps' sums, then the sequence that holds the range's start and its position
+    volatile int* sc = reinterpret_cast<volatile int*>(smem_raw + (scan - raw));
     if (lane == 31) sc[warp] = incl;
     __syncthreads();
     int before = 0, total = 0;
@@ -720,7 +728,8 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     }
     // ---- a row that is whole in this CTA gives its result, one cut by a border its state
     if (warp == 0) {
-      float* rec = part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_u > 0 ? 0 : 1)) * RG * (D + 4);
+      const int slot = seg_u > 0 ? 0 : 1;
+      float* rec = part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * RG * (D + 4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -784,7 +793,7 @@ __global__ void __launch_bounds__(DP_MERGE_THREADS)
   const int nrow = min(RG, grp - rg * RG);
   const size_t h0 = static_cast<size_t>(b) * H + hk * grp + rg * RG;
   const int n_sl = h.c1 - h.c0, sl = x - h.c0 - 1, n = n_sl + 1;
-  int gs = 0;                                    // threads per output: up to 16, PER / 2 states each
+  int gs = 0;                                    // up to 16 threads per output, PER / 2 states each
   while (gs < 4 && (PER / 2 << gs) < n) ++gs;
   const int tg = threadIdx.x & ((1 << gs) - 1), outs = DP_MERGE_THREADS >> gs;
   const int n_out = nrow * (D / 4);
@@ -887,8 +896,8 @@ cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   const long long longest = a.window > 0 && a.window < cap ? a.window : cap;
   const long long cost = decode_paged_cost(a.Hkv, D, C8, longest), most = a.B * cost / 2;
   const int n_rg = (a.H / a.Hkv + 8 * NT - 1) / (8 * NT);
-  const bool direct = rows_direct((cost / a.Hkv - 1) / 2, static_cast<long long>(a.B) * a.Hkv * n_rg,
-                                  grid_of(NT));
+  const bool direct = rows_direct((cost / a.Hkv - 1) / 2,
+                                  static_cast<long long>(a.B) * a.Hkv * n_rg, grid_of(NT));
   // at least two positions per range, ranges no more than run at once
   const long long fit = grid_of(NT) / n_rg;
   const long long ranges = direct ? static_cast<long long>(a.B) * a.Hkv
@@ -898,7 +907,8 @@ cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   trace_begin(TR_DEC_SPLIT, st);
   e = launch_dependent(kern, grid, 32 * DP_WARPS, smem, st, a.tmK, a.tmV, a.Q, a.O, a.L, ws, a.B,
-                       a.H, a.Hkv, a.window, static_cast<int>(direct), a.box_log2, a.c_log2, a.o_scale, a.pg, a.ctl);
+                       a.H, a.Hkv, a.window, static_cast<int>(direct), a.box_log2, a.c_log2, a.o_scale,
+                       a.pg, a.ctl);
   trace_end(TR_DEC_SPLIT, st);
   if (e != cudaSuccess || direct || ranges == 1) return e;   // no row is cut
   trace_begin(TR_DEC_MERGE, st);

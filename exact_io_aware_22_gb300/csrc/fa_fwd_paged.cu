@@ -81,8 +81,9 @@ struct PagedArgs {
   int box_log2, causal, window;    // window: kNoLimit for none
   int pack;                        // log2 of the heads in a query tile
   int n_split;                     // KV ranges per query tile (1: no workspace)
-  float* part;                     // [n_split][total * H][D] results of the ranges
-  float* part_l;                   // [n_split][total * H] their logsumexp (natural log)
+  size_t rows;                     // (query, head) pairs of all sequences: B * max_seqlen * H
+  float* part;                     // [n_split][rows][D] results of the ranges
+  float* part_l;                   // [n_split][rows] their logsumexp (natural log)
 };
 constexpr int kNoLimit = 1 << 30;
 // Keys of a sequence with nq query rows: query row i is at key position i + off and sees keys
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   grid_dep_launch();                            // the next kernel may start setting up
   grid_dep_wait();                              // offsets, lengths, table and inputs are written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const BlockPos bp = block_pos(n_qblk);        // bp.bh: (sequence, block of packed heads, KV range)
+  const BlockPos bp = block_pos(n_qblk);        // bp.bh: (sequence, block of heads, KV range)
   const int pack = px.pack, blocks = H >> pack;
   const int split = bp.bh % px.n_split, bh = bp.bh / px.n_split;
   const int b = bh / blocks;
@@ -288,12 +289,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   const int n_stream = n_max - j0;              // KV tiles loaded, j0 .. n_max - 1
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  // where row `grow` lies in O, and in L or its range's part of the workspace
+  // where row `grow` lies in O, in the workspace, and in L or the workspace's L
   auto row_at = [&](int grow) -> size_t {
     return static_cast<size_t>(sr.base + (grow >> pack)) * H + hq + (grow & ((1 << pack) - 1));
   };
+  auto part_at = [&](int grow) -> size_t {
+    return split * px.rows + (static_cast<size_t>(b) * N + (grow >> pack)) * H + hq +
+           (grow & ((1 << pack) - 1));
+  };
   auto lse_at = [&](int grow) -> float* {
-    if (shared) return px.part_l + static_cast<size_t>(split) * total * H + row_at(grow);
+    if (shared) return px.part_l + part_at(grow);
     return Lout + static_cast<size_t>(hq + (grow & ((1 << pack) - 1))) * total + sr.base +
            (grow >> pack);
   };
@@ -554,8 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld_wait_regs(o);
         if (shared) {
           if (valid) {
-            float4* dst = reinterpret_cast<float4*>(
-                px.part + (static_cast<size_t>(split) * total * H + row_at(grow)) * D + 32 * cc);
+            float4* dst = reinterpret_cast<float4*>(px.part + part_at(grow) * D + 32 * cc);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[i] = make_float4(
@@ -602,6 +606,7 @@ PagedArgs paged_args(const FwdArgs& a) {
   px.window = a.window;
   px.pack = a.pack;
   px.n_split = a.n_split;
+  px.rows = static_cast<size_t>(a.B) * a.N * a.H;
   px.part = a.part;
   px.part_l = a.part_l;
   return px;
@@ -616,13 +621,14 @@ cudaError_t launch_fwd_paged2_t(const FwdArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int n_qblk = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + NT * BM - 1) / (NT * BM));
+  const int n_qblk =
+      static_cast<int>(((static_cast<long long>(a.N) << a.pack) + NT * BM - 1) / (NT * BM));
   const long long grid = static_cast<long long>(n_qblk) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
-  e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, smem, st, a.tmQ,
-                       a.tmK, a.tmV, a.O, a.L, a.N, n_qblk, a.group, a.cu_seqlens, a.H, a.total, a.c_log2,
-                       a.ctl, paged_args(a));
+  e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, smem, st, a.tmQ, a.tmK, a.tmV,
+                       a.O, a.L, a.N, n_qblk, a.group, a.cu_seqlens, a.H, a.total, a.c_log2, a.ctl,
+                       paged_args(a));
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -631,8 +637,9 @@ cudaError_t launch_fwd_paged2_t(const FwdArgs& a, cudaStream_t st) {
 // One 128-row query tile at a time per CTA, two CTAs per SM, each persistent: it takes further
 // tiles from CTAs that have not been launched yet (cluster launch control).
 //   warp 0      TMA producer and scheduler: publishes each tile, with what its look-ups gave
-//               (lengths, ranges), in a two-slot ring, loads its Q tile (double-buffered) and streams K_j / V_j into a ring
-//               that runs on across tiles, then asks for the next tile.
+//               (lengths, ranges), in a two-slot ring, loads its Q tile (double-buffered) and
+//               streams K_j / V_j into a ring that runs on across tiles, then asks for the next
+//               tile.
 //   warp 1      TMEM allocator; lane 0 issues every tcgen05.mma and commit.
 //   warps 2-5   softmax, one thread per query row (TMEM lane quadrant = warp % 4),
 //               and the epilogue of each tile.
@@ -776,7 +783,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
     // ------------------------------------------------------------ producer, scheduler
     {
       const bool lead = lane == 0;               // does what is done once
-      auto wait = [&](uint32_t b, uint32_t parity) -> bool { return mbar_wait_warp(b, parity, ctl); };
+      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        return mbar_wait_warp(b, parity, ctl);
+      };
       bool ok = true;
       int tile = static_cast<int>(blockIdx.x);
       int g = 0, kq = 0, nk = 0, nv = 0;         // steps, Q tiles, K and V tiles loaded
@@ -957,12 +966,16 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       const int nt = ti->nt, lo = ti->lo, row0 = ti->row0, Nk = ti->kr.n;
       const RowKeys rk = row_keys(ti->kr, row0, row0 + rit, pack, px.window);
       const int grow = row0 + rit;               // query row
-      // where a row lies in O, and in L or its range's part of the workspace
+      // where a row lies in O, in the workspace, and in L or the workspace's L
       auto row_at = [&](int r) -> size_t {
         return static_cast<size_t>(ti->base + (r >> pack)) * H + ti->hq + (r & ((1 << pack) - 1));
       };
+      auto part_at = [&](int r) -> size_t {
+        return ti->split * px.rows + (static_cast<size_t>(ti->b) * N + (r >> pack)) * H + ti->hq +
+               (r & ((1 << pack) - 1));
+      };
       auto lse_at = [&](int r) -> float* {
-        if (ti->shared) return px.part_l + static_cast<size_t>(ti->split) * total * H + row_at(r);
+        if (ti->shared) return px.part_l + part_at(r);
         return Lout + static_cast<size_t>(ti->hq + (r & ((1 << pack) - 1))) * total + ti->base +
                (r >> pack);
       };
@@ -1082,8 +1095,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         tmem_ld_wait_regs(o);
         if (shared) {
           if (valid) {
-            float4* dst = reinterpret_cast<float4*>(
-                px.part + (static_cast<size_t>(ti->split) * total * H + row_at(grow)) * D + 32 * cc);
+            float4* dst = reinterpret_cast<float4*>(px.part + part_at(grow) * D + 32 * cc);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[i] = make_float4(
@@ -1145,8 +1157,8 @@ cudaError_t launch_fwd_paged1_t(const FwdArgs& a, cudaStream_t st) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
   e = launch_dependent(kern, static_cast<unsigned>(grid), one::THREADS, smem, st, a.tmQ,
-                       a.tmK, a.tmV, a.O, a.L, a.N, n_qt, a.group, a.cu_seqlens, a.H, a.total, a.c_log2,
-                       a.ctl, paged_args(a));
+                       a.tmK, a.tmV, a.O, a.L, a.N, n_qt, a.group, a.cu_seqlens, a.H, a.total,
+                       a.c_log2, a.ctl, paged_args(a));
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1163,7 +1175,8 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   SeqRows sr;
   KeyRows kr;
   rows_of(px, cu_seqlens, b, N, total, sr, kr);
-  const long long i = static_cast<long long>(blockIdx.x) * (MERGE_THREADS / 32) + (threadIdx.x >> 5);
+  const long long i =
+      static_cast<long long>(blockIdx.x) * (MERGE_THREADS / 32) + (threadIdx.x >> 5);
   if (i >= static_cast<long long>(sr.n) * H) return;
   const int q = static_cast<int>(i / H), h = static_cast<int>(i % H);
   // the row in its block of packed heads, and the first row of its tiles
@@ -1171,8 +1184,7 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   const SplitRange sp = split_range<TILES>(kr, row / (TILES * BM) * (TILES * BM), sr.n << px.pack,
                                            px.window, px.pack, px.n_split);
   if (sp.used <= 1) return;
-  const size_t rows = static_cast<size_t>(total) * H;
-  const size_t at = static_cast<size_t>(sr.base + q) * H + h;
+  const size_t rows = px.rows, at = (static_cast<size_t>(b) * N + q) * H + h;   // in the workspace
   float l_max = -INFINITY;
   for (int s = lane; s < sp.used; s += 32) l_max = fmaxf(l_max, px.part_l[s * rows + at]);
 #pragma unroll
@@ -1204,9 +1216,9 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   for (int w = 16; w >= 1; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  T* dst = static_cast<T*>(Out) + at * D + lane * (D / 32);
+  T* dst = static_cast<T*>(Out) + (static_cast<size_t>(sr.base + q) * H + h) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
+  for (int e = 0; e < E; ++e) {
     if constexpr (BF16) dst[e] = __float2bfloat16_rn(acc[e] * inv);
     else dst[e] = __float2half_rn(acc[e] * inv);
   }

@@ -467,7 +467,7 @@ def test_fwd_repeats_and_replays_bit_for_bit():
         kc, vc, tb, sl = pool.cuda()
         cu = torch.tensor([0, 300, 310, 333], dtype=torch.int32, device="cuda")
         q = torch.randn(333, H, d, device="cuda").bfloat16()
-        assert (fa.fwd_paged_workspace_size(3, 333, 300, H, 2, d) > 0) == (H == 4)
+        assert (fa.fwd_paged_workspace_size(3, 300, H, 2, d) > 0) == (H == 4)
         want = fa.fwd_paged(q, kc, vc, tb, sl, cu, 300)
         o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
         graph = torch.cuda.CUDAGraph()

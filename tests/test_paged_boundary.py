@@ -95,7 +95,7 @@ def test_strides_of_single_entries_do_not_matter(lib):
     (dict(O=5 * M), INVALID), (dict(O=M + 512), INVALID), (dict(L=2 * M), INVALID),
     (dict(O=3 * M), INVALID), (dict(L=4 * M), INVALID), (dict(L=6 * M + 16), INVALID),
     (dict(ws=6 * M, ws_bytes=1 << 30), INVALID), (dict(ws=2 * M, ws_bytes=1 << 30), INVALID),
-    (dict(B=2 ** 31 - 1), UNSUPPORTED), (dict(H=4880, Hkv=1), UNSUPPORTED),
+    (dict(B=2 ** 31 - 1), UNSUPPORTED), (dict(H=4880, Hkv=1), UNSUPPORTED), (dict(scale=3e38), INVALID),
 ])
 def test_decode_rejects(lib, kw, code):
     assert decode(lib, **kw) == code
@@ -103,7 +103,7 @@ def test_decode_rejects(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(d=64), UNSUPPORTED), (dict(ks=0.0), INVALID), (dict(vs=float("inf")), INVALID),
-    (dict(ks=-1.0), INVALID), (dict(vs=1e-45), INVALID),
+    (dict(ks=-1.0), INVALID), (dict(vs=1e-45), INVALID), (dict(ks=1e-30, scale=1e-20), INVALID),
 ])
 def test_decode_fp8_rejects(lib, kw, code):
     assert decode(lib, fp8=True, **kw) == code
@@ -174,6 +174,7 @@ def test_fwd_cache_rejects(lib, kw, code):
     (dict(O=M), INVALID), (dict(L=2 * M + 64), INVALID), (dict(O=3 * M), INVALID),
     (dict(L=4 * M), INVALID), (dict(L=8 * M), INVALID), (dict(L=6 * M + 64), INVALID),
     (dict(max_len=(1 << 27) + 1), UNSUPPORTED), (dict(B=65536), UNSUPPORTED),
+    (dict(scale=3e38), INVALID),
     (dict(ws=11 * M, ws_bytes=64), INVALID), (dict(ws=11 * M + 8, ws_bytes=1 << 30), MISALIGNED),
     (dict(ws=6 * M, ws_bytes=1 << 30), INVALID), (dict(ws=2 * M, ws_bytes=1 << 30), INVALID),
 ])
@@ -184,12 +185,12 @@ def test_fwd_rejects(lib, kw, code):
 def test_fwd_workspace_size(lib):
     f = lib.fa_fwd_paged_workspace_size
     # 3 sequences x 2 blocks of 4 packed heads x 1 tile of 256 rows: 152 // 6 = 25 ranges of
-    # 40 x 8 rows of 128 columns and a logsumexp, in fp32
-    assert f(3, 40, 20, 8, 2, 128) == 25 * 40 * 8 * 129 * 4
+    # 3 x 20 x 8 rows of 128 columns and a logsumexp, in fp32, whatever the padded total
+    assert f(3, 20, 8, 2, 128) == 25 * 60 * 8 * 129 * 4
     # at d = 64 tiles of 128 rows, two CTAs on each SM
-    assert f(3, 120, 40, 8, 2, 64) == (304 // 12) * 120 * 8 * 65 * 4
-    assert f(4, 4096, 1024, 32, 8, 128) == 0                  # tiles enough
-    assert f(3, 40, 20, 8, 3, 128) == 0 and f(3, 0, 20, 8, 2, 128) == 0
+    assert f(3, 40, 8, 2, 64) == (304 // 12) * 120 * 8 * 65 * 4
+    assert f(4, 1024, 32, 8, 128) == 0                        # tiles enough
+    assert f(3, 20, 8, 3, 128) == 0 and f(3, 0, 8, 2, 128) == 0
 
 
 def test_fwd_without_cache_rejects(lib):
