@@ -477,138 +477,161 @@ def decode_fp8(q, k_cache8, v_cache8, cache_seqlens, k_scale: float, v_scale: fl
 
 
 # The calls on paged caches are made once per layer and generated token, so what they do on
-# the host counts: each looks at every tensor once, asks torch for the raw stream handle and
-# takes workspaces from torch's allocator without making a tensor of them (making a Stream or
-# a tensor between two launches costs 2 and 7 us on the GB300's host).
+# the host counts (an attribute of a tensor costs 0.1 us, the launch itself 2): each looks at
+# every tensor once, asks torch for the raw stream handle and takes workspaces from torch's
+# allocator without making a tensor of them (making a Stream or a tensor between two launches
+# costs 2 and 7 us on the GB300's host).
+@functools.lru_cache(maxsize=1)
+def _paged_env():
+    """(torch, int32, fp32, {dtype: its code in the C ABI}, current device, raw stream of a
+    device): looked up once, since this module imports torch only when it is used."""
+    import torch
+    return (torch, torch.int32, torch.float32, {torch.float16: FA_FP16, torch.bfloat16: FA_BF16},
+            torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+
+
 def _one_device(*ts) -> int:
-    """Index of the one CUDA device of all tensors."""
+    """Index of the one CUDA device of all tensors (None entries aside)."""
     dev = ts[0].get_device()
     if dev < 0 or not ts[0].is_cuda:
         raise ValueError("all tensors must be CUDA tensors")
     for t in ts:
-        if t.get_device() != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be CUDA tensors on one device")
     return dev
 
 
-def _on_device(dev: int, fn, *args) -> int:
+def _call(dev: int, fn, *args) -> int:
     """fn(*args, current stream of dev) with dev current, as the library's calls expect."""
-    import torch
-    if dev == torch._C._cuda_getDevice():
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    torch, _, _, _, current, stream = _paged_env()
+    if dev == current():
+        return fn(*args, stream(dev))
     with torch.cuda.device(dev):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        return fn(*args, stream(dev))
 
 
-def _with_workspace(dev: int, workspace, need: int, fn, head, tail) -> int:
+def _call_ws(dev: int, workspace, need: int, fn, head, tail) -> int:
     """fn(*head, workspace, its bytes, *tail, stream): the caller's workspace, or `need` bytes
     from torch's allocator, given back once the call has enqueued its work (they are then
     reused by later work of the same stream only; inside a capture they belong to the graph)."""
-    import torch
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError("workspace must be contiguous, on q's device")
-        return _on_device(dev, fn, *head, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), *tail)
+        return _call(dev, fn, *head, workspace.data_ptr(),
+                     workspace.numel() * workspace.element_size(), *tail)
     if need == 0:
-        return _on_device(dev, fn, *head, None, 0, *tail)
-    if dev != torch._C._cuda_getDevice():
+        return _call(dev, fn, *head, None, 0, *tail)
+    torch, _, _, _, current, stream = _paged_env()
+    if dev != current():
         with torch.cuda.device(dev):
-            return _with_workspace(dev, None, need, fn, head, tail)
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+            return _call_ws(dev, None, need, fn, head, tail)
+    st = stream(dev)
+    ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, st)
     try:
-        return fn(*head, ws, need, *tail, stream)
+        return fn(*head, ws, need, *tail, st)
     finally:
         torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
 
 
+def _16bit(dtype, codes) -> int:
+    code = codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: fp16 or bf16 expected")
+    return code
+
+
 def _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B: int, d: int):
     """struct fa_paged_cache of caches (pages, Hkv, page_size, d), and Hkv; dtype None: codes."""
-    import torch
-    shape, st = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or shape != v_cache.shape or shape[3] != d:
+    i32 = _paged_env()[1]
+    shape, st, t = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if shape != v_cache.shape or len(shape) != 4:
         raise ValueError("the caches must share one (pages, Hkv, page_size, d) shape")
-    t = k_cache.dtype
-    if t != v_cache.dtype or (k_cache.element_size() != 1 if dtype is None else t != dtype):
+    pages, Hkv, page_size, cols = shape
+    if cols != d:
+        raise ValueError("the caches' rows must have the columns of q, k and v")
+    if t is not v_cache.dtype or (k_cache.element_size() != 1 if dtype is None else t is not dtype):
         raise TypeError("E4M3 caches must be 1-byte tensors" if dtype is None
                         else "the caches must have the dtype of q, k and v")
     if st != v_cache.stride() or st[3] != 1:
         raise ValueError("the caches must share their strides, with contiguous columns")
     rows, ts = page_table.shape, page_table.stride()
-    if page_table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B \
+    if page_table.dtype is not i32 or len(rows) != 2 or rows[0] != B \
             or ts[1] != 1 and rows[1] > 1:
         raise ValueError("page_table must be int32 (B, max_pages) with contiguous rows")
-    if cache_seqlens.dtype != torch.int32 or cache_seqlens.shape != (B,) \
+    if cache_seqlens.dtype is not i32 or cache_seqlens.shape != (B,) \
             or not cache_seqlens.is_contiguous():
         raise ValueError("cache_seqlens must be a contiguous int32 tensor of B lengths")
+    width = rows[1]
     return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                       cache_seqlens.data_ptr(), st[0], st[1], st[2], ts[0] if B > 1 else rows[1],
-                       shape[0], shape[2], rows[1]), shape[1]
+                       cache_seqlens.data_ptr(), st[0], st[1], st[2], ts[0] if B > 1 else width,
+                       pages, page_size, width), Hkv
 
 
-def _token_stride(x, n: int, d: int) -> int:
-    """Elements between the tokens of x (T, n, d), whose heads and columns must be contiguous."""
-    s0, s1, s2 = x.stride()
-    if s2 != 1 or s1 != d and n > 1:
-        raise ValueError("heads and columns of a token must be contiguous")
-    return s0
+def _offsets(cu_seqlens, i32) -> int:
+    """Sequences of contiguous int32 offsets (B+1,)."""
+    if cu_seqlens.dtype is not i32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B+1 offsets")
+    B = cu_seqlens.numel() - 1
+    if B < 1:
+        raise ValueError("cu_seqlens must hold B+1 offsets")
+    return B
+
+
+def _result(t, shape, dtype, dev: int, name: str):
+    """The caller's contiguous output tensor, checked."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on the inputs' device")
+    return t
 
 
 def _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, scales, cu_seqlens, cos_sin,
                   interleaved, positions, q, q_out):
-    import torch
-    dev = _one_device(k, v, k_cache, v_cache, page_table, cache_seqlens)
+    torch, i32, f32, codes, _, _ = _paged_env()
+    dev = _one_device(k, v, k_cache, v_cache, page_table, cache_seqlens, q, cos_sin, cu_seqlens,
+                      positions)
     shape, dtype = k.shape, k.dtype
-    if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
+    if shape != v.shape or len(shape) != 3 or dtype is not v.dtype:
         raise ValueError("k and v must share one (T, Hkv, d) shape and dtype")
-    B = T = shape[0]
-    Hkv, d = shape[1], shape[2]
-    cu = pos = cs = qp = qo = None
-    H, q_stride, rot, max_pos = Hkv, 0, 0, 0
-    if cu_seqlens is not None:
-        _one_device(k, cu_seqlens)
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 \
-                or not cu_seqlens.is_contiguous():
-            raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B+1 offsets")
-        B, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
-    elif page_table.shape[0] != T:
-        raise ValueError("without cu_seqlens every sequence brings one token: T must be B")
+    T, Hkv, d = shape
+    code = _16bit(dtype, codes)
+    B = T if cu_seqlens is None else _offsets(cu_seqlens, i32)
     pc, heads = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else dtype, B, d)
     if heads != Hkv or Hkv < 1:
         raise ValueError("the caches must have the heads of k and v")
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if k2 != 1 or v2 != 1 or (k1 != d or v1 != d) and Hkv > 1:
+        raise ValueError("heads and columns of a token must be contiguous")
+    H, q0, q_ptr, out_ptr = Hkv, 0, None, None
     if q is not None:
-        _one_device(k, q)
         qs = q.shape
-        if len(qs) != 3 or qs[0] != T or qs[2] != d or q.dtype != dtype or qs[1] % Hkv:
+        if len(qs) != 3 or qs[0] != T or qs[2] != d or q.dtype is not dtype or qs[1] % Hkv:
             raise ValueError("q must be (T, H, d) of k's dtype with H a multiple of Hkv")
         H = qs[1]
+        q0, q1, q2 = q.stride()
+        if q2 != 1 or q1 != d and H > 1:
+            raise ValueError("heads and columns of a token must be contiguous")
         if q_out is None:
             q_out = torch.empty(qs, dtype=dtype, device=q.device)
-        elif q_out.shape != qs or q_out.dtype != dtype or not q_out.is_contiguous() \
-                or q_out.get_device() != dev:
-            raise ValueError("q_out must be contiguous, on q's device, and match q")
-        q_stride, qp, qo = _token_stride(q, H, d), q.data_ptr(), q_out.data_ptr()
+        else:
+            _result(q_out, qs, dtype, dev, "q_out")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
+    rot, max_pos, cs = 0, 0, None
     if cos_sin is not None:
-        _one_device(k, cos_sin)
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if cos_sin.dtype is not f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be contiguous fp32 (max_pos, rot_dim)")
         (max_pos, rot), cs = cos_sin.shape, cos_sin.data_ptr()
-    if positions is not None:
-        _one_device(k, positions)
-        if positions.dtype != torch.int32 or positions.shape != (T,) \
-                or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int32 tensor of T positions")
-        pos = positions.data_ptr()
+    if positions is not None and (positions.dtype is not i32 or positions.shape != (T,)
+                                  or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 tensor of T positions")
     lib = load_library()
-    args = (pc, k.data_ptr(), _token_stride(k, Hkv, d), v.data_ptr(), _token_stride(v, Hkv, d), qp,
-            q_stride, qo, cu, pos, cs, max_pos, rot, interleaved, B, T, H, Hkv, d)
-    if scales:
-        st = _on_device(dev, lib.fa_append_paged_fp8, *args, *scales, _dtype_code(k))
-    else:
-        st = _on_device(dev, lib.fa_append_paged, *args, _dtype_code(k))
+    st = _call(dev, lib.fa_append_paged_fp8 if scales else lib.fa_append_paged,
+               pc, k.data_ptr(), k0, v.data_ptr(), v0, q_ptr, q0, out_ptr,
+               None if cu_seqlens is None else cu_seqlens.data_ptr(),
+               None if positions is None else positions.data_ptr(), cs, max_pos, rot, interleaved,
+               B, T, H, Hkv, d, *scales, code)
     if st:
         _check(st, "fa_append_paged_fp8" if scales else "fa_append_paged")
     return q_out
@@ -629,7 +652,7 @@ def append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens=N
     ``interleaved``.  With q (T, H, d) the same tokens' queries are turned into q_out, which
     is returned (else None).  A token whose page or angle position lies outside its tensor
     is left out, and ``device_status()`` then reports FA_ERR_INVALID_VALUE."""
-    return _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, None, cu_seqlens,
+    return _append_paged(k, v, k_cache, v_cache, page_table, cache_seqlens, (), cu_seqlens,
                          cos_sin, interleaved, positions, q, q_out)
 
 
@@ -661,30 +684,29 @@ def decode_paged_workspace_size(H: int, Hkv: int, d: int) -> int:
 
 def _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scales, scale, window, out, lse,
                   workspace):
-    import torch
+    torch, _, f32, codes, _, _ = _paged_env()
     dev = _one_device(q, k_cache, v_cache, page_table, cache_seqlens)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous (B, H, d) tensor")
     B, H, d = shape
+    code = _16bit(dtype, codes)
     pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, None if scales else dtype, B, d)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
-    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous() \
-            or out.get_device() != dev:
-        raise ValueError("out must be contiguous, on q's device, and match q")
+    else:
+        _result(out, shape, dtype, dev, "out")
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    elif lse.shape != (B, H) or lse.dtype != torch.float32 or not lse.is_contiguous() \
-            or lse.get_device() != dev:
-        raise ValueError("lse must be contiguous fp32 (B, H) on q's device")
+        lse = torch.empty((B, H), dtype=f32, device=q.device)
+    else:
+        _result(lse, (B, H), f32, dev, "lse")
     lib = load_library()
-    st = _with_workspace(
-        dev, workspace, decode_paged_workspace_size(H, Hkv, d) if workspace is None else 0,
-        lib.fa_decode_paged_fp8 if scales else lib.fa_decode_paged,
-        (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
-        (B, H, Hkv, d, window, 1.0 / math.sqrt(d) if scale is None else scale) + scales
-        + (_dtype_code(q),))
+    st = _call_ws(dev, workspace,
+                  decode_paged_workspace_size(H, Hkv, d) if workspace is None else 0,
+                  lib.fa_decode_paged_fp8 if scales else lib.fa_decode_paged,
+                  (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
+                  (B, H, Hkv, d, window, 1.0 / math.sqrt(d) if scale is None else scale, *scales,
+                   code))
     if st:
         _check(st, "fa_decode_paged_fp8" if scales else "fa_decode_paged")
     return out, lse
@@ -725,34 +747,29 @@ def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_se
     of those the last ``window``.  max_seqlen bounds every nq.  L is (H, total) fp32; a row
     without keys gets O = 0, L = -inf.  ``workspace``: an optional CUDA tensor of at least
     ``fwd_paged_workspace_size`` bytes; calls that may overlap need one each."""
-    import torch
+    torch, i32, f32, codes, _, _ = _paged_env()
     dev = _one_device(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous (total, H, d) tensor")
     total, H, d = shape
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 \
-            or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor of B+1 offsets")
-    B = cu_seqlens.numel() - 1
+    code = _16bit(dtype, codes)
+    B = _offsets(cu_seqlens, i32)
     window = _window(causal, window)
     pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B, d)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
-    elif out.shape != shape or out.dtype != dtype or not out.is_contiguous() \
-            or out.get_device() != dev:
-        raise ValueError("out must be contiguous, on q's device, and match q")
+    else:
+        _result(out, shape, dtype, dev, "out")
     if lse is None:
-        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
-    elif lse.shape != (H, total) or lse.dtype != torch.float32 or not lse.is_contiguous() \
-            or lse.get_device() != dev:
-        raise ValueError("lse must be contiguous fp32 (H, total) on q's device")
+        lse = torch.empty((H, total), dtype=f32, device=q.device)
+    else:
+        _result(lse, (H, total), f32, dev, "lse")
     need = fwd_paged_workspace_size(B, max_seqlen, H, Hkv, d) if workspace is None else 0
-    st = _with_workspace(
-        dev, workspace, need, load_library().fa_fwd_paged,
-        (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
-        (cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d, int(causal), window,
-         1.0 / math.sqrt(d) if scale is None else scale, _dtype_code(q)))
+    st = _call_ws(dev, workspace, need, load_library().fa_fwd_paged,
+                  (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
+                  (cu_seqlens.data_ptr(), B, total, max_seqlen, H, Hkv, d, int(causal), window,
+                   1.0 / math.sqrt(d) if scale is None else scale, code))
     if st:
         _check(st, "fa_fwd_paged")
     return out, lse
