@@ -43,6 +43,10 @@ constexpr int BN = 128;       // keys per K/V tile
 constexpr int NT = 2;         // Q tiles per CTA
 constexpr int THREADS = 384;
 constexpr float RESCALE_LOG2 = 8.0f;   // the running maximum moves in steps of 2^8 or more
+// P is formed with 2^7 times its weight where it is f16 (p <= 2^15), so that the small p of a
+// long context, which add up, stay clear of f16's subnormals; l carries the same factor.
+template <bool BF16>
+constexpr float P_LOG2 = BF16 ? 0.f : 7.f;
 constexpr int kMaskSlots = 8;         // ring of 128-bit key masks, one per KV tile
 
 template <int D>
@@ -215,7 +219,10 @@ __device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row,
 // Masks a row's scores with the keys kbase .. kbase + BN - 1: those outside [lo, lim) and those
 // of absent pages (slot: the tile's mask in the ring).  One block for all of them, entered for
 // few tiles: separate ones cost the unmasked tiles more (1 x 8192, 32 heads, d = 128: 393
-// against 371 us).
+// against 371 us).  At d <= 64 words of 32 keys that are whole are skipped, which most of a
+// diagonal tile's are (ragged prompts, window 512: 38.4 against 36.4 us); the branches cost
+// the d = 128 kernel more than they save (2 x 2048 tokens: 350 against 355 us).
+template <bool WORDS>
 __device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_t slot,
                                             uint32_t (&s)[BN]) {
   uint32_t w[4];
@@ -231,8 +238,12 @@ __device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_
     if (lo > 0) w[i] &= lo < 32 ? ~0u << lo : 0u;
   }
 #pragma unroll
-  for (int c = 0; c < BN; ++c)
-    if (!((w[c / 32] >> (c % 32)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+  for (int i = 0; i < 4; ++i) {
+    if (WORDS && w[i] == ~0u) continue;
+#pragma unroll
+    for (int c = 32 * i; c < 32 * i + 32; ++c)
+      if (!((w[i] >> (c % 32)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+  }
 }
 // Clears row r of a V tile (all its columns, so the swizzle does not matter).
 template <int D>
@@ -493,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
       tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
       const int kbase = (lo_t[t] + j) * BN;
-      paged_masks(rk, kbase, sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, sr);
+      paged_masks<false>(rk, kbase, sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, sr);
       if (kbase + BN > Nk) {                     // the last tile's V rows past the keys
         const int jj = lo_t[t] + j - j0;         // stream position
         if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
@@ -507,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float m_use = grow_m ? m_tile : m_run;
       const float alpha = grow_m ? ex2(m_run - m_use) : 1.f;
       const float m_sub = (m_use == -INFINITY) ? 0.f : m_use;
-      const float2 c2 = make_float2(c_log2, c_log2), nm2 = make_float2(-m_sub, -m_sub);
+      const float2 c2 = make_float2(c_log2, c_log2), nm2 = make_float2(P_LOG2<BF16> - m_sub, P_LOG2<BF16> - m_sub);
       float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -582,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (valid)
-        *lse_at(grow) = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+        *lse_at(grow) = none ? -INFINITY : (m_run - P_LOG2<BF16> + log2f(l_run)) * 0.69314718055994531f;
     } else if (nt <= 0 && grow < Nr) {
       empty_row(grow);
     }
@@ -1004,7 +1015,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         tc_fence_before();
         mbar_arrive(bar(B_SFREE));               // S may now receive the next step
         const int kbase = (lo + j) * BN;
-        paged_masks(rk, kbase, sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
+        paged_masks<true>(rk, kbase, sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
         if (kbase + BN > Nk) {                   // the last tile's V rows past the keys
           const int st = g % STAGES;
           if (!(ok = mbar_wait_warp(bar(B_VF(st)), (g / STAGES) & 1, ctl))) break;
@@ -1017,7 +1028,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         const float m_use = grow_m ? m_tile : m_run;
         const float alpha = grow_m ? ex2(m_run - m_use) : 1.f;
         const float m_sub = (m_use == -INFINITY) ? 0.f : m_use;
-        const float2 c2 = make_float2(c_log2, c_log2), nm2 = make_float2(-m_sub, -m_sub);
+        const float2 c2 = make_float2(c_log2, c_log2), nm2 = make_float2(P_LOG2<BF16> - m_sub, P_LOG2<BF16> - m_sub);
         float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // p for keys [32h, 32h + 32) as 16 packed pairs
         auto exp_pairs = [&](int h, uint32_t (&pk)[16]) {
@@ -1116,7 +1127,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       }
       tc_fence_before();                         // O read before the next tile's p_full
       if (valid)
-        *lse_at(grow) = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+        *lse_at(grow) = none ? -INFINITY : (m_run - P_LOG2<BF16> + log2f(l_run)) * 0.69314718055994531f;
       if (shared) {                              // nothing staged
         release();
         continue;

@@ -637,7 +637,7 @@ def test_tables_and_lengths_seen_through_strides():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
-def test_decode_many_small_weights_add_up():
+def test_many_small_weights_add_up():
     """One key far above 100000 others whose weights are about 2^-26 each: together 0.2 % of the
     sum, which f16 weights of at most 1 would lose."""
     fa = fa_()
@@ -652,16 +652,21 @@ def test_decode_many_small_weights_add_up():
         q = torch.full((1, 1, d), 18.0 / d, dtype=t, device="cuda")
         tb = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
         sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+        one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        s = float(q.double().sum())
         if cache == "e4m3":
             kc, vc = (x.to(torch.float8_e4m3fn) for x in (kc, vc))
-            o, _ = fa.decode_paged_fp8(q, kc, vc, tb, sl, 1.0, 1.0, scale=1.0)
+            got = [fa.decode_paged_fp8(q, kc, vc, tb, sl, 1.0, 1.0, scale=1.0)]
         else:
-            o, _ = fa.decode_paged(q, kc, vc, tb, sl, scale=1.0)
+            got = [fa.decode_paged(q, kc, vc, tb, sl, scale=1.0),
+                   fa.fwd_paged(q, kc, vc, tb, sl, one, 1, scale=1.0)]
         ok()
-        s = float(q.double().sum())
         want = (n - 64) / (math.exp(s) + n - 1)
         # the output's rounding, and each weight's: 2^-26 2^7 is f16's 2^-19, a multiple of 2^-24
-        assert abs(float(o[0, 0, 0]) / want - 1) <= 2.0 ** -11 + 2.0 ** -10
+        for o, lse in got:
+            assert abs(float(o[0, 0, 0]) / want - 1) <= 2.0 ** -11 + 2.0 ** -10
+            # the sum of 10^5 weights in fp32, and L's own roundings
+            assert abs(float(lse.view(-1)[0]) - math.log(math.exp(s) + n - 1)) <= 1e-5
 
 
 def test_calls_on_two_streams():
