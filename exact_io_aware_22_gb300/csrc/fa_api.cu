@@ -972,16 +972,9 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   if ((st = make_map_paged(&a.tmK, c.K, c, Hkv, d, type, elem, 1u << lg)) != FA_OK) return st;
   if ((st = make_map_paged(&a.tmV, c.V, c, Hkv, d, type, elem, 1u << lg)) != FA_OK) return st;
   if ((st = ctl_for_launch(&a.ctl)) != FA_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void* ws = workspace;
-  if (!ws) {
-    cudaError_t e = cudaMallocAsync(&ws, need, s);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
   a.Q = Q;
   a.O = O;
   a.L = L;
-  a.ws = ws;
   a.B = B;
   a.H = H;
   a.Hkv = Hkv;
@@ -989,9 +982,16 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   a.box_log2 = lg;
   a.c_log2 = c_log2;
   a.o_scale = c8 ? v_scale : 1.f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool owned = !workspace && fa::decode_paged_cuts_rows(a, d, c8);
+  a.ws = workspace;
+  if (owned) {
+    cudaError_t e = cudaMallocAsync(&a.ws, need, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   cudaError_t e = fa::launch_decode_paged(a, d, dtype == FA_BF16, c8, s);
-  if (!workspace) {
-    cudaError_t e2 = cudaFreeAsync(ws, s);
+  if (owned) {
+    cudaError_t e2 = cudaFreeAsync(a.ws, s);
     if (e == cudaSuccess) e = e2;
   }
   if (e == cudaErrorInvalidConfiguration) return FA_ERR_UNSUPPORTED;

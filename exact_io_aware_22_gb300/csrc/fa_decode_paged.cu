@@ -886,22 +886,32 @@ bool rows_direct(long long units, long long rows, int slots) {
   return units <= 8 || (units <= 16 && rows >= 152) || (units <= 32 && rows >= 2 * slots);
 }
 
+// Ranges of a call, and whether they are its rows.
+struct Plan {
+  long long ranges;
+  bool direct;
+};
+Plan plan(const DecodePagedArgs& a, int d, bool c8, int nt) {
+  const long long cap = static_cast<long long>(a.pg.max_pages) * a.pg.page.div;
+  const long long longest = a.window > 0 && a.window < cap ? a.window : cap;
+  const long long cost = decode_paged_cost(a.Hkv, d, c8, longest), rows = 1LL * a.B * a.Hkv;
+  const int n_rg = (a.H / a.Hkv + 8 * nt - 1) / (8 * nt);
+  if (rows_direct((cost / a.Hkv - 1) / 2, rows * n_rg, grid_of(nt))) return {rows, true};
+  // at least two positions per range, ranges no more than run at once
+  const long long most = a.B * cost / 2, fit = grid_of(nt) / n_rg;
+  return {most < fit ? (most > 1 ? most : 1) : fit, false};
+}
+
 template <int D, bool BF16, bool C8, int NT>
 cudaError_t launch_t(const DecodePagedArgs& a, cudaStream_t st) {
   auto kern = decode_paged_kernel<D, BF16, C8, NT>;
   constexpr int smem = smem_bytes<D, C8, NT>();
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const long long cap = static_cast<long long>(a.pg.max_pages) * a.pg.page.div;
-  const long long longest = a.window > 0 && a.window < cap ? a.window : cap;
-  const long long cost = decode_paged_cost(a.Hkv, D, C8, longest), most = a.B * cost / 2;
+  const Plan pl = plan(a, D, C8, NT);
   const int n_rg = (a.H / a.Hkv + 8 * NT - 1) / (8 * NT);
-  const bool direct = rows_direct((cost / a.Hkv - 1) / 2,
-                                  static_cast<long long>(a.B) * a.Hkv * n_rg, grid_of(NT));
-  // at least two positions per range, ranges no more than run at once
-  const long long fit = grid_of(NT) / n_rg;
-  const long long ranges = direct ? static_cast<long long>(a.B) * a.Hkv
-                                  : most < fit ? (most > 1 ? most : 1) : fit;
+  const long long ranges = pl.ranges;
+  const bool direct = pl.direct;
   if (ranges * n_rg > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(ranges * n_rg);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
@@ -937,6 +947,10 @@ long long decode_paged_cost(int Hkv, int d, bool c8, long long n) {
 bool decode_paged_group_fits(int H, int Hkv) {
   const int nt = n_blocks(H, Hkv);
   return (H / Hkv + 8 * nt - 1) / (8 * nt) <= grid_of(nt);
+}
+
+bool decode_paged_cuts_rows(const DecodePagedArgs& a, int d, bool c8) {
+  return !plan(a, d, c8, n_blocks(a.H, a.Hkv)).direct;
 }
 
 size_t decode_paged_ws_bytes(int H, int Hkv, int d) {

@@ -213,6 +213,8 @@ long long decode_paged_cost(int Hkv, int d, bool c8, long long n);
 // Whether a group of H / Hkv heads fits the grid.
 bool decode_paged_group_fits(int H, int Hkv);
 size_t decode_paged_ws_bytes(int H, int Hkv, int d);
+// Whether a call's ranges may cut rows, so that it touches its workspace.
+bool decode_paged_cuts_rows(const DecodePagedArgs& a, int d, bool c8);
 cudaError_t launch_decode_paged(const DecodePagedArgs& a, int d, bool bf16, bool c8,
                                 cudaStream_t st);
 

@@ -314,7 +314,9 @@ fa_status fa_append_paged_fp8(const fa_paged_cache* cache, const void* K, long l
  *   Q (B, H, d), O (B, H, d), L (B, H) as in fa_decode; a row without attended keys gets
  *   O = 0, L = -inf.
  *   workspace    fa_decode_paged_workspace_size(H, Hkv, d) bytes (16-byte aligned), or NULL:
- *                allocated and freed on `stream`.  Its contents do not matter before a call.
+ *                allocated and freed on `stream` if the call cuts rows (it does not where the
+ *                table or the window keeps every row short).  Its contents do not matter
+ *                before a call.
  *   Errors: as for the cache and fa_decode, FA_ERR_INVALID_VALUE for window < 0 or a scale
  *   that (times k_scale) overflows or vanishes in fp32, and
  *   FA_ERR_UNSUPPORTED for more than 4864 query heads per K/V head. */

@@ -669,6 +669,29 @@ def test_many_small_weights_add_up():
             assert abs(float(lse.view(-1)[0]) - math.log(math.exp(s) + n - 1)) <= 1e-5
 
 
+@pytest.mark.parametrize("n", [100, 5000])
+def test_c_calls_that_allocate_their_workspace(n):
+    """The C entry points with workspace NULL, where rows get a CTA each and where they are cut,
+    against the Python calls."""
+    fa = fa_()
+    lib = fa.load_library()
+    pool = pu.Pool((n, n // 2), 2, 64, 16, "fp16")
+    kc, vc, tb, sl = pool.cuda()
+    q = torch.randn(2, 8, 64, device="cuda").half()
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    pc, _ = fa._paged(kc, vc, tb, sl, torch.float16, 2, 64)
+    o, lse, o2, lse2 = (torch.empty_like(q), torch.empty(2, 8, device="cuda"), torch.empty_like(q),
+                        torch.empty(8, 2, device="cuda"))
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.fa_decode_paged(q.data_ptr(), pc, o.data_ptr(), lse.data_ptr(), None, 0, 2, 8, 2, 64, 0,
+                               0.125, 0, st) == 0
+    assert lib.fa_fwd_paged(q.data_ptr(), pc, o2.data_ptr(), lse2.data_ptr(), None, 0, cu.data_ptr(),
+                            2, 2, 1, 8, 2, 64, 1, 0, 0.125, 0, st) == 0
+    want = fa.decode_paged(q, kc, vc, tb, sl) + fa.fwd_paged(q, kc, vc, tb, sl, cu, 1)
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip((o, lse, o2, lse2), want))
+
+
 def test_calls_on_two_streams():
     fa = fa_()
     pool = pu.Pool((3000, 2000), 2, 128, 64, "bf16")
