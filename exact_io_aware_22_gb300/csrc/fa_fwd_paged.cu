@@ -25,8 +25,8 @@
 //              2^(L_s - L).
 //
 // Bound: at d = 128 the tensor pipe and the exponentials (2 x 2048 tokens on 8192 keys, 32/8
-// heads: 0.343 ms, 1391 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
-// slots; with few tokens the latency of start, split and join (the 5 tokens above: 16.7 us for
+// heads: 0.342 ms, 1394 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
+// slots; with few tokens the latency of start, split and join (the 5 tokens above: 17.3 us for
 // 34 MB of keys).
 //
 // The kernels stand apart from fa_fwd.cu's although the pipelines are alike: pages, packed heads
@@ -216,20 +216,24 @@ __device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row,
   r.past = ((row0 + BM - 1) >> pack) + k.off - window + 1;
   return r;
 }
+// A KV tile's mask in the ring, a bit per key whose page is there.  The d = 128 kernel reads it
+// before it waits for the scores (2 x 2048 tokens: 350 against 345 us); at d <= 64 the order
+// made no difference.
+__device__ __forceinline__ void load_mask(uint32_t slot, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(slot)
+               : "memory");
+}
 // Masks a row's scores with the keys kbase .. kbase + BN - 1: those outside [lo, lim) and those
-// of absent pages (slot: the tile's mask in the ring).  One block for all of them, entered for
+// of absent pages (w).  One block for all of them, entered for
 // few tiles: separate ones cost the unmasked tiles more (1 x 8192, 32 heads, d = 128: 393
 // against 371 us).  At d <= 64 words of 32 keys that are whole are skipped, which most of a
 // diagonal tile's are (ragged prompts, window 512: 38.4 against 36.4 us); the branches cost
 // the d = 128 kernel more than they save (2 x 2048 tokens: 350 against 355 us).
 template <bool WORDS>
-__device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_t slot,
+__device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_t (&w)[4],
                                             uint32_t (&s)[BN]) {
-  uint32_t w[4];
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(slot)
-               : "memory");
   if (kbase + BN <= r.full && kbase >= r.past && (w[0] & w[1] & w[2] & w[3]) == ~0u) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -494,7 +498,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int j = 0; j < nt; ++j) {
       if (!(ok = mbar_wait_warp(bar(B_SF(t)), j & 1, ctl))) break;
       tc_fence_after();
-      uint32_t sr[BN];
+      uint32_t mask[4], sr[BN];
+      load_mask(sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, mask);
       tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
       tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
       tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
       const int kbase = (lo_t[t] + j) * BN;
-      paged_masks<false>(rk, kbase, sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, sr);
+      paged_masks<false>(rk, kbase, mask, sr);
       if (kbase + BN > Nk) {                     // the last tile's V rows past the keys
         const int jj = lo_t[t] + j - j0;         // stream position
         if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
@@ -1015,7 +1020,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         tc_fence_before();
         mbar_arrive(bar(B_SFREE));               // S may now receive the next step
         const int kbase = (lo + j) * BN;
-        paged_masks<true>(rk, kbase, sb + C1::MASK_OFF + (g % kMaskSlots) * 16, sr_);
+        uint32_t mask[4];
+        load_mask(sb + C1::MASK_OFF + (g % kMaskSlots) * 16, mask);
+        paged_masks<true>(rk, kbase, mask, sr_);
         if (kbase + BN > Nk) {                   // the last tile's V rows past the keys
           const int st = g % STAGES;
           if (!(ok = mbar_wait_warp(bar(B_VF(st)), (g / STAGES) & 1, ctl))) break;
