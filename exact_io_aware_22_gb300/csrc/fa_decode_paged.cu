@@ -471,7 +471,9 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
             const float2 f = unpack2<true>(qw[nt][ks][e]);
             qf[nt][ks][e] = pack2<false>(f.x * dn, f.y * dn);
           }
-        const float up = __uint_as_float(eb) * c_log2;          // lane 4h holds head h's
+        // lane 4h holds head h's; never 0, which would make a masked score NaN (the least
+        // normal number in its place moves no score by 2^-100)
+        const float up = fmaxf(__uint_as_float(eb) * c_log2, 0x1p-126f);
         cs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
         cs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
       } else {

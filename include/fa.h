@@ -319,7 +319,8 @@ fa_status fa_append_paged_fp8(const fa_paged_cache* cache, const void* K, long l
  *                before a call.
  *   Errors: as for the cache and fa_decode, FA_ERR_INVALID_VALUE for window < 0 or a scale
  *   that (times k_scale) overflows or vanishes in fp32, and
- *   FA_ERR_UNSUPPORTED for more than 4864 query heads per K/V head. */
+ *   FA_ERR_UNSUPPORTED for more than 4864 query heads per K/V head or for a table whose rows
+ *   have room for about 2^44 bytes of keys together. */
 size_t fa_decode_paged_workspace_size(int H, int Hkv, int d);
 fa_status fa_decode_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
                           void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int d,

@@ -143,6 +143,11 @@ def test_decode_fp8_tiny_and_huge_queries():
     run_decode((200,), 8, 2, 128, "bf16", 32, "e4m3", scale=2.0 ** 20, qmul=2.0 ** -20)
 
 
+def test_decode_fp8_scores_that_underflow():
+    # scale * log2(e) times the queries' exponent is below fp32's least number: all scores are 0
+    run_decode((70, 33, 500), 8, 2, 128, "bf16", 32, "e4m3", scale=1e-8, qmul=1e-38)
+
+
 def test_decode_attended_nan_and_inf_propagate():
     fa = fa_()
     pool = pu.Pool((100, 100, 100), 2, 64, 16, "bf16")
