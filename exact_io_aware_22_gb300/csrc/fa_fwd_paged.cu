@@ -103,7 +103,7 @@ __device__ __forceinline__ void rows_of(const PagedArgs& px, const int* cu, int 
   sr = {a, min(e - a, N), true};
   const long long cap = static_cast<long long>(px.pg.max_pages) * px.pg.page.div;
   k.n = static_cast<int>(min(static_cast<long long>(max(len, 0)), cap));
-  k.off = k.n - sr.n;
+  k.off = k.n - (e - a);                         // rows past N are left out, the others stay
   k.hi = px.causal ? k.off : kNoLimit;
 }
 // KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of a sequence's nr; row i is

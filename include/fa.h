@@ -338,7 +338,8 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
  * rows and nk = cache_seqlens[b] keys, causal query i sees keys j <= nk - nq + i, and with
  * window > 0 of those the last `window`; not causal: all nk keys.
  *   Layout   Q, O (total, H, d); L (H, total) as in fa_fwd_varlen; cu_seqlens, total and
- *            max_seqlen too (offsets that break its rules leave rows uncomputed).  Rows of no
+ *            max_seqlen too (offsets that break its rules leave rows uncomputed: of a sequence
+ *            longer than max_seqlen those past it).  Rows of no
  *            sequence are left as they were.  A row without keys gets O = 0, L = -inf.
  *   workspace  fa_fwd_paged_workspace_size(B, max_seqlen, H, Hkv, d) bytes (16-byte
  *            aligned), or NULL: allocated and freed on `stream`.  0 bytes, and then unused,

@@ -464,6 +464,28 @@ def test_fwd_offsets_that_break_the_rules_touch_nothing_outside():
     ok()
 
 
+@pytest.mark.parametrize("d,dtype,H,B", [(128, "bf16", 8, 2), (64, "fp16", 8, 2), (128, "fp16", 8, 80)])
+def test_fwd_sequences_longer_than_max_seqlen(d, dtype, H, B):
+    # the rows up to max_seqlen get what they would get without it, the others are left alone
+    fa = fa_()
+    lens, new, most = [500, 90] + [40] * (B - 2), [200, 90] + [30] * (B - 2), 70
+    pool = pu.Pool(lens, 2, d, 16, dtype)
+    kc, vc, tb, sl = pool.cuda()
+    cu = torch.tensor([0] + new).cumsum(0)
+    total, t = int(cu[-1]), pu.DT[dtype]
+    q = torch.randn((total, H, d), generator=torch.Generator().manual_seed(B)).to(t)
+    o = torch.full((total, H, d), 7.0, dtype=t, device="cuda")
+    lse = torch.full((H, total), 7.0, device="cuda")
+    fa.fwd_paged(q.cuda(), kc, vc, tb, sl, cu.int().cuda(), most, out=o, lse=lse)
+    ok()
+    for b in range(B):
+        m, c = min(new[b], most), int(cu[b])
+        at = torch.arange(lens[b] - new[b], lens[b] - new[b] + m)
+        ref = pu.reference(pool, q[c:c + m], b, at, 1 / math.sqrt(d))
+        pu.check_rows(o[c:c + m], lse[:, c:c + m].t(), ref, t, p_half=pu.HALF[t])
+        assert (o[c + m:c + new[b]] == 7).all() and (lse[:, c + m:c + new[b]] == 7).all()
+
+
 def test_fwd_repeats_and_replays_bit_for_bit():
     fa = fa_()
     # 333 rows: tiles enough at 128 heads, keys split at 4
