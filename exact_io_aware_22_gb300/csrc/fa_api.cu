@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -998,12 +999,6 @@ fa_status decode_paged_impl(const void* Q, const fa_paged_cache* cache, void* O,
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-// Bytes of fa_fwd_paged's workspace: each range's O and L of every (query, head), in fp32.
-size_t fwd_paged_ws(int splits, int B, int max_seqlen, int H, int d) {
-  return splits > 1 ? static_cast<size_t>(splits) * B * max_seqlen * H * (d + 1) * sizeof(float)
-                    : 0;
-}
-
 fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, float* L,
                          void* workspace, size_t workspace_bytes, const int* cu_seqlens, int B,
                          int total, int max_seqlen, int H, int Hkv, int d, int causal, int window,
@@ -1016,30 +1011,32 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   const float c_log2 = scale * 1.4426950408889634f;
   if (!(std::isfinite(c_log2) && c_log2 > 0.f)) return FA_ERR_INVALID_VALUE;
   const int pack = fa::fwd_paged_pack(H / Hkv);
-  if (static_cast<long long>(max_seqlen) << pack > (1 << 29) || B > 65535)
-    return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_seqlen) << pack > (1 << 29)) return FA_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(L, 4) || (workspace && !aligned(workspace, 16)))
     return FA_ERR_MISALIGNED;
-  const int splits = fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d);
-  const size_t need = fwd_paged_ws(splits, B, max_seqlen, H, d);
-  if (need && workspace && workspace_bytes < need) return FA_ERR_INVALID_VALUE;
+  const fa::FwdPagedPlan pl = fa::fwd_paged_plan(B, H, Hkv, max_seqlen, d);
+  if (pl.tiles > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const bool ws_in = pl.ws_bytes && workspace;
+  if (ws_in && workspace_bytes < pl.ws_bytes) return FA_ERR_INVALID_VALUE;
   fa::FwdArgs a;
   std::memset(&a, 0, sizeof(a));
   if ((st = check_paged(cache, Hkv, d, 2, &a.pg)) != FA_OK) return st;
   const fa_paged_cache c = used_strides(*cache, Hkv, d);
+  const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
+  const long long span = window > 0 ? std::min<long long>(cap, 256LL + max_seqlen + window) : cap;
+  const bool cut = fa::fwd_paged_may_cut(pl, span);
   const size_t qb = static_cast<size_t>(total) * H * d * 2, lb = static_cast<size_t>(total) * H * 4;
   const size_t pb = pool_bytes(c, Hkv, d, 2);
   const void* ins[6] = {Q, c.K, c.V, c.page_table, c.cache_seqlens, cu_seqlens};
   const size_t insz[6] = {qb, pb, pb,
                           static_cast<size_t>((B - 1) * c.table_stride + c.max_pages) * 4,
                           static_cast<size_t>(B) * 4, (static_cast<size_t>(B) + 1) * 4};
-  const bool ws_in = need && workspace;
   for (int j = 0; j < 6; ++j)
     if (overlap(O, qb, ins[j], insz[j]) || overlap(L, lb, ins[j], insz[j]) ||
-        (ws_in && overlap(workspace, need, ins[j], insz[j])))
+        (ws_in && overlap(workspace, pl.ws_bytes, ins[j], insz[j])))
       return FA_ERR_INVALID_VALUE;
   if (overlap(O, qb, L, lb)) return FA_ERR_INVALID_VALUE;
-  if (ws_in && (overlap(workspace, need, O, qb) || overlap(workspace, need, L, lb)))
+  if (ws_in && (overlap(workspace, pl.ws_bytes, O, qb) || overlap(workspace, pl.ws_bytes, L, lb)))
     return FA_ERR_INVALID_VALUE;
   const bool bf16 = dtype == FA_BF16;
   const int lg = box_rows_log2(c.page_size, 128);
@@ -1060,18 +1057,18 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   a.box_log2 = lg;
   a.B = B;
   a.pack = pack;
-  a.n_split = splits;
+  a.ranges = cut ? pl.ranges : 0;
   a.c_log2 = c_log2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = workspace;
-  if (need && !ws) {
-    cudaError_t e = cudaMallocAsync(&ws, need, s);
+  const bool owned = cut && !ws;
+  if (owned) {
+    cudaError_t e = cudaMallocAsync(&ws, pl.ws_bytes, s);
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  a.part = static_cast<float*>(ws);
-  a.part_l = a.part + static_cast<size_t>(splits) * B * max_seqlen * H * d;
+  a.ws = ws;
   cudaError_t e = fa::launch_fwd_paged(a, d, bf16, causal != 0, s);
-  if (need && !workspace) {
+  if (owned) {
     cudaError_t e2 = cudaFreeAsync(ws, s);
     if (e == cudaSuccess) e = e2;
   }
@@ -1131,7 +1128,7 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
 size_t fa_fwd_paged_workspace_size(int B, int max_seqlen, int H, int Hkv, int d) {
   if (check_common(B, H, max_seqlen, d, 1, 1.f, FA_FP16) != FA_OK || check_heads(H, Hkv) != FA_OK)
     return 0;
-  return fwd_paged_ws(fa::fwd_paged_splits(B, H, Hkv, max_seqlen, d), B, max_seqlen, H, d);
+  return fa::fwd_paged_plan(B, H, Hkv, max_seqlen, d).ws_bytes;
 }
 
 fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,

@@ -17,17 +17,21 @@
 //   tiles      A query tile holds the rows of 2^pack heads that share a K/V head, heads fastest:
 //              the tile of a few new tokens is better filled, K and V pass once for those
 //              heads, and less of a tile lies beyond the diagonal (5 tokens of 4 sequences of
-//              2000 keys, 32/8 heads, d = 128: 33.4 against 17.7 us with the split below;
-//              8 prompts of 1000: 110 against 100 us).
-//   split      Where there are fewer query tiles than the GPU runs at once, the KV tiles of
-//              each are cut into ranges of equal length for as many CTAs, whose results, each
-//              normalised with its own L, fwd_paged_merge_kernel joins by their weights
-//              2^(L_s - L).
+//              2000 keys, 32/8 heads, d = 128: 33.4 against 17.7 us with the keys split; 8
+//              prompts of 1000: 110 against 99 us).
+//   ranges     Where there are few query tiles, or uneven ones, the KV tiles of all are laid
+//              end to end and every CTA takes an equal range of them, which may begin and end
+//              inside a query tile.  The lengths lie on the device, so every CTA finds its range
+//              by a scan over the tiles, and decides there whether cutting pays.  A tile cut by
+//              range borders leaves in each of its CTAs a result normalised with its own L, and
+//              fwd_paged_merge_kernel joins these in order, by their weights 2^(L_s - L).  5
+//              tokens of 10 / 16 sequences of 16384-32768 keys: 163 / 252 us (6.2 and 6.4 TB/s);
+//              a CTA for each tile: 355 / 356 us.
 //
 // Bound: at d = 128 the tensor pipe and the exponentials (2 x 2048 tokens on 8192 keys, 32/8
-// heads: 0.342 ms, 1394 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
-// slots; with few tokens the latency of start, split and join (the 5 tokens above: 17.3 us for
-// 34 MB of keys).
+// heads: 0.338 ms, 1413 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
+// slots; with few tokens the latency of start, split and join (the 5 tokens above: 18 us for 34 MB
+// of keys), with few tokens on long caches the cache's bytes.
 //
 // The kernels stand apart from fa_fwd.cu's although the pipelines are alike: pages, packed heads
 // and ranges reach into every role, and the dense kernels' code does not change with them.
@@ -62,11 +66,13 @@ struct Cfg {
   static constexpr int K_OFF = Q_OFF + NT * TILE_BYTES;
   static constexpr int V_OFF = K_OFF + STAGES * TILE_BYTES;
   static constexpr int BAR_OFF = V_OFF + STAGES * TILE_BYTES;
-  // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_full[2], o_full[2], done
-  static constexpr int NBARS = 1 + 4 * STAGES + 7;
+  // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_full[2], o_full[2], done,
+  // q_empty, piece_full[2], piece_empty[2]
+  static constexpr int NBARS = 1 + 4 * STAGES + 7 + 5;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int MASK_OFF = (SLOT_OFF + 16 + 15) / 16 * 16;
-  static constexpr int SMEM_BYTES = MASK_OFF + kMaskSlots * 16 + 1024;   // + alignment slack
+  static constexpr int INFO_OFF = MASK_OFF + kMaskSlots * 16;            // two Pieces
+  static constexpr int SMEM_BYTES = INFO_OFF + 2 * 64 + 1024;            // + alignment slack
   static constexpr int TMEM_COLS = 512;
   static constexpr int S_COL = 0;                           // S_t at t * 128
   static constexpr int O_COL = 256;                         // O_t at 256 + t * D
@@ -80,14 +86,20 @@ __device__ __forceinline__ uint32_t kmajor_koff(int kk) {
   return (e / C::ATOM) * C::CHUNK_BYTES + (e % C::ATOM) * 2;
 }
 
+// The query tile that range x shares with range x - 1: its sequence's first token, its first head,
+// first row and rows (0: there is none), and the first and last range that have parts of it.
+struct RangeHeader {
+  int base, hq, row0, rows, c0, c1;
+};
 struct PagedArgs {
   PagedView pg;
   int box_log2, causal, window;    // window: kNoLimit for none
   int pack;                        // log2 of the heads in a query tile
-  int n_split;                     // KV ranges per query tile (1: no workspace)
-  size_t rows;                     // (query, head) pairs of all sequences: B * max_seqlen * H
-  float* part;                     // [n_split][rows][D] results of the ranges
-  float* part_l;                   // [n_split][rows] their logsumexp (natural log)
+  int B, n_qt;                     // sequences, query tiles of the longest
+  int ranges;                      // CTAs that may share the KV tiles of all query tiles (0: none)
+  RangeHeader* hdr;                // workspace, with ranges: [ranges], then
+  float* part;                     // [2 * ranges][rows of a query tile][D] results of pieces
+  float* part_l;                   // [2 * ranges][rows of a query tile] their L (natural log)
 };
 constexpr int kNoLimit = 1 << 30;
 // Keys of a sequence with nq query rows: query row i is at key position i + off and sees keys
@@ -114,26 +126,204 @@ __device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nr, int
   hi = r >= nr || last < 0 ? 0 : min((k.n + BN - 1) / BN, last / BN + 1);
   lo = min(max(0, (r >> pack) + k.off - window + 1) / BN, hi);
 }
-// How the KV tiles [lo, hi) of `TILES` query tiles from row r are cut: ranges of `per` tiles,
-// `used` of them (at least one).
-struct SplitRange {
-  int lo, hi, per, used;
+// KV tiles [lo, hi) of a query tile of TILES * BM rows from row r.
+struct Span {
+  int lo, hi;
 };
 template <int TILES>
-__device__ __forceinline__ SplitRange split_range(const KeyRows& k, int r, int nr, int window,
-                                                  int pack, int n_split) {
-  SplitRange s;
-  paged_tiles(k, r, nr, window, pack, s.lo, s.hi);
+__device__ __forceinline__ Span tile_span(const PagedArgs& px, const KeyRows& k, int r, int nr) {
+  Span s;
+  paged_tiles(k, r, nr, px.window, px.pack, s.lo, s.hi);
 #pragma unroll
   for (int t = 1; t < TILES; ++t) {
     int lo, hi;
-    paged_tiles(k, r + t * BM, nr, window, pack, lo, hi);
+    paged_tiles(k, r + t * BM, nr, px.window, px.pack, lo, hi);
     if (hi > s.hi) s.hi = hi;                    // lo rises with the row
   }
-  // two tiles at least: the join costs about as much as one
-  s.per = max((s.hi - s.lo + n_split - 1) / n_split, n_split > 1 ? 2 : 1);
-  s.used = max((s.hi - s.lo + s.per - 1) / s.per, 1);
   return s;
+}
+// Positions of a query tile of n KV tiles on the line that ranges are cut from: beginning and
+// ending a piece takes about as long as kTileCost KV tiles (1, 2 and 4 differ by up to 2 %, but
+// 4, of which a range has at least twice as much, leaves 4 x 5 tokens on 2000 keys at 25 us
+// instead of 18).  KV tile i is at position kTileCost + i.
+constexpr int kTileCost = 2;
+// What cutting costs a call, in KV tiles, besides moving the rows that are cut: 16 rows take
+// about as long as one.  5 tokens of 16 sequences, whole / cut: 500-2000 keys 31 / 33.5 us,
+// 4096-8192 keys 94 / 79; 8 x 128 tokens on 8192 keys 106 / 129.
+constexpr int kJoinCost = 8;
+__device__ __forceinline__ int tile_cost(const Span& s) {
+  return s.hi > s.lo ? s.hi - s.lo + kTileCost : 0;
+}
+
+// A piece of work: KV tiles [j0, j1) of the query tile of one block of packed heads at rows
+// row0 .. of a sequence.
+struct Piece {
+  int base, nr;                                  // the sequence's first token and query rows
+  KeyRows kr;
+  int hq, hk, row0, j0, j1;                      // first head, its K/V head, first row
+  int part;                                      // place in the workspace, -1: the tile is whole
+};
+// The pieces of one CTA, found by one warp.
+template <int TILES>
+struct Work {
+  static constexpr int ROWS = TILES * BM;
+  int b, qt, blk;                                // the current query tile
+  SeqRows sr;
+  KeyRows kr;
+  Span span;
+  int u, ue;                                     // its KV tiles of this CTA, from span.lo
+  int left;                                      // positions of the range after them
+
+  // The whole of query tile `id`, in the order of block_pos; nothing past the last one.
+  __device__ __forceinline__ void whole(const PagedArgs& px, const int* cu, int N, int H, int total,
+                                        int id) {
+    const int blocks = H >> px.pack, heads = px.B * blocks;
+    b = blk = qt = u = ue = left = 0;
+    sr = {0, 0, true};
+    kr = {0, 0, 0};
+    span = {0, 0};
+    if (id >= heads * px.n_qt) return;
+    const int g0 = id / (8 * px.n_qt) * 8, gsz = min(8, heads - g0), w = id - g0 * px.n_qt;
+    const int bh = g0 + w % gsz;
+    b = bh / blocks;
+    blk = bh % blocks;
+    qt = px.n_qt - 1 - w / gsz;                  // the last query tiles have the most work
+    rows_of(px, cu, b, N, total, sr, kr);
+    span = tile_span<TILES>(px, kr, qt * ROWS, sr.n << px.pack);
+    ue = max(span.hi - span.lo, 0);
+  }
+  // To this CTA's first piece, where the work may be cut; false: there is none.  `cut` tells
+  // whether it is: then the CTA has range blockIdx.x of px.ranges equal ones of all query
+  // tiles' KV tiles, laid end to end (sequences, their query tiles, blocks of heads).
+  __device__ __forceinline__ bool first(const PagedArgs& px, const int* cu, int N, int H, int total,
+                                        bool& cut) {
+    const int lane = threadIdx.x & 31, blocks = H >> px.pack, cta = static_cast<int>(blockIdx.x);
+    auto cost = [&](int i) -> int {              // of query tile i of all sequences, every block
+      SeqRows r;
+      KeyRows k;
+      rows_of(px, cu, i / px.n_qt, N, total, r, k);
+      return tile_cost(tile_span<TILES>(px, k, i % px.n_qt * ROWS, r.n << px.pack)) * blocks;
+    };
+    const int n_i = px.B * px.n_qt, per = (n_i + 31) / 32;   // query tiles per lane
+    int mine = 0, most = 0;
+    for (int i = lane * per; i < min(lane * per + per, n_i); ++i) {
+      const int c = cost(i);
+      mine += c;
+      most = max(most, c);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int w = 1; w < 32; w *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, w);
+      if (lane >= w) incl += o;
+    }
+    const int sum = __shfl_sync(0xffffffffu, incl, 31);
+    // What cutting saves: whole tiles take as long as the longest, or where there are more of
+    // them than CTAs, end about half of it apart.  What it costs: the join, and more the more
+    // rows it has to move.
+    most = __reduce_max_sync(0xffffffffu, most) / blocks;
+    const int saves = n_i * blocks <= px.ranges ? most - sum / px.ranges : most / 2;
+    cut = saves > kJoinCost + min(N << px.pack, ROWS) / 16;
+    if (!cut) {
+      if (lane == 0 && cta < px.ranges) px.hdr[cta].rows = 0;
+      whole(px, cu, N, H, total, cta);
+      return cta < n_i * blocks;
+    }
+    if (cta >= px.ranges) return false;
+    const int per_cta = max((sum - 1) / px.ranges + 1, 2 * kTileCost);
+    const int x0 = static_cast<int>(min(static_cast<long long>(cta) * per_cta,
+                                        static_cast<long long>(sum)));
+    const int x1 = x0 + min(per_cta, sum - x0);
+    RangeHeader h = {};
+    if (x0 < x1) {
+      const bool here = incl > x0 && incl - mine <= x0;            // one lane has position x0
+      int at = incl - mine, i = lane * per;
+      if (here)
+        for (int c; at + (c = cost(i)) <= x0; ++i) at += c;
+      const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      i = __shfl_sync(0xffffffffu, i, src);
+      at = __shfl_sync(0xffffffffu, at, src);
+      b = i / px.n_qt;
+      qt = i % px.n_qt;
+      rows_of(px, cu, b, N, total, sr, kr);
+      span = tile_span<TILES>(px, kr, qt * ROWS, sr.n << px.pack);
+      const int c = tile_cost(span);
+      blk = (x0 - at) / c;
+      at += blk * c;                             // the query tile's first position
+      const int off = x0 - at, take = min(c - off, x1 - x0);
+      u = max(off - kTileCost, 0);
+      ue = max(off + take - kTileCost, 0);
+      left = x1 - x0 - take;
+      if (u > 0 && u < ue)                       // its first KV tile lies in an earlier range
+        h = {sr.base, blk << px.pack, qt * ROWS, min(ROWS, (sr.n << px.pack) - qt * ROWS),
+             (at + kTileCost) / per_cta, (at + c - 1) / per_cta};
+    }
+    if (lane == 0) px.hdr[cta] = h;
+    return x0 < x1 && (u < ue || next(px, cu, N, H, total));
+  }
+  // To the next piece.
+  __device__ __forceinline__ bool next(const PagedArgs& px, const int* cu, int N, int H,
+                                       int total) {
+    do {
+      if (left <= 0) return false;
+      if (++blk == H >> px.pack) {
+        blk = 0;
+        do {
+          if ((++qt) * ROWS >= sr.n << px.pack) {
+            qt = 0;
+            if (++b >= px.B) return false;       // not reached: `left` counts existing tiles
+            rows_of(px, cu, b, N, total, sr, kr);
+          }
+          span = tile_span<TILES>(px, kr, qt * ROWS, sr.n << px.pack);
+        } while (span.hi <= span.lo);
+      }
+      const int take = min(tile_cost(span), left);
+      u = 0;
+      ue = max(take - kTileCost, 0);
+      left -= take;
+    } while (ue == 0);
+    return true;
+  }
+  __device__ __forceinline__ Piece piece(const PagedArgs& px, int group) const {
+    Piece p;
+    p.base = sr.base;
+    p.nr = sr.n << px.pack;
+    p.kr = kr;
+    p.hq = blk << px.pack;
+    p.hk = p.hq / group;
+    p.row0 = qt * ROWS;
+    p.j0 = span.lo + u;
+    p.j1 = span.lo + ue;
+    // a range has at most two pieces of cut tiles: one that it goes on with, one it begins
+    p.part = ue - u == max(span.hi - span.lo, 0) ? -1 : 2 * static_cast<int>(blockIdx.x) + (u == 0);
+    return p;
+  }
+};
+// Rows of query tiles that see no key, which no range has: O = 0, L = -inf.  Thread i of n.
+template <int TILES, int D>
+__device__ __forceinline__ void rows_without_keys(const PagedArgs& px, const int* cu, int N, int H,
+                                                  int total, uint16_t* Out, float* Lout, int i0,
+                                                  int n) {
+  constexpr int ROWS = TILES * BM;
+  const int heads = 1 << px.pack, blocks = H >> px.pack;
+  for (int b = static_cast<int>(blockIdx.x); b < px.B; b += static_cast<int>(gridDim.x)) {
+    SeqRows sr;
+    KeyRows kr;
+    rows_of(px, cu, b, N, total, sr, kr);
+    const int nr = sr.n << px.pack;
+    for (int row0 = 0; row0 < nr; row0 += ROWS) {
+      const Span s = tile_span<TILES>(px, kr, row0, nr);
+      if (s.hi > s.lo) continue;
+      const int rows = min(ROWS, nr - row0);
+      for (int i = i0; i < rows * blocks; i += n) {
+        const int r = row0 + i / blocks, h = i % blocks * heads + (r & (heads - 1));
+        const size_t tok = static_cast<size_t>(sr.base + (r >> px.pack));
+        uint4* dst = reinterpret_cast<uint4*>(Out + (tok * H + h) * D);
+        for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+        Lout[static_cast<size_t>(h) * total + tok] = -INFINITY;
+      }
+    }
+  }
 }
 
 // One warp's loads of 128-key tiles of a paged cache.  Lane i handles boxes i, i + 32, ...
@@ -263,13 +453,16 @@ __device__ __forceinline__ void clear_row(uint32_t tile, int r) {
                    : "memory");
 }
 
-template <int D, bool BF16>
+// RANGES: the CTA may have several pieces of work, which warp 0 finds and hands on; otherwise it
+// has one query tile, found by every thread.  The loop over pieces costs tiles that are not cut
+// 2 to 9 % (8 prompts of 1000 tokens 108 against 99 us, 2 x 2048 on 8192 keys 345 against 338).
+template <int D, bool BF16, bool RANGES>
 __global__ void __launch_bounds__(THREADS, 1)
     fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, void* __restrict__ Out,
-                     float* __restrict__ Lout, int N, int n_qblk, int group, const int* cu_seqlens,
-                     int H, int total, float c_log2, KernelCtl ctl, const PagedArgs px) {
+                     float* __restrict__ Lout, int N, int group, const int* cu_seqlens, int H,
+                     int total, float c_log2, KernelCtl ctl, const PagedArgs px) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -279,56 +472,39 @@ __global__ void __launch_bounds__(THREADS, 1)
   grid_dep_launch();                            // the next kernel may start setting up
   grid_dep_wait();                              // offsets, lengths, table and inputs are written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const BlockPos bp = block_pos(n_qblk);        // bp.bh: (sequence, block of heads, KV range)
-  const int pack = px.pack, blocks = H >> pack;
-  const int split = bp.bh % px.n_split, bh = bp.bh / px.n_split;
-  const int b = bh / blocks;
-  const int hq = (bh % blocks) << pack, hk = hq / group;   // the tile's first head, its K/V head
-  const int qblk = n_qblk - 1 - bp.rank;        // the last query tiles have the most work
-  SeqRows sr;
-  KeyRows kr;
-  rows_of(px, cu_seqlens, b, N, total, sr, kr);
-  const int Nr = sr.n << pack, Nk = kr.n;       // query rows, keys
-  const int row0 = qblk * (NT * BM);
-  // KV tiles [lo_t[t], n_t[t]) of Q tile t, cut to this CTA's range of those of both
-  const SplitRange sp = split_range<NT>(kr, row0, Nr, px.window, pack, px.n_split);
-  if (split >= sp.used) return;
-  const bool shared = sp.used > 1;              // the tile's other ranges are other CTAs'
-  const int j0 = sp.lo + split * sp.per, n_max = min(j0 + sp.per, sp.hi);
-  int n_t[NT], lo_t[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    paged_tiles(kr, row0 + t * BM, Nr, px.window, pack, lo_t[t], n_t[t]);
-    lo_t[t] = min(max(lo_t[t], j0), n_max);
-    n_t[t] = min(max(n_t[t], j0), n_max);
-  }
-  const int n_stream = n_max - j0;              // KV tiles loaded, j0 .. n_max - 1
+  const int pack = px.pack;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  // where row `grow` lies in O, in the workspace, and in L or the workspace's L
-  auto row_at = [&](int grow) -> size_t {
-    return static_cast<size_t>(sr.base + (grow >> pack)) * H + hq + (grow & ((1 << pack) - 1));
-  };
-  auto part_at = [&](int grow) -> size_t {
-    return split * px.rows + (static_cast<size_t>(b) * N + (grow >> pack)) * H + hq +
-           (grow & ((1 << pack) - 1));
-  };
-  auto lse_at = [&](int grow) -> float* {
-    if (shared) return px.part_l + part_at(grow);
-    return Lout + static_cast<size_t>(hq + (grow & ((1 << pack) - 1))) * total + sr.base +
-           (grow >> pack);
-  };
-  // row `grow` sees no key here: O = 0, L = -inf (a range's O is not read where its L is -inf)
-  auto empty_row = [&](int grow) {
-    if (!shared) {
-      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at(grow) * D);
+  Work<NT> work;
+  bool have = true, cuts = false;
+  Piece mine = {};                              // without ranges
+  if (!RANGES) {
+    work.whole(px, cu_seqlens, N, H, total, static_cast<int>(blockIdx.x));
+    mine = work.piece(px, group);
+    mine.part = -1;
+  }
+  if (!RANGES && mine.j0 >= mine.j1) {          // past the sequence's queries, or before its keys
+    const int heads = 1 << pack;
+    for (int r = mine.row0 + threadIdx.x; r < min(mine.row0 + NT * BM, mine.nr); r += THREADS) {
+      const int h = mine.hq + (r & (heads - 1));
+      const size_t tok = static_cast<size_t>(mine.base + (r >> pack));
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + (tok * H + h) * D);
       for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      Lout[static_cast<size_t>(h) * total + tok] = -INFINITY;
     }
-    *lse_at(grow) = -INFINITY;
-  };
-  if (n_stream <= 0) {                          // past the sequence's queries, or before its keys
-    for (int r = row0 + threadIdx.x; r < min(row0 + NT * BM, Nr); r += THREADS) empty_row(r);
     return;
   }
+  // Pieces pass to the warps that need them through two slots.
+  static_assert(sizeof(Piece) <= 64, "a slot of the ring");
+  auto info = [&](int k) -> volatile Piece* {
+    return reinterpret_cast<volatile Piece*>(sg + C::INFO_OFF + 64 * (k & 1));
+  };
+  // KV tiles [lo, hi) of Q tile t that a piece has
+  auto tiles_of = [&](const volatile Piece& p, int t, int& lo, int& hi) {
+    const KeyRows kr = {p.kr.n, p.kr.off, p.kr.hi};
+    paged_tiles(kr, p.row0 + t * BM, p.nr, px.window, pack, lo, hi);
+    lo = min(max(lo, p.j0), p.j1);
+    hi = min(max(hi, p.j0), p.j1);
+  };
 
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8 * i; };
   const int B_QF = 0;
@@ -339,14 +515,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto B_SF = [&](int t) { return 1 + 4 * C::STAGES + t; };
   auto B_PF = [&](int t) { return 3 + 4 * C::STAGES + t; };
   auto B_OF = [&](int t) { return 5 + 4 * C::STAGES + t; };
-  const int B_DONE = 7 + 4 * C::STAGES;
+  const int B_DONE = 7 + 4 * C::STAGES, B_QE = B_DONE + 1;
+  auto B_TF = [&](int k) { return B_DONE + 2 + (k & 1); };
+  auto B_TE = [&](int k) { return B_DONE + 4 + (k & 1); };
 
-  PagedTile first_tile;                         // its look-up passes under the set-up
-  if (warp == 0) paged_fetch(px, b, kr, j0 * BN, lane, first_tile);
   if (threadIdx.x == 0) {
+    if (!RANGES) *const_cast<Piece*>(info(0)) = mine;
     for (int i = 0; i < C::NBARS; ++i) mbar_init(bar(i), 1);
     for (int t = 0; t < NT; ++t) mbar_init(bar(B_PF(t)), 128);
+    for (int k = 0; k < 2; ++k) mbar_init(bar(B_TE(k)), 9);   // the MMA thread, 8 softmax warps
     fence_mbar_init();
+  }
+  PagedTile first_tile;                         // its look-up passes under the set-up
+  if (warp == 0) {
+    if (RANGES) have = work.first(px, cu_seqlens, N, H, total, cuts);
+    if (have && work.u < work.ue)
+      paged_fetch(px, work.b, work.kr, (work.span.lo + work.u) * BN, lane, first_tile);
   }
   if (warp == 1) {
     tmem_alloc(sb + C::SLOT_OFF, C::TMEM_COLS);
@@ -366,50 +550,78 @@ __global__ void __launch_bounds__(THREADS, 1)
     regs_dec<kRegsLow>();                          // warpgroup 0 (TMA, MMA issue): few registers
     // ------------------------------------------------------------ producer
     {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(B_QF), NT * C::TILE_BYTES);
-        for (int t = 0; t < NT; ++t)
-          for (int c = 0; c < C::NCHUNK; ++c)
-            tma_load_3d(sb + C::Q_OFF + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ, bar(B_QF),
-                        c * C::ATOM, hq, sr.base + ((row0 + t * BM) >> pack));
-      }
       bool ok = true;
-      PagedTile next = first_tile;
-      int j = 0;
-      for (; j < n_stream; ++j) {
-        const int s = j % C::STAGES;
-        const uint32_t ph = (j / C::STAGES) & 1;
-        const PagedTile cur = next;
-        if (j + 1 < n_stream) paged_fetch(px, b, kr, (j0 + j + 1) * BN, lane, next);
-        if (!(ok = mbar_wait_warp(bar(B_KE(s)), ph ^ 1, ctl))) break;
-        // the slot's last readers were the softmax threads of tile j - 8: they are done,
-        // since S(j - 2), whose K tile has just been released, waited for their P
-        paged_mask(px, lane, cur, sb + C::MASK_OFF + (j % kMaskSlots) * 16);
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_KF(s)), C::TILE_BYTES);
-        __syncwarp();
-        paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), hk, lane, cur);
-        if (!(ok = mbar_wait_warp(bar(B_VE(s)), ph ^ 1, ctl))) { ++j; break; }
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_VF(s)), C::TILE_BYTES);
-        __syncwarp();
-        paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), hk, lane, cur);
+      int g = 0, nk = 0, nv = 0, nq = 0;         // KV steps, K, V and Q tiles loaded
+      int n_pieces = 0;
+      for (int k = 0; !RANGES || have; ++k) {
+        const Piece p = RANGES ? work.piece(px, group) : mine;
+        if (RANGES) {
+          if (!(ok = mbar_wait_warp(bar(B_TE(k)), ((k >> 1) & 1) ^ 1, ctl))) break;
+          if (lane == 0) {
+            *const_cast<Piece*>(info(k)) = p;
+            mbar_arrive(bar(B_TF(k)));           // release: the piece is seen with the phase
+          }
+        }
+        if (p.j0 < p.j1) {
+          // Q free once the previous piece's last S is done
+          if (RANGES && !(ok = mbar_wait_warp(bar(B_QE), (nq & 1) ^ 1, ctl))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(B_QF), NT * C::TILE_BYTES);
+            for (int t = 0; t < NT; ++t)
+              for (int c = 0; c < C::NCHUNK; ++c)
+                tma_load_3d(sb + C::Q_OFF + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tmQ, bar(B_QF),
+                            c * C::ATOM, p.hq, p.base + ((p.row0 + t * BM) >> pack));
+          }
+          ++nq;
+          PagedTile next;
+          if (k == 0) next = first_tile;
+          else paged_fetch(px, work.b, p.kr, p.j0 * BN, lane, next);
+          for (int j = p.j0; j < p.j1; ++j, ++g) {
+            const int s = g % C::STAGES;
+            const uint32_t ph = (g / C::STAGES) & 1;
+            const PagedTile cur = next;
+            if (j + 1 < p.j1) paged_fetch(px, work.b, p.kr, (j + 1) * BN, lane, next);
+            if (!(ok = mbar_wait_warp(bar(B_KE(s)), ph ^ 1, ctl))) break;
+            // the slot's last readers were the softmax threads of step g - 8: they are done,
+            // since S(g - 2), whose K tile has just been released, waited for their P
+            paged_mask(px, lane, cur, sb + C::MASK_OFF + (g % kMaskSlots) * 16);
+            if (lane == 0) mbar_arrive_expect_tx(bar(B_KF(s)), C::TILE_BYTES);
+            __syncwarp();
+            paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), p.hk, lane, cur);
+            ++nk;
+            if (!(ok = mbar_wait_warp(bar(B_VE(s)), ph ^ 1, ctl))) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(B_VF(s)), C::TILE_BYTES);
+            __syncwarp();
+            paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), p.hk, lane, cur);
+            ++nv;
+          }
+          if (!ok) break;
+        }
+        if (!RANGES) break;
+        have = cuts && work.next(px, cu_seqlens, N, H, total);
+        n_pieces = k + 1;
+      }
+      if (RANGES && ok && (ok = mbar_wait_warp(bar(B_TE(n_pieces)), ((n_pieces >> 1) & 1) ^ 1, ctl))) {
+        if (lane == 0) {
+          info(n_pieces)->nr = -1;               // the end
+          mbar_arrive(bar(B_TF(n_pieces)));
+        }
       }
       if (!ok) {
         // drain: wait (bounded) for the copies in flight, so that none lands in shared memory
         // after the CTA has gone
-        mbar_wait_warp(bar(B_QF), 0, ctl);
-        for (int jj = max(0, j - C::STAGES); jj < j; ++jj) {
-          const int s = jj % C::STAGES;
-          const uint32_t ph = (jj / C::STAGES) & 1;
-          mbar_wait_warp(bar(B_KF(s)), ph, ctl);
-          mbar_wait_warp(bar(B_VF(s)), ph, ctl);
-        }
+        if (nq > 0) mbar_wait_warp(bar(B_QF), (nq - 1) & 1, ctl);
+        for (int i = max(0, nk - C::STAGES); i < nk; ++i)
+          mbar_wait_warp(bar(B_KF(i % C::STAGES)), (i / C::STAGES) & 1, ctl);
+        for (int i = max(0, nv - C::STAGES); i < nv; ++i)
+          mbar_wait_warp(bar(B_VF(i % C::STAGES)), (i / C::STAGES) & 1, ctl);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     regs_dec<kRegsLow>();
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n_stream > 0) {
+    if (lane == 0) {
       constexpr uint32_t idS = umma_idesc_f16(BM, BN, BF16, false, false);
       constexpr uint32_t idO = umma_idesc_f16(BM, D, BF16, false, true);
       // descriptor low words of Q tile 0 and of stage 0 of the K and V rings (K-major
@@ -434,47 +646,68 @@ __global__ void __launch_bounds__(THREADS, 1)
                     va + ((kk * 16 * C::SW) >> 4), HI, idO, kk > 0 ? 1u : acc0);
         }
       };
-      bool ok = mbar_wait(bar(B_QF), 0, ctl) && mbar_wait(bar(B_KF(0)), 0, ctl);
-      if (ok) {
+      // The step index g of the K and V rings runs on across pieces; p_full[t] has had np[t]
+      // phases before the current piece.
+      bool ok = true;
+      int g = 0, nq = 0, np[NT] = {};
+      for (int k = 0;; ++k) {
+        if (RANGES && !(ok = mbar_wait(bar(B_TF(k)), (k >> 1) & 1, ctl))) break;
+        const volatile Piece& p = *info(k);
+        if (p.nr < 0) break;
+        const int j0 = p.j0, n = p.j1 - j0;
+        int lo_t[NT], n_t[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) tiles_of(p, t, lo_t[t], n_t[t]);
+        if (RANGES) mbar_arrive(bar(B_TE(k)));
+        if (RANGES && n <= 0) continue;
+        if (!(ok = mbar_wait(bar(B_QF), nq & 1, ctl) &&
+                   mbar_wait(bar(B_KF(g % C::STAGES)), (g / C::STAGES) & 1, ctl)))
+          break;
+        ++nq;
         tc_fence_after();
         for (int t = 0; t < NT; ++t)
           if (lo_t[t] == j0 && n_t[t] > j0) {
-            issue_S(t, 0);
+            issue_S(t, g % C::STAGES);
             umma_commit(bar(B_SF(t)));
           }
-        umma_commit(bar(B_KE(0)));
-      }
-      // stream position jj holds KV tile j = j0 + jj; Q tile t takes part while
-      // lo_t[t] <= j < n_t[t], its own iteration index being j - lo_t[t]
-      for (int jj = 0; ok && jj < n_stream; ++jj) {
-        const int j = j0 + jj;
-        const int s = jj % C::STAGES;
-        const int s1 = (jj + 1) % C::STAGES;
-        const uint32_t ph = (jj / C::STAGES) & 1, ph1 = ((jj + 1) / C::STAGES) & 1;
-        if (!(ok = mbar_wait(bar(B_VF(s)), ph, ctl))) break;
-        bool k_next = false;
-        for (int t = 0; t < NT && ok; ++t) {
-          const bool in_t = j >= lo_t[t] && j < n_t[t];
-          if (in_t) {
-            if (!(ok = mbar_wait(bar(B_PF(t)), (j - lo_t[t]) & 1, ctl))) break;
-            tc_fence_after();
-            issue_PV(t, s, j > lo_t[t]);
-          }
-          if (j + 1 >= lo_t[t] && j + 1 < n_t[t]) {
-            if (!k_next) {
-              if (!(ok = mbar_wait(bar(B_KF(s1)), ph1, ctl))) break;
+        umma_commit(bar(B_KE(g % C::STAGES)));
+        if (RANGES && n == 1) umma_commit(bar(B_QE));
+        // step g holds KV tile j = j0 + jj; Q tile t takes part while
+        // lo_t[t] <= j < n_t[t], its own iteration index being j - lo_t[t]
+        for (int jj = 0; jj < n; ++jj, ++g) {
+          const int j = j0 + jj;
+          const int s = g % C::STAGES;
+          const int s1 = (g + 1) % C::STAGES;
+          const uint32_t ph = (g / C::STAGES) & 1, ph1 = ((g + 1) / C::STAGES) & 1;
+          if (!(ok = mbar_wait(bar(B_VF(s)), ph, ctl))) break;
+          bool k_next = false;
+          for (int t = 0; t < NT && ok; ++t) {
+            const bool in_t = j >= lo_t[t] && j < n_t[t];
+            if (in_t) {
+              if (!(ok = mbar_wait(bar(B_PF(t)), (np[t] + j - lo_t[t]) & 1, ctl))) break;
               tc_fence_after();
-              k_next = true;
+              issue_PV(t, s, j > lo_t[t]);
             }
-            issue_S(t, s1);
-            umma_commit(bar(B_SF(t)));
-          } else if (in_t) {
-            umma_commit(bar(B_OF(t)));
+            if (j + 1 >= lo_t[t] && j + 1 < n_t[t]) {
+              if (!k_next) {
+                if (!(ok = mbar_wait(bar(B_KF(s1)), ph1, ctl))) break;
+                tc_fence_after();
+                k_next = true;
+              }
+              issue_S(t, s1);
+              umma_commit(bar(B_SF(t)));
+            } else if (in_t) {
+              umma_commit(bar(B_OF(t)));
+            }
           }
+          if (!ok) break;
+          umma_commit(bar(B_VE(s)));
+          if (k_next) umma_commit(bar(B_KE(s1)));
+          if (RANGES && jj + 2 == n) umma_commit(bar(B_QE));   // the piece's last S is on its way
         }
-        if (!ok) break;
-        umma_commit(bar(B_VE(s)));
-        if (k_next) umma_commit(bar(B_KE(s1)));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) np[t] += n_t[t] - lo_t[t];
+        if (!RANGES || !ok) break;
       }
       // every MMA this thread issued has completed before TMEM is released
       umma_commit(bar(B_DONE));
@@ -486,124 +719,157 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;
     const int rit = (warp & 3) * 32 + lane;              // row within the tile (= TMEM lane)
-    const int grow = row0 + t * BM + rit;                // query row
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::S_COL + t * BN;
     const uint32_t tO = tmem + lane_off + C::O_COL + t * D;
-    const int nt = n_t[t] - lo_t[t];             // this tile's KV tiles, from lo_t[t]
-    const int tile_row0 = row0 + t * BM;
-    const RowKeys rk = row_keys(kr, tile_row0, grow, pack, px.window);
-    float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      if (!(ok = mbar_wait_warp(bar(B_SF(t)), j & 1, ctl))) break;
-      tc_fence_after();
-      uint32_t mask[4], sr[BN];
-      load_mask(sb + C::MASK_OFF + ((lo_t[t] + j - j0) % kMaskSlots) * 16, mask);
-      tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-      tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-      tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-      tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
-      tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-      tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-      tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-      tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
-      const int kbase = (lo_t[t] + j) * BN;
-      paged_masks<false>(rk, kbase, mask, sr);
-      if (kbase + BN > Nk) {                     // the last tile's V rows past the keys
-        const int jj = lo_t[t] + j - j0;         // stream position
-        if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
-        if (kbase + rit >= Nk) clear_row<D>(sb + C::V_OFF + (jj % C::STAGES) * C::TILE_BYTES, rit);
-        fence_proxy_async_smem();                // before this thread's arrival on p_full
-      }
-      // row maximum: four independent chains of 3-input max
-      const float mx = row_max128(sr);
-      const float m_tile = mx * c_log2;
-      const bool grow_m = m_tile > m_run + RESCALE_LOG2;
-      const float m_use = grow_m ? m_tile : m_run;
-      const float alpha = grow_m ? ex2(m_run - m_use) : 1.f;
-      const float m_sub = (m_use == -INFINITY) ? 0.f : m_use;
-      const float2 c2 = make_float2(c_log2, c_log2), nm2 = make_float2(P_LOG2<BF16> - m_sub, P_LOG2<BF16> - m_sub);
-      float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = 32 * h + 2 * i;
-          const float2 t = fma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2, nm2);
-          const float2 pp = make_float2(ex2(t.x), ex2(t.y));
-          rs2[i & 1] = add2(rs2[i & 1], pp);
-          pk[i] = pack2<BF16>(pp.x, pp.y);
+    int g = 0, ns = 0, no = 0;                   // ring steps, phases of s_full and o_full so far
+    for (int k = 0;; ++k) {
+      if (RANGES && !mbar_wait_warp(bar(B_TF(k)), (k >> 1) & 1, ctl)) break;
+      const volatile Piece& p = *info(k);
+      if (p.nr < 0) break;
+      int lo, hi;
+      tiles_of(p, t, lo, hi);
+      const int nt = hi - lo, g0 = g + lo - p.j0;   // this tile's KV tiles, its first step
+      const int Nk = p.kr.n;
+      const KeyRows kr = {Nk, p.kr.off, p.kr.hi};
+      const int tile_row0 = p.row0 + t * BM;
+      const RowKeys rk = row_keys(kr, tile_row0, tile_row0 + rit, pack, px.window);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < nt; ++j) {
+        if (!(ok = mbar_wait_warp(bar(B_SF(t)), (ns + j) & 1, ctl))) break;
+        tc_fence_after();
+        uint32_t mask[4], sr[BN];
+        load_mask(sb + C::MASK_OFF + ((g0 + j) % kMaskSlots) * 16, mask);
+        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+        tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+        const int kbase = (lo + j) * BN;
+        paged_masks<false>(rk, kbase, mask, sr);
+        if (kbase + BN > Nk) {                     // the last tile's V rows past the keys
+          const int jj = g0 + j;                   // step of the rings
+          if (!(ok = mbar_wait_warp(bar(B_VF(jj % C::STAGES)), (jj / C::STAGES) & 1, ctl))) break;
+          if (kbase + rit >= Nk) clear_row<D>(sb + C::V_OFF + (jj % C::STAGES) * C::TILE_BYTES, rit);
+          fence_proxy_async_smem();                // before this thread's arrival on p_full
         }
-        tmem_st16(tS + 16 * h, pk);
+        // row maximum: four independent chains of 3-input max
+        const float mx = row_max128(sr);
+        const float m_tile = mx * c_log2;
+        const bool grow_m = m_tile > m_run + RESCALE_LOG2;
+        const float m_use = grow_m ? m_tile : m_run;
+        const float alpha = grow_m ? ex2(m_run - m_use) : 1.f;
+        const float m_sub = (m_use == -INFINITY) ? 0.f : m_use;
+        const float2 c2 = make_float2(c_log2, c_log2), nm2 = make_float2(P_LOG2<BF16> - m_sub, P_LOG2<BF16> - m_sub);
+        float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = 32 * h + 2 * i;
+            const float2 t = fma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2, nm2);
+            const float2 pp = make_float2(ex2(t.x), ex2(t.y));
+            rs2[i & 1] = add2(rs2[i & 1], pp);
+            pk[i] = pack2<BF16>(pp.x, pp.y);
+          }
+          tmem_st16(tS + 16 * h, pk);
+        }
+        const float rs = (rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y);
+        l_run = l_run * alpha + rs;
+        if (j > 0 && __any_sync(0xffffffffu, grow_m)) {
+          // O holds sum over tiles < j; PV(j-1) has completed because S(j) was
+          // issued after it and its commit was observed above.
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * cc, o);
+            tmem_ld_wait_regs(o);
+            const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2);
+              o[2 * i] = __float_as_uint(v.x);
+              o[2 * i + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(tO + 32 * cc, o);
+          }
+        }
+        m_run = m_use;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(B_PF(t)));
       }
-      const float rs = (rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y);
-      l_run = l_run * alpha + rs;
-      if (j > 0 && __any_sync(0xffffffffu, grow_m)) {
-        // O holds sum over tiles < j; PV(j-1) has completed because S(j) was
-        // issued after it and its commit was observed above.
+      if (!ok) break;
+      // where the row lies in O, in the workspace, and in L or the workspace's L
+      const int grow = p.row0 + t * BM + rit, Nr = p.nr, part = RANGES ? p.part : -1;
+      const int h = p.hq + (grow & ((1 << pack) - 1));
+      const size_t tok = static_cast<size_t>(p.base + (grow >> pack)), row_at = tok * H + h;
+      const size_t part_at = static_cast<size_t>(part) * (NT * BM) + (t * BM + rit);
+      float* lse_at = part >= 0 ? px.part_l + part_at : Lout + static_cast<size_t>(h) * total + tok;
+      if (nt > 0) {
+        if (!(ok = mbar_wait_warp(bar(B_OF(t)), no & 1, ctl))) break;
+        ++no;
+        tc_fence_after();
+        const bool none = l_run == 0.f;            // a row whose keys are all masked: acc = 0
+        const float inv_l = none ? 0.f : 1.f / l_run;
+        const bool valid = grow < Nr;
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * cc, o);
           tmem_ld_wait_regs(o);
-          const float2 a2 = make_float2(alpha, alpha);
+          if (part >= 0) {
+            if (valid) {
+              float4* dst = reinterpret_cast<float4*>(px.part + part_at * D + 32 * cc);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 v = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2);
-            o[2 * i] = __float_as_uint(v.x);
-            o[2 * i + 1] = __float_as_uint(v.y);
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(
+                    __uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
+                    __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+            }
+            continue;
           }
-          tmem_st32(tO + 32 * cc, o);
-        }
-      }
-      m_run = m_use;
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(bar(B_PF(t)));
-    }
-    if (ok && nt > 0 && mbar_wait_warp(bar(B_OF(t)), 0, ctl)) {
-      tc_fence_after();
-      const bool none = l_run == 0.f;            // a row whose keys are all masked: acc = 0
-      const float inv_l = none ? 0.f : 1.f / l_run;
-      const bool valid = grow < Nr;
+          uint32_t w[16];
 #pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * cc, o);
-        tmem_ld_wait_regs(o);
-        if (shared) {
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
+                               __uint_as_float(o[2 * i + 1]) * inv_l);
           if (valid) {
-            float4* dst = reinterpret_cast<float4*>(px.part + part_at(grow) * D + 32 * cc);
+            uint4* dst =
+                reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at * D + 32 * cc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(
-                  __uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
-                  __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
-          continue;
         }
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
-                             __uint_as_float(o[2 * i + 1]) * inv_l);
-        if (valid) {
-          uint4* dst =
-              reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at(grow) * D + 32 * cc);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        if (valid)
+          *lse_at = none ? -INFINITY : (m_run - P_LOG2<BF16> + log2f(l_run)) * 0.69314718055994531f;
+        tc_fence_before();                         // O read before the next piece's p_full
+      } else if (grow < Nr) {
+        // the row sees no key here: O = 0, L = -inf (a piece's O is not read where its L is -inf)
+        if (part < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at * D);
+          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
         }
+        *lse_at = -INFINITY;
       }
-      if (valid)
-        *lse_at(grow) = none ? -INFINITY : (m_run - P_LOG2<BF16> + log2f(l_run)) * 0.69314718055994531f;
-    } else if (nt <= 0 && grow < Nr) {
-      empty_row(grow);
+      ns += nt;
+      g += p.j1 - p.j0;
+      if (!RANGES) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_TE(k)));  // the slot may take the piece after the next
     }
   } else {
-    regs_dec<kRegsLow>();                          // warps 2 and 3: idle
+    regs_dec<kRegsLow>();
+    // ------------------------------------------------------------ rows without keys
+    if (RANGES)
+      rows_without_keys<NT, D>(px, cu_seqlens, N, H, total, static_cast<uint16_t*>(Out), Lout,
+                               static_cast<int>(threadIdx.x) - 64, 64);
   }
   // ------------------------------------------------------------ teardown
   tc_fence_before();
@@ -614,37 +880,40 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-PagedArgs paged_args(const FwdArgs& a) {
+size_t hdr_bytes(int ranges) { return (ranges * sizeof(RangeHeader) + 15) / 16 * 16; }
+
+PagedArgs paged_args(const FwdArgs& a, int rows, int d) {
   PagedArgs px;
+  px.n_qt = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + rows - 1) / rows);
   px.pg = a.pg;
   px.box_log2 = a.box_log2;
   px.causal = a.causal;
   px.window = a.window;
   px.pack = a.pack;
-  px.n_split = a.n_split;
-  px.rows = static_cast<size_t>(a.B) * a.N * a.H;
-  px.part = a.part;
-  px.part_l = a.part_l;
+  px.B = a.B;
+  px.ranges = a.ranges;
+  px.hdr = static_cast<RangeHeader*>(a.ws);
+  px.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + hdr_bytes(a.ranges));
+  px.part_l = px.part + static_cast<size_t>(2 * a.ranges) * rows * d;
   return px;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool RANGES>
 cudaError_t launch_fwd_paged2_t(const FwdArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
   constexpr int smem = C::SMEM_BYTES;
-  auto kern = fwd_paged_kernel<D, BF16>;
+  auto kern = fwd_paged_kernel<D, BF16, RANGES>;
   cudaError_t e = check_split_regs(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
   e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int n_qblk =
-      static_cast<int>(((static_cast<long long>(a.N) << a.pack) + NT * BM - 1) / (NT * BM));
-  const long long grid = static_cast<long long>(n_qblk) * a.BH;
+  const PagedArgs px = paged_args(a, NT * BM, D);
+  const long long tiles = static_cast<long long>(px.n_qt) * a.BH;
+  const long long grid = tiles > a.ranges ? tiles : a.ranges;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
   e = launch_dependent(kern, static_cast<unsigned>(grid), THREADS, smem, st, a.tmQ, a.tmK, a.tmV,
-                       a.O, a.L, a.N, n_qblk, a.group, a.cu_seqlens, a.H, a.total, a.c_log2, a.ctl,
-                       paged_args(a));
+                       a.O, a.L, a.N, a.group, a.cu_seqlens, a.H, a.total, a.c_log2, a.ctl, px);
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -685,7 +954,7 @@ struct Cfg1 {
   static constexpr int CLC_OFF = (BAR_OFF + NBARS * 8 + 15) / 16 * 16;   // 16-byte response
   static constexpr int SLOT_OFF = CLC_OFF + 16;             // TMEM base, tile slots[2]
   static constexpr int MASK_OFF = SLOT_OFF + 16;            // key masks
-  static constexpr int INFO_OFF = MASK_OFF + kMaskSlots * 16;   // two Tile1
+  static constexpr int INFO_OFF = MASK_OFF + kMaskSlots * 16;   // two Pieces
   static constexpr int SMEM_BYTES = INFO_OFF + 2 * 64;
   static constexpr int TMEM_COLS = 256;
   static constexpr uint32_t S_COL = 0, P_COL = 128, O_COL = 192;
@@ -694,37 +963,6 @@ struct Cfg1 {
   static_assert(O_COL + D <= TMEM_COLS, "TMEM layout");
 };
 
-// One query tile of the grid: its first head, K/V head and first row, and its KV tiles
-// [lo, lo + nt).
-struct Tile1 {
-  int b, hq, hk, row0, lo, nt;
-  int base, nr;                                  // first token and query rows of the sequence
-  KeyRows kr;
-  int split;                                     // its KV range, if it has one of several
-  bool shared;
-};
-static_assert(sizeof(Tile1) <= 64, "a slot of the tile ring");
-__device__ __forceinline__ Tile1 tile1(int id, int n_qt, int N, int group, const int* cu_seqlens,
-                                       int H, int total, const PagedArgs& px) {
-  Tile1 t;
-  const BlockPos bp = block_pos(n_qt, id);       // bp.bh: sequence, block of heads, KV range
-  const int blocks = H >> px.pack, bh = bp.bh / px.n_split;
-  t.split = bp.bh % px.n_split;
-  t.b = bh / blocks;
-  t.hq = (bh % blocks) << px.pack;
-  t.hk = t.hq / group;
-  t.row0 = (n_qt - 1 - bp.rank) * BM;            // the last query tiles have the most work
-  SeqRows sr;
-  rows_of(px, cu_seqlens, t.b, N, total, sr, t.kr);
-  t.base = sr.base;
-  t.nr = sr.n << px.pack;
-  const SplitRange sp = split_range<1>(t.kr, t.row0, t.nr, px.window, px.pack, px.n_split);
-  t.shared = sp.used > 1;
-  t.lo = sp.lo + t.split * sp.per;
-  t.nt = max(min(sp.per, sp.hi - t.lo), 0);
-  if (t.split >= sp.used) t.nr = t.nt = 0;       // nothing to do or to write
-  return t;
-}
 }  // namespace one
 
 template <int D, bool BF16>
@@ -732,8 +970,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
     fwd1_paged_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, void* __restrict__ Out,
-                      float* __restrict__ Lout, int N, int n_qt, int group, const int* cu_seqlens,
-                      int H, int total, float c_log2, KernelCtl ctl, const PagedArgs px) {
+                      float* __restrict__ Lout, int N, int group, const int* cu_seqlens, int H,
+                      int total, float c_log2, KernelCtl ctl, const PagedArgs px) {
   using C = Cfg<D>;
   using C1 = one::Cfg1<D>;
   constexpr int STAGES = C1::STAGES;
@@ -742,7 +980,10 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   grid_dep_launch();                            // the next kernel may start setting up
   if (sb & 1023u) {                             // see FA_DEV_SMEM_ALIGN
     grid_dep_wait();
-    if (threadIdx.x == 0) atomicOr(ctl.status, FA_DEV_SMEM_ALIGN);
+    if (threadIdx.x == 0) {
+      atomicOr(ctl.status, FA_DEV_SMEM_ALIGN);
+      if (static_cast<int>(blockIdx.x) < px.ranges) px.hdr[blockIdx.x].rows = 0;
+    }
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -786,8 +1027,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sg + C1::SLOT_OFF);
   grid_dep_wait();                              // inputs written, outputs free to overwrite
 
-  auto info = [&](int b) -> one::Tile1* {
-    return reinterpret_cast<one::Tile1*>(sg + C1::INFO_OFF + 64 * b);
+  auto info = [&](int b) -> Piece* {
+    return reinterpret_cast<Piece*>(sg + C1::INFO_OFF + 64 * b);
   };
   // Consumers read tile k from slot k & 1; the last tile published is -1.
   auto next_tile = [&](int k, bool& ok) -> int {
@@ -803,17 +1044,19 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         return mbar_wait_warp(b, parity, ctl);
       };
       bool ok = true;
-      int tile = static_cast<int>(blockIdx.x);
+      Work<1> work;
+      int tile = static_cast<int>(blockIdx.x);   // in a range: >= 0 while there are pieces
+      bool cuts = false;
+      if (px.ranges && !work.first(px, cu_seqlens, N, H, total, cuts)) tile = -1;
       int g = 0, kq = 0, nk = 0, nv = 0;         // steps, Q tiles, K and V tiles loaded
       bool pending = false;                       // a request for the next tile is out
       int n_req = 0;                               // requests made
       for (int k = 0; ok; ++k) {
         if (!(ok = wait(bar(B_TE(k & 1)), ((k >> 1) & 1) ^ 1))) break;
-        one::Tile1 t;
-        if (tile >= 0) {
-          t = one::tile1(tile, n_qt, N, group, cu_seqlens, H, total, px);
-          if (lead) *info(k & 1) = t;
-        }
+        if (tile >= 0 && (k > 0 ? !cuts : !px.ranges)) work.whole(px, cu_seqlens, N, H, total, tile);
+        const Piece t = work.piece(px, group);
+        const int nt = t.j1 - t.j0;
+        if (lead && tile >= 0) *info(k & 1) = t;
         if (lead) {
           slot[k & 1] = tile;
           mbar_arrive(bar(B_TF(k & 1)));        // release: the slot write is seen with the phase
@@ -832,8 +1075,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
           pending = true;
           ++n_req;
         };
-        if (t.nt <= 0) request();
-        if (t.nt > 0) {
+        if (nt <= 0 && !cuts) request();
+        if (nt > 0) {
           const int qb = kq & 1;
           if (!(ok = wait(bar(B_QE(qb)), ((kq >> 1) & 1) ^ 1))) break;
           if (lead) {
@@ -844,13 +1087,13 @@ __global__ void __launch_bounds__(one::THREADS, 2)
           }
           ++kq;
           PagedTile next;
-          paged_fetch(px, t.b, t.kr, t.lo * BN, lane, next);
-          for (int j = 0; j < t.nt; ++j, ++g) {
+          paged_fetch(px, work.b, t.kr, t.j0 * BN, lane, next);
+          for (int j = 0; j < nt; ++j, ++g) {
             const int st = g % STAGES;
             const uint32_t ph = (g / STAGES) & 1;
-            const int krow = (t.lo + j) * BN;
+            const int krow = (t.j0 + j) * BN;
             const PagedTile cur = next;
-            if (j + 1 < t.nt) paged_fetch(px, t.b, t.kr, krow + BN, lane, next);
+            if (j + 1 < nt) paged_fetch(px, work.b, t.kr, krow + BN, lane, next);
             if (!(ok = wait(bar(B_KE(st)), ph ^ 1))) break;
             // the mask slot's last readers were the softmax threads of step g - 8: they are
             // done, since S(g - STAGES), whose K tile has just been released, came two steps
@@ -867,9 +1110,13 @@ __global__ void __launch_bounds__(one::THREADS, 2)
             paged_load<D>(px, &tmV, sb + C1::V_OFF + st * C1::TILE_BYTES, bar(B_VF(st)), t.hk, lane,
                           cur);
             ++nv;
-            if (j + 1 == t.nt) request();
+            if (j + 1 == nt && !cuts) request();
           }
           if (!ok) break;
+        }
+        if (cuts) {
+          if (!work.next(px, cu_seqlens, N, H, total)) tile = -1;
+          continue;
         }
         // the next tile: a CTA that had not started, if any was left
         if (!(ok = wait(bar(B_CLC), k & 1))) break;
@@ -918,7 +1165,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       for (int k = 0; ok; ++k) {
         const int tile = next_tile(k, ok);
         if (!ok) break;
-        const int nt = info(k & 1)->nt;
+        const int nt = info(k & 1)->j1 - info(k & 1)->j0;
         mbar_arrive(bar(B_TE(k & 1)));
         if (tile < 0) break;
         if (nt == 0) continue;
@@ -966,6 +1213,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
     const uint32_t tP = tmem + lane_off + C1::P_COL;
     const uint32_t tO = tmem + lane_off + C1::O_COL;
     bool ok = true;
+    if (px.ranges)
+      rows_without_keys<1, D>(px, cu_seqlens, N, H, total, static_cast<uint16_t*>(Out), Lout,
+                              static_cast<int>(threadIdx.x) - 64, 128);
     int g = 0, kq = 0;
     for (int k = 0; ok; ++k) {
       int tile = next_tile(k, ok);
@@ -978,8 +1228,8 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       };
       if (tile < 0) release();
       if (tile < 0) break;
-      const one::Tile1* ti = info(k & 1);
-      const int nt = ti->nt, lo = ti->lo, row0 = ti->row0, Nk = ti->kr.n;
+      const Piece* ti = info(k & 1);
+      const int lo = ti->j0, nt = ti->j1 - lo, row0 = ti->row0, Nk = ti->kr.n;
       const RowKeys rk = row_keys(ti->kr, row0, row0 + rit, pack, px.window);
       const int grow = row0 + rit;               // query row
       // where a row lies in O, in the workspace, and in L or the workspace's L
@@ -987,11 +1237,10 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         return static_cast<size_t>(ti->base + (r >> pack)) * H + ti->hq + (r & ((1 << pack) - 1));
       };
       auto part_at = [&](int r) -> size_t {
-        return ti->split * px.rows + (static_cast<size_t>(ti->b) * N + (r >> pack)) * H + ti->hq +
-               (r & ((1 << pack) - 1));
+        return static_cast<size_t>(ti->part) * BM + (r - row0);
       };
       auto lse_at = [&](int r) -> float* {
-        if (ti->shared) return px.part_l + part_at(r);
+        if (ti->part >= 0) return px.part_l + part_at(r);
         return Lout + static_cast<size_t>(ti->hq + (r & ((1 << pack) - 1))) * total + ti->base +
                (r >> pack);
       };
@@ -1096,7 +1345,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       ++kq;
       tc_fence_after();
       const int Nr = ti->nr;
-      const bool shared = ti->shared;
+      const bool shared = ti->part >= 0;
       const bool none = l_run == 0.f;            // a row whose keys are all masked: acc = 0
       const float inv_l = none ? 0.f : 1.f / l_run;
       const bool valid = grow < Nr;
@@ -1170,91 +1419,95 @@ cudaError_t launch_fwd_paged1_t(const FwdArgs& a, cudaStream_t st) {
   auto kern = fwd1_paged_kernel<D, BF16>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int n_qt = static_cast<int>(((static_cast<long long>(a.N) << a.pack) + BM - 1) / BM);
-  const long long grid = static_cast<long long>(n_qt) * a.BH;
+  const PagedArgs px = paged_args(a, BM, D);
+  const long long tiles = static_cast<long long>(px.n_qt) * a.BH;
+  const long long grid = tiles > a.ranges ? tiles : a.ranges;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   trace_begin(TR_FWD, st);
   e = launch_dependent(kern, static_cast<unsigned>(grid), one::THREADS, smem, st, a.tmQ,
-                       a.tmK, a.tmV, a.O, a.L, a.N, n_qt, a.group, a.cu_seqlens, a.H, a.total,
-                       a.c_log2, a.ctl, paged_args(a));
+                       a.tmK, a.tmV, a.O, a.L, a.N, a.group, a.cu_seqlens, a.H, a.total,
+                       a.c_log2, a.ctl, px);
   trace_end(TR_FWD, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Joins the KV ranges of a query tile: one warp per (query, head) of a sequence, which is
-// left alone where its tile was not cut.  TILES: query tiles of 128 rows that are cut together.
+// Joins the pieces of a query tile cut by range borders, a warp per row: the CTAs of range x
+// take part for the tile that it shares with range x - 1.
 constexpr int MERGE_THREADS = 128;
 template <int D, bool BF16, int TILES>
 __global__ void __launch_bounds__(MERGE_THREADS)
-    fwd_paged_merge_kernel(void* Out, float* Lout, const int* cu_seqlens, int N, int H, int total,
-                           const PagedArgs px) {
-  grid_dep_wait();                               // the ranges' results
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  SeqRows sr;
-  KeyRows kr;
-  rows_of(px, cu_seqlens, b, N, total, sr, kr);
-  const long long i =
-      static_cast<long long>(blockIdx.x) * (MERGE_THREADS / 32) + (threadIdx.x >> 5);
-  if (i >= static_cast<long long>(sr.n) * H) return;
-  const int q = static_cast<int>(i / H), h = static_cast<int>(i % H);
-  // the row in its block of packed heads, and the first row of its tiles
-  const int row = (q << px.pack) + (h & ((1 << px.pack) - 1));
-  const SplitRange sp = split_range<TILES>(kr, row / (TILES * BM) * (TILES * BM), sr.n << px.pack,
-                                           px.window, px.pack, px.n_split);
-  if (sp.used <= 1) return;
-  const size_t rows = px.rows, at = (static_cast<size_t>(b) * N + q) * H + h;   // in the workspace
-  float l_max = -INFINITY;
-  for (int s = lane; s < sp.used; s += 32) l_max = fmaxf(l_max, px.part_l[s * rows + at]);
+    fwd_paged_merge_kernel(void* Out, float* Lout, int H, int total, const PagedArgs px) {
+  constexpr int ROWS = TILES * BM, WARPS = MERGE_THREADS / 32;
+  grid_dep_wait();                               // the pieces' results
+  const RangeHeader hd = px.hdr[blockIdx.x];
+  if (hd.rows == 0) return;
+  const int lane = threadIdx.x & 31, n_sl = hd.c1 - hd.c0, used = n_sl + 1;
+  const int first = ((static_cast<int>(blockIdx.x) - hd.c0 - 1) * static_cast<int>(gridDim.y) +
+                     static_cast<int>(blockIdx.y)) * WARPS + (static_cast<int>(threadIdx.x) >> 5);
+  // piece s of row r: the first one is the second of its range, the others the first
+  auto at = [&](int s, int r) -> size_t {
+    return (2 * static_cast<size_t>(hd.c0 + s) + (s == 0)) * ROWS + r;
+  };
+  for (int r = first; r < hd.rows; r += n_sl * static_cast<int>(gridDim.y) * WARPS) {
+    float l_max = -INFINITY;
+    for (int s = lane; s < used; s += 32) l_max = fmaxf(l_max, px.part_l[at(s, r)]);
 #pragma unroll
-  for (int w = 16; w >= 1; w /= 2) l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, w));
-  // weights of 32 ranges at a time, one per lane; their rows in batches of 8 loads that do not
-  // wait for one another (a range without keys has weight 0 and left nothing to read)
-  constexpr int E = D / 32;
-  float sum = 0.f, acc[E] = {};
-  for (int s0 = 0; s0 < sp.used; s0 += 32) {
-    const float ls = s0 + lane < sp.used ? px.part_l[(s0 + lane) * rows + at] : -INFINITY;
-    const float wl = ls == -INFINITY ? 0.f : ex2((ls - l_max) * 1.4426950408889634f);
-    sum += wl;
-    for (int k0 = 0; k0 < min(32, sp.used - s0); k0 += 8) {
-      float v[8][E], w[8];
+    for (int w = 16; w >= 1; w /= 2) l_max = fmaxf(l_max, __shfl_xor_sync(0xffffffffu, l_max, w));
+    // weights of 32 ranges at a time, one per lane; their rows in batches of 8 loads that do not
+    // wait for one another (a range without keys has weight 0 and left nothing to read)
+    constexpr int E = D / 32;
+    float sum = 0.f, acc[E] = {};
+    for (int s0 = 0; s0 < used; s0 += 32) {
+      const float ls = s0 + lane < used ? px.part_l[at(s0 + lane, r)] : -INFINITY;
+      const float wl = ls == -INFINITY ? 0.f : ex2((ls - l_max) * 1.4426950408889634f);
+      sum += wl;
+      for (int k0 = 0; k0 < min(32, used - s0); k0 += 8) {
+        float v[8][E], w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        w[k] = __shfl_sync(0xffffffffu, wl, k0 + k);
-        const float* src = px.part + ((s0 + k0 + k) * rows + at) * D + lane * E;
+        for (int k = 0; k < 8; ++k) {
+          w[k] = __shfl_sync(0xffffffffu, wl, k0 + k);
+          const float* src = px.part + at(s0 + k0 + k, r) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = w[k] > 0.f ? src[e] : 0.f;
+          for (int e = 0; e < E; ++e) v[k][e] = w[k] > 0.f ? src[e] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(v[k][e], w[k], acc[e]);
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[k][e], w[k], acc[e]);
     }
-  }
 #pragma unroll
-  for (int w = 16; w >= 1; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  T* dst = static_cast<T*>(Out) + (static_cast<size_t>(sr.base + q) * H + h) * D + lane * E;
+    for (int w = 16; w >= 1; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    const int row = hd.row0 + r, h = hd.hq + (row & ((1 << px.pack) - 1));
+    const size_t tok = static_cast<size_t>(hd.base + (row >> px.pack));
+    T* dst = static_cast<T*>(Out) + (tok * H + h) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (BF16) dst[e] = __float2bfloat16_rn(acc[e] * inv);
-    else dst[e] = __float2half_rn(acc[e] * inv);
+    for (int e = 0; e < E; ++e) {
+      if constexpr (BF16) dst[e] = __float2bfloat16_rn(acc[e] * inv);
+      else dst[e] = __float2half_rn(acc[e] * inv);
+    }
+    if (lane == 0)
+      Lout[static_cast<size_t>(h) * total + tok] =
+          sum == 0.f ? -INFINITY : l_max + log2f(sum) * 0.69314718055994531f;
   }
-  if (lane == 0)
-    Lout[static_cast<size_t>(h) * total + sr.base + q] =
-        sum == 0.f ? -INFINITY : l_max + log2f(sum) * 0.69314718055994531f;
 }
 
 template <int D, bool BF16>
 cudaError_t launch_fwd_paged_t(const FwdArgs& a, cudaStream_t st) {
   cudaError_t e;
-  if constexpr (D == 128) e = launch_fwd_paged2_t<D, BF16>(a, st);
+  if constexpr (D == 128)
+    e = a.ranges ? launch_fwd_paged2_t<D, BF16, true>(a, st)
+                 : launch_fwd_paged2_t<D, BF16, false>(a, st);
   else e = launch_fwd_paged1_t<D, BF16>(a, st);
-  if (e != cudaSuccess || a.n_split == 1) return e;
-  const long long warps = static_cast<long long>(a.N) * a.H;
+  if (e != cudaSuccess || !a.ranges) return e;
+  constexpr int TILES = D == 128 ? NT : 1, ROWS = TILES * BM;
+  const long long rows = static_cast<long long>(a.N) << a.pack;
+  // CTAs per range: a warp for four of a query tile's rows
+  const unsigned y = static_cast<unsigned>(((rows < ROWS ? rows : ROWS) + 15) / 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps * 32 + MERGE_THREADS - 1) / MERGE_THREADS),
-                     static_cast<unsigned>(a.B));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ranges), y);
   cfg.blockDim = dim3(MERGE_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1262,8 +1515,8 @@ cudaError_t launch_fwd_paged_t(const FwdArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fwd_paged_merge_kernel<D, BF16, D == 128 ? NT : 1>, a.O, a.L,
-                            a.cu_seqlens, a.N, a.H, a.total, paged_args(a));
+  return cudaLaunchKernelEx(&cfg, fwd_paged_merge_kernel<D, BF16, TILES>, a.O, a.L, a.H, a.total,
+                            paged_args(a, ROWS, D));
 }
 
 template <bool BF16>
@@ -1282,21 +1535,33 @@ int fwd_paged_pack(int group) {
   return p;
 }
 
-// Ranges per query tile: none where the tiles fill half the GPU or more (152 SMs; two CTAs
-// each at d <= 64), else as many as fill it once.
-int fwd_paged_splits(int B, int H, int Hkv, int max_seqlen, int d) {
+// Which calls may cut: those whose tiles the GPU runs at once (152 SMs; two CTAs each at
+// d <= 64), or in up to four rounds where a tile holds all rows of a sequence: more tiles, or
+// those of long prompts, of which the short ones come last, even out by themselves (2 x 2048
+// tokens on 8192 keys, 512 tiles: 337 whole, 342 us cut).  Whether they do the device decides by
+// the lengths (Work::first).
+FwdPagedPlan fwd_paged_plan(int B, int H, int Hkv, int max_seqlen, int d) {
   const int pack = fwd_paged_pack(H / Hkv), rows = d == 128 ? NT * BM : BM;
-  const long long tiles = static_cast<long long>(B) * (H >> pack) *
-                          (((static_cast<long long>(max_seqlen) << pack) + rows - 1) / rows);
-  const long long slots = d == 128 ? 152 : 304;
-  return tiles * 2 > slots ? 1 : static_cast<int>(slots / tiles);
+  const int slots = d == 128 ? 152 : 304;
+  const long long n_qt = ((static_cast<long long>(max_seqlen) << pack) + rows - 1) / rows;
+  FwdPagedPlan p = {static_cast<long long>(B) * (H >> pack) * n_qt, 0, 0};
+  if (p.tiles > (n_qt == 1 ? 4 : 1) * slots) return p;
+  p.ranges = slots;
+  p.ws_bytes = hdr_bytes(slots) + 2 * sizeof(float) * slots * rows * (d + 1);
+  return p;
+}
+
+// Not for rows of up to four KV tiles, and not where the tiles' lengths may not add up in 32 bits.
+bool fwd_paged_may_cut(const FwdPagedPlan& p, long long keys) {
+  const long long most = (keys + BN - 1) / BN;
+  return p.ranges > 0 && most > 4 && p.tiles * (most + kTileCost) <= 0x7fffffffLL;
 }
 
 cudaError_t launch_fwd_paged(const FwdArgs& args, int d, bool bf16, bool causal, cudaStream_t st) {
   FwdArgs a = args;
   a.causal = causal;
   if (!causal || a.window == 0) a.window = kNoLimit;
-  a.BH = a.B * (a.H >> a.pack) * a.n_split;
+  a.BH = a.B * (a.H >> a.pack);
   return bf16 ? launch_fwd_paged_b<true>(a, d, st) : launch_fwd_paged_b<false>(a, d, st);
 }
 

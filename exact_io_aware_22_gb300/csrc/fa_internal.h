@@ -111,17 +111,24 @@ struct FwdArgs {
   int causal;
   int B;
   int pack;                    // log2 of the heads that share a query tile (0 elsewhere)
-  int n_split;                 // KV ranges per query tile
-  float* part;                 // workspace of the ranges, n_split > 1: results, then their L
-  float* part_l;
+  int ranges;                  // CTAs that may share the KV tiles of all query tiles (0: none)
+  void* ws;                    // their workspace
   float c_log2;                // scale * log2(e)
   KernelCtl ctl;
 };
 cudaError_t launch_fwd(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st);
 cudaError_t launch_fwd_paged(const FwdArgs& a, int d, bool bf16, bool causal, cudaStream_t st);
-// log2 of the heads packed in a query tile, and KV ranges per query tile, of a paged call.
+// log2 of the heads packed in a query tile of a paged call.
 int fwd_paged_pack(int group);
-int fwd_paged_splits(int B, int H, int Hkv, int max_seqlen, int d);
+// Query tiles of a paged call, and the CTAs that may share their KV tiles, with their workspace.
+struct FwdPagedPlan {
+  long long tiles;
+  int ranges;
+  size_t ws_bytes;
+};
+FwdPagedPlan fwd_paged_plan(int B, int H, int Hkv, int max_seqlen, int d);
+// Whether they do if a row may see up to `keys` keys.
+bool fwd_paged_may_cut(const FwdPagedPlan& p, long long keys);
 
 struct BwdArgs {
   CUtensorMap tmQ, tmK, tmV, tmO, tmdO;

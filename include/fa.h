@@ -343,14 +343,15 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
  *            sequence are left as they were.  A row without keys gets O = 0, L = -inf.
  *   workspace  fa_fwd_paged_workspace_size(B, max_seqlen, H, Hkv, d) bytes (16-byte
  *            aligned), or NULL: allocated and freed on `stream`.  0 bytes, and then unused,
- *            unless there are too few query rows to fill the GPU and the keys are split.
+ *            where there are query rows enough to fill the GPU without splitting the keys.  Its
+ *            contents do not matter before a call.
  *   A V element that is not finite reaches the query rows of its 128-key tile even where the
  *   causal mask or the window hides its key (0 x NaN), as in fa_fwd; what lies in absent pages
  *   and past the last key never does.
  *   Errors   as for the cache and fa_fwd_varlen, FA_ERR_INVALID_VALUE for a scale that times
  *            log2(e) overflows or vanishes in fp32; FA_ERR_UNSUPPORTED for more than 2^29 rows of
  *            one sequence's heads that share a tile (max_seqlen times the largest power of two
- *            that divides H / Hkv, at most 128) or more than 65535 sequences. */
+ *            that divides H / Hkv, at most 128) or 2^31 or more query tiles. */
 size_t fa_fwd_paged_workspace_size(int B, int max_seqlen, int H, int Hkv, int d);
 fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, float* L,
                        void* workspace, size_t workspace_bytes, const int* cu_seqlens, int B,

@@ -426,6 +426,12 @@ FWD = [
     ((3, 2), (2500, 300), 128, 1, 64, "bf16", 32, {}),
     ((33, 7), (2000, 100), 6, 1, 64, "fp16", 16, dict(pad=(2, 3))),
     ((9, 130), (3000, 700), 12, 2, 32, "bf16", 16, dict(causal=False)),
+    # ranges of several pieces: long and short sequences, some without rows or keys, and tiles
+    # for more than one round
+    ((5, 1, 0, 64, 3) * 8, (1, 9000, 300, 40, 0) * 8, 8, 2, 128, "bf16", 64, {}),
+    ((5, 1, 0, 30, 3) * 13, (1, 7000, 300, 40, 0) * 13, 16, 4, 64, "fp16", 16, dict(window=6000)),
+    ((300, 2, 40), (8000, 60, 5), 12, 3, 128, "fp16", 16, dict(pad=(2, 3))),
+    ((300, 2, 40), (8000, 60, 5), 12, 3, 32, "bf16", 16, dict(causal=False)),
 ]
 
 
@@ -484,6 +490,13 @@ def test_fwd_sequences_longer_than_max_seqlen(d, dtype, H, B):
         ref = pu.reference(pool, q[c:c + m], b, at, 1 / math.sqrt(d))
         pu.check_rows(o[c:c + m], lse[:, c:c + m].t(), ref, t, p_half=pu.HALF[t])
         assert (o[c + m:c + new[b]] == 7).all() and (lse[:, c + m:c + new[b]] == 7).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
+def test_fwd_ranges_of_rows_without_keys(d, dtype):
+    # cut: among long sequences, prompts longer than their keys, and sequences without keys
+    lens = [9000, 3, 0, 40, 5000, 0]
+    run_fwd((4, 40, 30, 60, 1, 1), None, 8, 2, d, dtype, 16, lens=lens)
 
 
 def test_fwd_repeats_and_replays_bit_for_bit():

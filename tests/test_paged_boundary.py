@@ -173,7 +173,7 @@ def test_fwd_cache_rejects(lib, kw, code):
     (dict(cu=8 * M + 2), MISALIGNED), (dict(L=7 * M + 1), MISALIGNED), (dict(O=5 * M + 4096), INVALID),
     (dict(O=M), INVALID), (dict(L=2 * M + 64), INVALID), (dict(O=3 * M), INVALID),
     (dict(L=4 * M), INVALID), (dict(L=8 * M), INVALID), (dict(L=6 * M + 64), INVALID),
-    (dict(max_len=(1 << 27) + 1), UNSUPPORTED), (dict(B=65536), UNSUPPORTED),
+    (dict(max_len=(1 << 27) + 1), UNSUPPORTED), (dict(B=1 << 30), UNSUPPORTED),
     (dict(scale=3e38), INVALID),
     (dict(ws=11 * M, ws_bytes=64), INVALID), (dict(ws=11 * M + 8, ws_bytes=1 << 30), MISALIGNED),
     (dict(ws=6 * M, ws_bytes=1 << 30), INVALID), (dict(ws=2 * M, ws_bytes=1 << 30), INVALID),
@@ -184,12 +184,13 @@ def test_fwd_rejects(lib, kw, code):
 
 def test_fwd_workspace_size(lib):
     f = lib.fa_fwd_paged_workspace_size
-    # 3 sequences x 2 blocks of 4 packed heads x 1 tile of 256 rows: 152 // 6 = 25 ranges of
-    # 3 x 20 x 8 rows of 128 columns and a logsumexp, in fp32, whatever the padded total
-    assert f(3, 20, 8, 2, 128) == 25 * 60 * 8 * 129 * 4
-    # at d = 64 tiles of 128 rows, two CTAs on each SM
-    assert f(3, 40, 8, 2, 64) == (304 // 12) * 120 * 8 * 65 * 4
-    assert f(4, 1024, 32, 8, 128) == 0                        # tiles enough
+    # a header of 6 ints for each of 152 CTAs, and two tiles of 256 rows of 128 columns and a
+    # logsumexp, in fp32; at d = 64 tiles of 128 rows, two CTAs on each SM
+    ws = 152 * (24 + 2 * 256 * 129 * 4)
+    assert f(3, 20, 8, 2, 128) == ws
+    assert f(3, 40, 8, 2, 64) == 304 * (24 + 2 * 128 * 65 * 4)
+    assert f(76, 64, 32, 8, 128) == ws and f(77, 64, 32, 8, 128) == 0     # four rounds of tiles
+    assert f(1, 1216, 32, 8, 128) == ws and f(1, 1217, 32, 8, 128) == 0   # one, of long prompts
     assert f(3, 20, 8, 3, 128) == 0 and f(3, 0, 8, 2, 128) == 0
 
 
