@@ -137,6 +137,10 @@ KERNEL_SOURCES = {
     "bwd_dq_kernel": "exact_io_aware_22_gb300/csrc/fa_bwd128.cu",
     "decode_split_kernel": "exact_io_aware_22_gb300/csrc/fa_decode.cu",
     "fwd_fp8_kernel": "exact_io_aware_22_gb300/csrc/fa_fwd8.cu",
+    "append_kernel": "exact_io_aware_22_gb300/csrc/fa_append.cu",
+    "decode_paged_kernel": "exact_io_aware_22_gb300/csrc/fa_decode_paged.cu",
+    "fwd_paged_kernel": "exact_io_aware_22_gb300/csrc/fa_fwd_paged.cu",
+    "fwd1_paged_kernel": "exact_io_aware_22_gb300/csrc/fa_fwd_paged.cu",
 }
 
 
