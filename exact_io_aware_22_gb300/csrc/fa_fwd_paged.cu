@@ -9,11 +9,11 @@
 // d <= 64 a persistent one, two CTAs per SM, one query tile at a time.  Their pipelines are the
 // dense kernels' (TMA producer, one MMA issuer, a softmax thread per query row; S, P and O in
 // tensor memory).  What pages change:
-//   producer   a whole warp.  Each lane looks up the pages of its boxes (the largest power of
-//              two of rows that divides the page size) one tile ahead and loads them; a 128-row
-//              tile lies in shared memory as one box would.  Boxes of absent pages read as
-//              zeros and their keys are masked; V rows past the last key, which may hold
-//              anything, are cleared before the product that reads them (0 x NaN).
+//   producer   a whole warp, or up to three (d = 128).  Each lane looks up the pages of its boxes
+//              (the largest power of two of rows that divides the page size) one tile ahead and
+//              loads them; a 128-row tile lies in shared memory as one box would.  Boxes of
+//              absent pages read as zeros and their keys are masked; V rows past the last key,
+//              which may hold anything, are cleared before the product that reads them (0 x NaN).
 //   tiles      A query tile holds the rows of 2^pack heads that share a K/V head, heads fastest:
 //              the tile of a few new tokens is better filled, K and V pass once for those
 //              heads, and less of a tile lies beyond the diagonal (5 tokens of 4 sequences of
@@ -29,7 +29,7 @@
 //              a CTA for each tile: 355 / 356 us.
 //
 // Bound: at d = 128 the tensor pipe and the exponentials (2 x 2048 tokens on 8192 keys, 32/8
-// heads: 0.338 ms, 1413 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
+// heads: 0.335 ms, 1425 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
 // slots; with few tokens the latency of start, split and join (the 5 tokens above: 18 us for 34 MB
 // of keys), with few tokens on long caches the cache's bytes.
 //
@@ -158,7 +158,7 @@ __device__ __forceinline__ int tile_cost(const Span& s) {
 // A piece of work: KV tiles [j0, j1) of the query tile of one block of packed heads at rows
 // row0 .. of a sequence.
 struct Piece {
-  int base, nr;                                  // the sequence's first token and query rows
+  int b, base, nr;                               // sequence, its first token and query rows
   KeyRows kr;
   int hq, hk, row0, j0, j1;                      // first head, its K/V head, first row
   int part;                                      // place in the workspace, -1: the tile is whole
@@ -286,6 +286,7 @@ struct Work {
   }
   __device__ __forceinline__ Piece piece(const PagedArgs& px, int group) const {
     Piece p;
+    p.b = b;
     p.base = sr.base;
     p.nr = sr.n << px.pack;
     p.kr = kr;
@@ -374,16 +375,17 @@ __device__ __forceinline__ void paged_mask(const PagedArgs& px, int lane, const 
                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                  : "memory");
 }
+// Of `shares` warps (1 or 3), `share` issues every shares-th box.
 template <int D>
 __device__ __forceinline__ void paged_load(const PagedArgs& px, const CUtensorMap* map,
                                            uint32_t dst, uint32_t bar, int hk, int lane,
-                                           const PagedTile& t) {
+                                           const PagedTile& t, int share = 0, int shares = 1) {
   using C = Cfg<D>;
   const int n_box = BN >> px.box_log2;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int bx = lane + 32 * i;
-    if (bx < n_box) {
+    if (bx < n_box && (shares == 1 || bx % 3 == share)) {
       const int w = paged_in_pool(px, t.id[i]) ? t.id[i] : px.pg.pages;   // past the pool: zeros
 #pragma unroll
       for (int c = 0; c < C::NCHUNK; ++c)
@@ -516,6 +518,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto B_PF = [&](int t) { return 3 + 4 * C::STAGES + t; };
   auto B_OF = [&](int t) { return 5 + 4 * C::STAGES + t; };
   const int B_DONE = 7 + 4 * C::STAGES, B_QE = B_DONE + 1;
+  // Producers: issuing a box takes a warp about 50 cycles, small ones more in all than the products
+  // take.  Boxes of 32 rows and more: warp 0 alone; of 16: warp 2 issues V's; of 8 and fewer: warps
+  // 0, 2 and 3 a third of them each.  One / two / three warps, 2 x 1024 tokens on 4096 keys: pages
+  // of 32 rows 94.7 / 96.2 / 101.6 us, of 16 105 / 96.5 / 100.6, of 8 152 / - / 103, of one
+  // 820 / - / 341; 5 tokens of 16 sequences of 16384-32768 keys, pages of 16: 306 / 257 / 308.
+  const int producers = px.box_log2 <= 3 ? 3 : px.box_log2 == 4 ? 2 : 1;
   auto B_TF = [&](int k) { return B_DONE + 2 + (k & 1); };
   auto B_TE = [&](int k) { return B_DONE + 4 + (k & 1); };
 
@@ -523,7 +531,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!RANGES) *const_cast<Piece*>(info(0)) = mine;
     for (int i = 0; i < C::NBARS; ++i) mbar_init(bar(i), 1);
     for (int t = 0; t < NT; ++t) mbar_init(bar(B_PF(t)), 128);
-    for (int k = 0; k < 2; ++k) mbar_init(bar(B_TE(k)), 9);   // the MMA thread, 8 softmax warps
+    // readers of a piece: the MMA thread, 8 softmax warps, and the other producers
+    for (int k = 0; k < 2; ++k) mbar_init(bar(B_TE(k)), 8 + producers);
     fence_mbar_init();
   }
   PagedTile first_tile;                         // its look-up passes under the set-up
@@ -587,12 +596,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             paged_mask(px, lane, cur, sb + C::MASK_OFF + (g % kMaskSlots) * 16);
             if (lane == 0) mbar_arrive_expect_tx(bar(B_KF(s)), C::TILE_BYTES);
             __syncwarp();
-            paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), p.hk, lane, cur);
+            paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), p.hk, lane, cur,
+                          0, producers == 3 ? 3 : 1);
             ++nk;
+            if (producers == 2) continue;
             if (!(ok = mbar_wait_warp(bar(B_VE(s)), ph ^ 1, ctl))) break;
             if (lane == 0) mbar_arrive_expect_tx(bar(B_VF(s)), C::TILE_BYTES);
             __syncwarp();
-            paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), p.hk, lane, cur);
+            paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), p.hk, lane, cur,
+                          0, producers);
             ++nv;
           }
           if (!ok) break;
@@ -866,6 +878,51 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     regs_dec<kRegsLow>();
+    // ------------------------------------------------------------ further producers
+    if (warp <= producers) {
+      bool ok = true;
+      int g = 0, nk = 0, nv = 0;
+      for (int k = 0;; ++k) {
+        if (RANGES && !(ok = mbar_wait_warp(bar(B_TF(k)), (k >> 1) & 1, ctl))) break;
+        const volatile Piece& p = *info(k);
+        if (p.nr < 0) break;
+        const KeyRows kr = {p.kr.n, p.kr.off, p.kr.hi};
+        const int b = p.b, hk = p.hk, j0 = p.j0, j1 = p.j1;
+        if (RANGES) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_TE(k)));
+        }
+        PagedTile next;
+        if (j0 < j1) paged_fetch(px, b, kr, j0 * BN, lane, next);
+        for (int j = j0; j < j1; ++j, ++g) {
+          const int s = g % C::STAGES;
+          const uint32_t ph = (g / C::STAGES) & 1;
+          const PagedTile cur = next;
+          if (j + 1 < j1) paged_fetch(px, b, kr, (j + 1) * BN, lane, next);
+          // of three producers warp 0 announces the bytes, which may come before: the phase lasts
+          // until it has
+          if (producers == 3) {
+            if (!(ok = mbar_wait_warp(bar(B_KE(s)), ph ^ 1, ctl))) break;
+            paged_load<D>(px, &tmK, sb + C::K_OFF + s * C::TILE_BYTES, bar(B_KF(s)), hk, lane, cur,
+                          warp - 1, 3);
+            ++nk;
+          }
+          if (!(ok = mbar_wait_warp(bar(B_VE(s)), ph ^ 1, ctl))) break;
+          if (producers == 2 && lane == 0) mbar_arrive_expect_tx(bar(B_VF(s)), C::TILE_BYTES);
+          __syncwarp();
+          paged_load<D>(px, &tmV, sb + C::V_OFF + s * C::TILE_BYTES, bar(B_VF(s)), hk, lane, cur,
+                        producers == 3 ? warp - 1 : 0, producers == 3 ? 3 : 1);
+          ++nv;
+        }
+        if (!RANGES || !ok) break;
+      }
+      if (!ok) {                                   // as warp 0
+        for (int i = max(0, nk - C::STAGES); i < nk; ++i)
+          mbar_wait_warp(bar(B_KF(i % C::STAGES)), (i / C::STAGES) & 1, ctl);
+        for (int i = max(0, nv - C::STAGES); i < nv; ++i)
+          mbar_wait_warp(bar(B_VF(i % C::STAGES)), (i / C::STAGES) & 1, ctl);
+      }
+    }
     // ------------------------------------------------------------ rows without keys
     if (RANGES)
       rows_without_keys<NT, D>(px, cu_seqlens, N, H, total, static_cast<uint16_t*>(Out), Lout,

@@ -432,6 +432,8 @@ FWD = [
     ((5, 1, 0, 30, 3) * 13, (1, 7000, 300, 40, 0) * 13, 16, 4, 64, "fp16", 16, dict(window=6000)),
     ((300, 2, 40), (8000, 60, 5), 12, 3, 128, "fp16", 16, dict(pad=(2, 3))),
     ((300, 2, 40), (8000, 60, 5), 12, 3, 32, "bf16", 16, dict(causal=False)),
+    ((30, 2, 40), (8000, 60, 5), 12, 3, 128, "bf16", 8, {}),             # several producers
+    ((4, 90), (9000, 30), 4, 1, 128, "fp16", 1, dict(layout="nhd")),
 ]
 
 
