@@ -151,6 +151,13 @@ constexpr int kTileCost = 2;
 // about as long as one.  5 tokens of 16 sequences, whole / cut: 500-2000 keys 31 / 33.5 us,
 // 4096-8192 keys 94 / 79; 8 x 128 tokens on 8192 keys 106 / 129.
 constexpr int kJoinCost = 8;
+__host__ __device__ constexpr int join_cost(int rows) { return kJoinCost + rows / 16; }
+// What cutting saves a call of `tiles` query tiles: whole ones take as long as the longest, or
+// where there are more of them than the `ranges` CTAs, end about half of it apart.
+__host__ __device__ constexpr long long cut_saves(long long tiles, int ranges, int longest,
+                                                  int mean) {
+  return tiles <= ranges ? longest - mean : longest / 2;
+}
 __device__ __forceinline__ int tile_cost(const Span& s) {
   return s.hi > s.lo ? s.hi - s.lo + kTileCost : 0;
 }
@@ -218,12 +225,9 @@ struct Work {
       if (lane >= w) incl += o;
     }
     const int sum = __shfl_sync(0xffffffffu, incl, 31);
-    // What cutting saves: whole tiles take as long as the longest, or where there are more of
-    // them than CTAs, end about half of it apart.  What it costs: the join, and more the more
-    // rows it has to move.
     most = __reduce_max_sync(0xffffffffu, most) / blocks;
-    const int saves = n_i * blocks <= px.ranges ? most - sum / px.ranges : most / 2;
-    cut = saves > kJoinCost + min(N << px.pack, ROWS) / 16;
+    cut = cut_saves(n_i * blocks, px.ranges, most, sum / px.ranges) >
+          join_cost(min(N << px.pack, ROWS));
     if (!cut) {
       if (lane == 0 && cta < px.ranges) px.hdr[cta].rows = 0;
       whole(px, cu, N, H, total, cta);
@@ -1601,17 +1605,20 @@ FwdPagedPlan fwd_paged_plan(int B, int H, int Hkv, int max_seqlen, int d) {
   const int pack = fwd_paged_pack(H / Hkv), rows = d == 128 ? NT * BM : BM;
   const int slots = d == 128 ? 152 : 304;
   const long long n_qt = ((static_cast<long long>(max_seqlen) << pack) + rows - 1) / rows;
-  FwdPagedPlan p = {static_cast<long long>(B) * (H >> pack) * n_qt, 0, 0};
+  const long long r = static_cast<long long>(max_seqlen) << pack;
+  FwdPagedPlan p = {static_cast<long long>(B) * (H >> pack) * n_qt, 0,
+                    static_cast<int>(r < rows ? r : rows), 0};
   if (p.tiles > (n_qt == 1 ? 4 : 1) * slots) return p;
   p.ranges = slots;
   p.ws_bytes = hdr_bytes(slots) + 2 * sizeof(float) * slots * rows * (d + 1);
   return p;
 }
 
-// Not for rows of up to four KV tiles, and not where the tiles' lengths may not add up in 32 bits.
+// Not where the longest tile possible is too short, nor where the lengths may not add up in 32 bits.
 bool fwd_paged_may_cut(const FwdPagedPlan& p, long long keys) {
-  const long long most = (keys + BN - 1) / BN;
-  return p.ranges > 0 && most > 4 && p.tiles * (most + kTileCost) <= 0x7fffffffLL;
+  const long long most = (keys + BN - 1) / BN + kTileCost;
+  return p.ranges > 0 && p.tiles * most <= 0x7fffffffLL &&
+         cut_saves(p.tiles, p.ranges, static_cast<int>(most), 0) > join_cost(p.rows);
 }
 
 cudaError_t launch_fwd_paged(const FwdArgs& args, int d, bool bf16, bool causal, cudaStream_t st) {

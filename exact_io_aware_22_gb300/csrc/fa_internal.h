@@ -123,7 +123,7 @@ int fwd_paged_pack(int group);
 // Query tiles of a paged call, and the CTAs that may share their KV tiles, with their workspace.
 struct FwdPagedPlan {
   long long tiles;
-  int ranges;
+  int ranges, rows;            // CTAs; rows of a tile that are used, at most
   size_t ws_bytes;
 };
 FwdPagedPlan fwd_paged_plan(int B, int H, int Hkv, int max_seqlen, int d);
