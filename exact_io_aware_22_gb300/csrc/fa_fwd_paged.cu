@@ -88,6 +88,9 @@ __device__ __forceinline__ uint32_t kmajor_koff(int kk) {
 
 // The query tile that range x shares with range x - 1: its sequence's first token, its first head,
 // first row and rows (0: there is none), and the first and last range that have parts of it.
+// Range 0 shares none; its header's `base` says whether the call is cut at all, and where it is
+// not, no other header is written: at d <= 64 a CTA that has not started may be cancelled and its
+// tile taken by another.  So every CTA that starts stores it, before anything that may fail.
 struct RangeHeader {
   int base, hq, row0, rows, c0, c1;
 };
@@ -229,7 +232,7 @@ struct Work {
     cut = cut_saves(n_i * blocks, px.ranges, most, sum / px.ranges) >
           join_cost(min(N << px.pack, ROWS));
     if (!cut) {
-      if (lane == 0 && cta < px.ranges) px.hdr[cta].rows = 0;
+      if (lane == 0) px.hdr[0].base = 0;
       whole(px, cu, N, H, total, cta);
       return cta < n_i * blocks;
     }
@@ -238,7 +241,7 @@ struct Work {
     const int x0 = static_cast<int>(min(static_cast<long long>(cta) * per_cta,
                                         static_cast<long long>(sum)));
     const int x1 = x0 + min(per_cta, sum - x0);
-    RangeHeader h = {};
+    RangeHeader h = {cta == 0, 0, 0, 0, 0, 0};
     if (x0 < x1) {
       const bool here = incl > x0 && incl - mine <= x0;            // one lane has position x0
       int at = incl - mine, i = lane * per;
@@ -1043,7 +1046,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
     grid_dep_wait();
     if (threadIdx.x == 0) {
       atomicOr(ctl.status, FA_DEV_SMEM_ALIGN);
-      if (static_cast<int>(blockIdx.x) < px.ranges) px.hdr[blockIdx.x].rows = 0;
+      if (px.ranges) px.hdr[0].base = 0;
     }
     return;
   }
@@ -1500,8 +1503,9 @@ __global__ void __launch_bounds__(MERGE_THREADS)
     fwd_paged_merge_kernel(void* Out, float* Lout, int H, int total, const PagedArgs px) {
   constexpr int ROWS = TILES * BM, WARPS = MERGE_THREADS / 32;
   grid_dep_wait();                               // the pieces' results
+  const int cut = px.hdr[0].base;
   const RangeHeader hd = px.hdr[blockIdx.x];
-  if (hd.rows == 0) return;
+  if (cut == 0 || hd.rows == 0) return;          // not cut: the other headers are not written
   const int lane = threadIdx.x & 31, n_sl = hd.c1 - hd.c0, used = n_sl + 1;
   const int first = ((static_cast<int>(blockIdx.x) - hd.c0 - 1) * static_cast<int>(gridDim.y) +
                      static_cast<int>(blockIdx.y)) * WARPS + (static_cast<int>(threadIdx.x) >> 5);
