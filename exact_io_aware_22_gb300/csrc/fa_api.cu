@@ -1053,7 +1053,7 @@ fa_status fwd_paged_impl(const void* Q, const fa_paged_cache* cache, void* O, fl
   a.L = L;
   a.N = max_seqlen;
   a.group = H / Hkv;
-  a.window = window < (1 << 30) ? window : 0;   // no cache holds more keys
+  a.window = window;
   a.box_log2 = lg;
   a.B = B;
   a.pack = pack;

@@ -154,7 +154,7 @@ __device__ __forceinline__ float weight(float m, float ref) {
 }
 
 // Keys [lo, n) of a sequence are attended; its units start at key a0 = lo rounded down to
-// whole stages.
+// whole stages.  A window counts from the length as it is given, and may lie past the table.
 struct SeqKeys {
   int lo, n, a0, units;
 };
@@ -162,10 +162,11 @@ template <int KEYS, int UNIT>
 __device__ __forceinline__ SeqKeys seq_keys(const PagedView& pg, int b, int window) {
   const long long cap = static_cast<long long>(pg.max_pages) * pg.page.div;
   SeqKeys s;
-  s.n = static_cast<int>(min(static_cast<long long>(max(pg.seqlens[b], 0)), cap));
-  s.lo = window > 0 && window < s.n ? s.n - window : 0;
+  const int len = max(pg.seqlens[b], 0);
+  s.n = static_cast<int>(min(static_cast<long long>(len), cap));
+  s.lo = window > 0 && window < len ? len - window : 0;
   s.a0 = s.lo & ~(KEYS - 1);
-  s.units = (s.n - s.a0 + UNIT - 1) / UNIT;
+  s.units = s.lo < s.n ? (s.n - s.a0 + UNIT - 1) / UNIT : 0;
   return s;
 }
 
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     }
     __syncthreads();
     for (int b = blockIdx.x; b < B; b += gridDim.x)
-      if (pg.seqlens[b] <= 0) empty_heads(b, 0, H);
+      if (seq_keys<KEYS, G::UNIT>(pg, b, window).units == 0) empty_heads(b, 0, H);
     if (x0 >= x1) {
       if (threadIdx.x == 0) hdr[blockIdx.x].row = -1;
       return;

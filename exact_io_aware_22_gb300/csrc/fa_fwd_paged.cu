@@ -96,7 +96,7 @@ struct RangeHeader {
 };
 struct PagedArgs {
   PagedView pg;
-  int box_log2, causal, window;    // window: kNoLimit for none
+  int box_log2, causal, window;    // window: 0 for none
   int pack;                        // log2 of the heads in a query tile
   int B, n_qt;                     // sequences, query tiles of the longest
   int ranges;                      // CTAs that may share the KV tiles of all query tiles (0: none)
@@ -104,30 +104,34 @@ struct PagedArgs {
   float* part;                     // [2 * ranges][rows of a query tile][D] results of pieces
   float* part_l;                   // [2 * ranges][rows of a query tile] their L (natural log)
 };
-constexpr int kNoLimit = 1 << 30;
-// Keys of a sequence with nq query rows: query row i is at key position i + off and sees keys
-// up to i + hi (all of them unless causal) and from i + off - window + 1.
+constexpr int kNoLimit = 1 << 30;  // no table has room for more keys
+// Keys of a sequence: query row i sees keys i + lo up to i + hi of its n.
 struct KeyRows {
-  int n, off, hi;
+  int n, lo, hi;
 };
 // Query and key rows of sequence b; the three loads go out together.
 __device__ __forceinline__ void rows_of(const PagedArgs& px, const int* cu, int b, int N,
                                         int total, SeqRows& sr, KeyRows& k) {
-  const int c0 = cu[b], c1 = cu[b + 1], len = px.pg.seqlens[b];
+  const int c0 = cu[b], c1 = cu[b + 1], len = max(px.pg.seqlens[b], 0);
   const int a = min(max(c0, 0), total), e = min(max(c1, a), total);
   sr = {a, min(e - a, N), true};
   const long long cap = static_cast<long long>(px.pg.max_pages) * px.pg.page.div;
-  k.n = static_cast<int>(min(static_cast<long long>(max(len, 0)), cap));
-  k.off = k.n - (e - a);                         // rows past N are left out, the others stay
-  k.hi = px.causal ? k.off : kNoLimit;
+  k.n = static_cast<int>(min(static_cast<long long>(len), cap));
+  // Row i is at position i + off, which goes by the length and the offsets as they are given: rows
+  // past N and keys past the table are left out, the others stay where they are.  Rows are below
+  // 2^29 (the call refuses more), so sums with the limits stay in 32 bits.
+  const long long none = kNoLimit, off = static_cast<long long>(len) - c1 + a;
+  const long long lo = px.window > 0 ? off - px.window + 1 : -none;
+  k.lo = static_cast<int>(max(min(lo, none), -none));
+  k.hi = px.causal ? static_cast<int>(min(off, none)) : kNoLimit;
 }
 // KV tiles [lo, hi) of the query tile at rows r .. r + BM - 1 of a sequence's nr; row i is
 // a head of query i >> pack.
-__device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nr, int window, int pack,
-                                            int& lo, int& hi) {
+__device__ __forceinline__ void paged_tiles(const KeyRows& k, int r, int nr, int pack, int& lo,
+                                            int& hi) {
   const int last = (min(r + BM - 1, nr - 1) >> pack) + k.hi;
   hi = r >= nr || last < 0 ? 0 : min((k.n + BN - 1) / BN, last / BN + 1);
-  lo = min(max(0, (r >> pack) + k.off - window + 1) / BN, hi);
+  lo = min(max(0, (r >> pack) + k.lo) / BN, hi);
 }
 // KV tiles [lo, hi) of a query tile of TILES * BM rows from row r.
 struct Span {
@@ -136,11 +140,11 @@ struct Span {
 template <int TILES>
 __device__ __forceinline__ Span tile_span(const PagedArgs& px, const KeyRows& k, int r, int nr) {
   Span s;
-  paged_tiles(k, r, nr, px.window, px.pack, s.lo, s.hi);
+  paged_tiles(k, r, nr, px.pack, s.lo, s.hi);
 #pragma unroll
   for (int t = 1; t < TILES; ++t) {
     int lo, hi;
-    paged_tiles(k, r + t * BM, nr, px.window, px.pack, lo, hi);
+    paged_tiles(k, r + t * BM, nr, px.pack, lo, hi);
     if (hi > s.hi) s.hi = hi;                    // lo rises with the row
   }
   return s;
@@ -406,13 +410,12 @@ __device__ __forceinline__ void paged_load(const PagedArgs& px, const CUtensorMa
 struct RowKeys {
   int lo, lim, past, full;
 };
-__device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row, int pack,
-                                            int window) {
+__device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row, int pack) {
   RowKeys r;
   r.lim = min((row >> pack) + k.hi + 1, k.n);
-  r.lo = (row >> pack) + k.off - window + 1;
+  r.lo = (row >> pack) + k.lo;
   r.full = min((row0 >> pack) + k.hi + 1, k.n);
-  r.past = ((row0 + BM - 1) >> pack) + k.off - window + 1;
+  r.past = ((row0 + BM - 1) >> pack) + k.lo;
   return r;
 }
 // A KV tile's mask in the ring, a bit per key whose page is there.  The d = 128 kernel reads it
@@ -509,8 +512,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   // KV tiles [lo, hi) of Q tile t that a piece has
   auto tiles_of = [&](const volatile Piece& p, int t, int& lo, int& hi) {
-    const KeyRows kr = {p.kr.n, p.kr.off, p.kr.hi};
-    paged_tiles(kr, p.row0 + t * BM, p.nr, px.window, pack, lo, hi);
+    const KeyRows kr = {p.kr.n, p.kr.lo, p.kr.hi};
+    paged_tiles(kr, p.row0 + t * BM, p.nr, pack, lo, hi);
     lo = min(max(lo, p.j0), p.j1);
     hi = min(max(hi, p.j0), p.j1);
   };
@@ -751,9 +754,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       tiles_of(p, t, lo, hi);
       const int nt = hi - lo, g0 = g + lo - p.j0;   // this tile's KV tiles, its first step
       const int Nk = p.kr.n;
-      const KeyRows kr = {Nk, p.kr.off, p.kr.hi};
+      const KeyRows kr = {Nk, p.kr.lo, p.kr.hi};
       const int tile_row0 = p.row0 + t * BM;
-      const RowKeys rk = row_keys(kr, tile_row0, tile_row0 + rit, pack, px.window);
+      const RowKeys rk = row_keys(kr, tile_row0, tile_row0 + rit, pack);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = mbar_wait_warp(bar(B_SF(t)), (ns + j) & 1, ctl))) break;
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (RANGES && !(ok = mbar_wait_warp(bar(B_TF(k)), (k >> 1) & 1, ctl))) break;
         const volatile Piece& p = *info(k);
         if (p.nr < 0) break;
-        const KeyRows kr = {p.kr.n, p.kr.off, p.kr.hi};
+        const KeyRows kr = {p.kr.n, p.kr.lo, p.kr.hi};
         const int b = p.b, hk = p.hk, j0 = p.j0, j1 = p.j1;
         if (RANGES) {
           __syncwarp();
@@ -1294,7 +1297,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (tile < 0) break;
       const Piece* ti = info(k & 1);
       const int lo = ti->j0, nt = ti->j1 - lo, row0 = ti->row0, Nk = ti->kr.n;
-      const RowKeys rk = row_keys(ti->kr, row0, row0 + rit, pack, px.window);
+      const RowKeys rk = row_keys(ti->kr, row0, row0 + rit, pack);
       const int grow = row0 + rit;               // query row
       // where a row lies in O, in the workspace, and in L or the workspace's L
       auto row_at = [&](int r) -> size_t {
@@ -1628,7 +1631,6 @@ bool fwd_paged_may_cut(const FwdPagedPlan& p, long long keys) {
 cudaError_t launch_fwd_paged(const FwdArgs& args, int d, bool bf16, bool causal, cudaStream_t st) {
   FwdArgs a = args;
   a.causal = causal;
-  if (!causal || a.window == 0) a.window = kNoLimit;
   a.BH = a.B * (a.H >> a.pack);
   return bf16 ? launch_fwd_paged_b<true>(a, d, st) : launch_fwd_paged_b<false>(a, d, st);
 }

@@ -239,9 +239,11 @@ fa_status fa_decode_fp8(const void* Q, const void* Kc8, const void* Vc8, const i
  * page_size, d), (pages, page_size, Hkv, d) and halves of one common pool all fit.
  *   page_table     device int32 [B][max_pages], rows table_stride entries apart.  Pages may be
  *                  shared by sequences that only read them.
- *   cache_seqlens  device int32 [B]: keys of each sequence, clamped to [0, max_pages *
- *                  page_size].  For the calls that bring new tokens it counts these in: the
- *                  new tokens are the sequence's last keys.
+ *   cache_seqlens  device int32 [B]: keys of each sequence; a negative length is 0.  For the
+ *                  calls that bring new tokens it counts these in: the new tokens are the
+ *                  sequence's last keys.  Of a length beyond max_pages * page_size the keys
+ *                  past the table do not exist, and the others keep their positions: new
+ *                  tokens, queries and windows stand where the length puts them.
  *   A page id outside [0, pages) stands for an absent page: its keys are not attended (a
  *   sliding window's dropped pages may be marked -1); nothing outside the pools is touched.
  *   Supported: page_size >= 1 (even for d = 32), max_pages * page_size <= 2^30.

@@ -1,5 +1,6 @@
-"""Calls on paged caches at the edges of what they document: offsets that break the rules inside
-guarded tensors.  Against the definitions in 64 bits (tests/paged_util.py)."""
+"""Calls on paged caches at the edges of what they document: lengths past the table, offsets that
+break the rules inside guarded tensors.  Against the definitions in 64 bits
+(tests/paged_util.py)."""
 import math
 
 import pytest
@@ -22,6 +23,93 @@ def ok():
 
 def ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ lengths past the table
+@gpu
+@pytest.mark.parametrize("window", [0, 33])
+@pytest.mark.parametrize("d,dtype,H", [(128, "bf16", 8), (64, "fp16", 8), (32, "bf16", 2)])
+def test_lengths_past_the_table_keep_positions(d, dtype, H, window):
+    """Sequences of which the table holds only the first keys: the tokens that fit are appended
+    at the positions their length gives them, and queries, those of the others among them, see
+    the keys that a window and the causal order leave them of those."""
+    fa = fa_()
+    Hkv, page, room, t = 2, 16, 80, pu.DT[dtype]
+    lens, new = [95, 80, 85, 400, 60], [40, 9, 3, 30, 1]
+    held = [min(n, room) for n in lens]
+    pool = pu.Pool(held, Hkv, d, page, dtype, width=room // page)
+    kc, vc, tb, _ = pool.cuda()
+    sl, starts = ints(lens), [sum(new[:i]) for i in range(6)]
+    cu = ints(starts)
+    total = sum(new)
+    g = torch.Generator().manual_seed(d)
+    q, k, v = (torch.randn((total, n, d), generator=g).to(t).cuda() for n in (H, Hkv, Hkv))
+    torch.cuda.synchronize()
+    fa.device_status()
+    fa.append_paged(k, v, kc, vc, tb, sl, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 1                 # tokens without a place
+    pool.kc, pool.vc = kc.cpu(), vc.cpu()
+    for b in range(5):
+        for i in range(new[b]):
+            p = lens[b] - new[b] + i
+            if p < room:
+                at = int(pool.table[b, p // page])
+                assert torch.equal(pool.kc[at, :, p % page], k[starts[b] + i].cpu())
+    o, lse = fa.fwd_paged(q, kc, vc, tb, sl, cu, max(new), window=window)
+    last = torch.tensor(starts[1:], device="cuda") - 1
+    od, ld = fa.decode_paged(q[last], kc, vc, tb, sl, window=window)
+    ok()
+    for b in range(5):
+        c, m = starts[b], new[b]
+        at = torch.arange(lens[b] - m, lens[b])
+        ref = pu.reference(pool, q[c:c + m].cpu(), b, at, 1 / math.sqrt(d), window=window)
+        pu.check_rows(o[c:c + m], lse[:, c:c + m].t(), ref, t, p_half=pu.HALF[t])
+        ref = pu.reference(pool, q[c + m - 1:c + m].cpu(), b, at[-1:], 1 / math.sqrt(d), window=window)
+        pu.check_rows(od[b:b + 1], ld[b:b + 1], ref, t)
+
+
+@gpu
+@pytest.mark.parametrize("cache", ["16", "e4m3"])
+@pytest.mark.parametrize("width", [4, 400])
+def test_decode_windows_past_the_table(cache, width):
+    # rows whole and cut; windows that reach back into the table's keys or do not
+    fa = fa_()
+    page, d, H, Hkv = 16, 128, 8, 2
+    room = width * page
+    lens = [room + 10, room + 70, room - 3, 2 ** 31 - 1, 0]
+    pool = pu.Pool([min(n, room) for n in lens], Hkv, d, page, "e4m3" if cache == "e4m3" else "bf16")
+    assert pool.width == width
+    kc, vc, tb, _ = pool.cuda()
+    q = torch.randn((5, H, d), generator=torch.Generator().manual_seed(1)).bfloat16()
+    for window in (40, 70, 2 ** 31 - 1):
+        if cache == "e4m3":
+            o, lse = fa.decode_paged_fp8(q.cuda(), kc, vc, tb, ints(lens), *pool.scales, window=window)
+        else:
+            o, lse = fa.decode_paged(q.cuda(), kc, vc, tb, ints(lens), window=window)
+        ok()
+        for b, n in enumerate(lens):
+            ref = pu.reference(pool, q[b:b + 1], b, torch.tensor([n - 1]), 1 / math.sqrt(d), window=window)
+            pu.check_rows(o[b:b + 1], lse[b:b + 1], ref, torch.bfloat16)
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
+@pytest.mark.parametrize("window", [0, 1 << 30, 2 ** 31 - 1])
+def test_fwd_lengths_near_32_bits(d, dtype, window):
+    # every key of the table is earlier than every query; the longest window leaves the first some
+    fa = fa_()
+    pool = pu.Pool([64, 64, 64], 2, d, 16, dtype)
+    kc, vc, tb, _ = pool.cuda()
+    lens, new = [2 ** 31 - 1, 2 ** 30 + 40, 64], [200, 70, 5]
+    cu = [0, 200, 270, 275]
+    q = torch.randn((275, 4, d), generator=torch.Generator().manual_seed(2)).to(pu.DT[dtype])
+    o, lse = fa.fwd_paged(q.cuda(), kc, vc, tb, ints(lens), ints(cu), 200, window=window)
+    ok()
+    for b, (n, m) in enumerate(zip(lens, new)):
+        rows = slice(cu[b], cu[b] + m)
+        ref = pu.reference(pool, q[rows], b, torch.arange(n - m, n), 1 / math.sqrt(d), window=window)
+        pu.check_rows(o[rows], lse[:, rows].t(), ref, pu.DT[dtype], p_half=pu.HALF[pu.DT[dtype]])
 
 
 # ------------------------------------------------------------------ offsets that break the rules
