@@ -837,7 +837,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!(ok = mbar_wait_warp(bar(B_OF(t)), no & 1, ctl))) break;
         ++no;
         tc_fence_after();
-        const bool none = l_run == 0.f;            // a row whose keys are all masked: acc = 0
+        // a row whose keys are all masked: 0, whatever its tiles' values (0 x NaN) left in acc
+        const bool none = l_run == 0.f;
         const float inv_l = none ? 0.f : 1.f / l_run;
         const bool valid = grow < Nr;
 #pragma unroll
@@ -859,8 +860,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
-                               __uint_as_float(o[2 * i + 1]) * inv_l);
+            w[i] = none ? 0u
+                        : pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
+                                      __uint_as_float(o[2 * i + 1]) * inv_l);
           if (valid) {
             uint4* dst =
                 reinterpret_cast<uint4*>(reinterpret_cast<T*>(Out) + row_at * D + 32 * cc);
@@ -1413,7 +1415,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       tc_fence_after();
       const int Nr = ti->nr;
       const bool shared = ti->part >= 0;
-      const bool none = l_run == 0.f;            // a row whose keys are all masked: acc = 0
+      const bool none = l_run == 0.f;            // as in the d = 128 kernel: O = 0
       const float inv_l = none ? 0.f : 1.f / l_run;
       const bool valid = grow < Nr;
       // Each thread writes its row of O (16-bit) to this warp's 32 staging rows in shared
@@ -1441,8 +1443,9 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
-                             __uint_as_float(o[2 * i + 1]) * inv_l);
+          w[i] = none ? 0u
+                      : pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
+                                    __uint_as_float(o[2 * i + 1]) * inv_l);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           stage[lane * CPR + ((4 * cc + i) ^ (lane % CPR))] =

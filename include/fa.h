@@ -347,9 +347,9 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
  *            aligned), or NULL: allocated and freed on `stream`.  0 bytes, and then unused,
  *            where there are query rows enough to fill the GPU without splitting the keys.  Its
  *            contents do not matter before a call.
- *   A V element that is not finite reaches the query rows of its 128-key tile even where the
- *   causal mask or the window hides its key (0 x NaN), as in fa_fwd; what lies in absent pages
- *   and past the last key never does.
+ *   A V element that is not finite reaches the query rows of its 128-key tile that have keys even
+ *   where the causal mask or the window hides its key (0 x NaN), as in fa_fwd; what lies in absent
+ *   pages and past the last key never does, and rows without keys are 0 whatever the tile holds.
  *   Errors   as for the cache and fa_fwd_varlen, FA_ERR_INVALID_VALUE for a scale that times
  *            log2(e) overflows or vanishes in fp32; FA_ERR_UNSUPPORTED for more than 2^29 rows of
  *            one sequence's heads that share a tile (max_seqlen times the largest power of two

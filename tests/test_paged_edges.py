@@ -1,6 +1,6 @@
-"""Calls on paged caches at the edges of what they document: lengths past the table, offsets that
-break the rules inside guarded tensors.  Against the definitions in 64 bits
-(tests/paged_util.py)."""
+"""Calls on paged caches at the edges of what they document: lengths past the table, rows without
+keys beside values that are not finite, offsets that break the rules inside guarded tensors.
+Against the definitions in 64 bits (tests/paged_util.py)."""
 import math
 
 import pytest
@@ -110,6 +110,37 @@ def test_fwd_lengths_near_32_bits(d, dtype, window):
         rows = slice(cu[b], cu[b] + m)
         ref = pu.reference(pool, q[rows], b, torch.arange(n - m, n), 1 / math.sqrt(d), window=window)
         pu.check_rows(o[rows], lse[:, rows].t(), ref, pu.DT[dtype], p_half=pu.HALF[pu.DT[dtype]])
+
+
+# ------------------------------------------------------------------ rows without keys
+@gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16"), (32, "bf16")])
+def test_rows_without_keys_beside_values_that_are_not_finite(d, dtype, bad):
+    """More tokens than keys, and windows that end in absent pages: those rows are 0 whatever the
+    values of keys that other rows of their tile see; tiles whole, and cut beside a long sequence."""
+    fa = fa_()
+    for lens, new in (([30, 9], [70, 20]), ([30, 9, 9000], [70, 20, 2])):
+        pool = pu.Pool(lens, 2, d, 16, dtype)
+        for b in (0, 1):
+            pool.vc[int(pool.table[b, 0]), :, 3] = bad
+        kc, vc, tb, sl = pool.cuda()
+        cu = ints([sum(new[:i]) for i in range(len(new) + 1)])
+        q = torch.randn(sum(new), 4, d, device="cuda").to(pu.DT[dtype])
+        o, lse = fa.fwd_paged(q, kc, vc, tb, sl, cu, max(new))
+        ok()
+        for c, n in ((0, 40), (70, 11)):
+            assert (o[c:c + n] == 0).all() and (lse[:, c:c + n] == -math.inf).all()
+            assert not torch.isfinite(o[c + n + 3:c + (70 if c == 0 else 20)]).any()
+    pool = pu.Pool([100], 2, d, 16, dtype)
+    pool.vc[int(pool.table[0, 0]), :, 3] = bad      # key 3; keys 16 .. 31 are absent
+    pool.table[0, 1] = -1
+    kc, vc, tb, sl = pool.cuda()
+    q = torch.randn(100, 4, d, device="cuda").to(pu.DT[dtype])
+    o, lse = fa.fwd_paged(q, kc, vc, tb, sl, ints([0, 100]), 100, window=5)
+    ok()
+    assert (o[20:32] == 0).all() and (lse[:, 20:32] == -math.inf).all()
+    assert torch.isfinite(lse[:, 32:]).all()
 
 
 # ------------------------------------------------------------------ offsets that break the rules
