@@ -450,7 +450,9 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
     for (int nt = 0; nt < NT; ++nt) {
       if constexpr (C8 && BF16) {
         // bf16 q as f16 after an exact power-of-two scaling that brings the head's largest
-        // magnitude to [1, 2): entries 2^-14 below the largest lose bits, no entry overflows
+        // magnitude to [1, 2), or below 4: no entry overflows, and an entry's 8 bits stay whole
+        // down to 2^-17.  A smaller entry is off by at most 2^-25 (half of f16's least step):
+        // times a code k, less than fp32's rounding of the largest entry times k.
         float mx = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
@@ -461,9 +463,10 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // the power of two at mx: its exponent bits (0 and infinities: no scaling)
+        // the power of two at mx: its exponent bits, up to 2^126, whose reciprocal is a normal
+        // number (0 and infinities: no scaling)
         uint32_t eb = __float_as_uint(mx) & 0x7f800000u;
-        if (eb == 0u || eb >= 0x7e800000u) eb = 0x3f800000u;
+        eb = eb == 0u || eb == 0x7f800000u ? 0x3f800000u : min(eb, 0x7e800000u);
         const float dn = __uint_as_float(0x7f000000u - eb);     // 1 / 2^e
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
@@ -473,8 +476,9 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
             qf[nt][ks][e] = pack2<false>(f.x * dn, f.y * dn);
           }
         // lane 4h holds head h's; never 0, which would make a masked score NaN (the least
-        // normal number in its place moves no score by 2^-100)
-        const float up = fmaxf(__uint_as_float(eb) * c_log2, 0x1p-126f);
+        // normal number in its place moves no score by 2^-100), nor infinite, which would a
+        // score of 0
+        const float up = fminf(fmaxf(__uint_as_float(eb) * c_log2, 0x1p-126f), 0x1.fffffep127f);
         cs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
         cs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
       } else {

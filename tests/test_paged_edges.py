@@ -1,6 +1,6 @@
 """Calls on paged caches at the edges of what they document: lengths past the table, rows without
-keys beside values that are not finite, offsets that break the rules inside guarded tensors.
-Against the definitions in 64 bits (tests/paged_util.py)."""
+keys beside values that are not finite, the largest queries, offsets that break the rules inside
+guarded tensors.  Against the definitions in 64 bits (tests/paged_util.py)."""
 import math
 
 import pytest
@@ -141,6 +141,44 @@ def test_rows_without_keys_beside_values_that_are_not_finite(d, dtype, bad):
     ok()
     assert (o[20:32] == 0).all() and (lse[:, 20:32] == -math.inf).all()
     assert torch.isfinite(lse[:, 32:]).all()
+
+
+# ------------------------------------------------------------------ the largest queries
+@gpu
+@pytest.mark.parametrize("H", [4, 24])
+@pytest.mark.parametrize("e", [125, 126])
+def test_decode_fp8_largest_queries(e, H):
+    # bf16 queries up to the type's largest against codes and scales so small that scores are not
+    pool = pu.Pool((200, 33), 2, 128, 32, "e4m3")
+    small = (pu.e4m3(pool.kc) * pool.scales[0] / 16).to(torch.float8_e4m3fn)
+    pool.kc.copy_(small.view(torch.uint8))
+    pool.scales = (2.0 ** -122, pool.scales[1])
+    scale = 2.0 ** (125 - e)
+    g = torch.Generator().manual_seed(e)
+    top = float(torch.finfo(torch.bfloat16).max)
+    q = (torch.randn((2, H, 128), generator=g) * 2.0 ** e).clamp(-top, top).bfloat16()
+    assert q.isfinite().all() and q.abs().amax(-1).max() >= 2.0 ** (e + 1)
+    kc, vc, tb, sl = pool.cuda()
+    o, lse = fa_().decode_paged_fp8(q.cuda(), kc, vc, tb, sl, *pool.scales, scale=scale)
+    ok()
+    for b, n in enumerate(pool.lens):
+        ref = pu.reference(pool, q[b:b + 1], b, torch.tensor([n - 1]), scale)
+        pu.check_rows(o[b:b + 1], lse[b:b + 1], ref, torch.bfloat16)
+
+
+@gpu
+def test_decode_fp8_zero_keys_under_the_largest_scale():
+    # the scale of the scores overflows, the scores are 0: the mean of the values
+    pool = pu.Pool((70,), 2, 128, 32, "e4m3")
+    pool.kc.masked_fill_(pool.kc != 0x7F, 0)
+    pool.scales = (1.0, pool.scales[1])
+    kc, vc, tb, sl = pool.cuda()
+    for top, scale in ((2.0 ** 127, 8.0), (2.0 ** 100, 2.0 ** 40)):
+        q = torch.full((1, 4, 128), top, dtype=torch.bfloat16)
+        o, lse = fa_().decode_paged_fp8(q.cuda(), kc, vc, tb, sl, *pool.scales, scale=scale)
+        ok()
+        ref = pu.reference(pool, q, 0, torch.tensor([69]), scale)
+        pu.check_rows(o, lse, ref, torch.bfloat16)
 
 
 # ------------------------------------------------------------------ offsets that break the rules
