@@ -1,6 +1,6 @@
 """Calls on paged caches at the edges of what they document: lengths past the table, rows without
-keys beside values that are not finite, the largest queries, offsets that break the rules inside
-guarded tensors.  Against the definitions in 64 bits (tests/paged_util.py)."""
+keys beside values that are not finite, the largest queries, sizes past 32 bits, offsets that break
+the rules inside guarded tensors.  Against the definitions in 64 bits (tests/paged_util.py)."""
 import math
 
 import pytest
@@ -179,6 +179,31 @@ def test_decode_fp8_zero_keys_under_the_largest_scale():
         ok()
         ref = pu.reference(pool, q, 0, torch.tensor([69]), scale)
         pu.check_rows(o, lse, ref, torch.bfloat16)
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+@gpu
+def test_windows_and_bounds_past_32_bits():
+    fa = fa_()
+    pool = pu.Pool((90, 40), 2, 64, 16, "fp16")
+    kc, vc, tb, sl = pool.cuda()
+    q = torch.randn(2, 8, 64, device="cuda").half()
+    cu = ints([0, 1, 2])
+    k = torch.randn(1, 2, 40, 64, device="cuda").half()
+    want = fa.decode_paged(q, kc, vc, tb, sl), fa.fwd_paged(q, kc, vc, tb, sl, cu, 1), fa.fwd(k, k, k)
+    for w in (2 ** 31, 2 ** 32 + 5, 2 ** 40):
+        got = (fa.decode_paged(q, kc, vc, tb, sl, window=w),
+               fa.fwd_paged(q, kc, vc, tb, sl, cu, 1, window=w), fa.fwd(k, k, k, window=w))
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y)), w
+    for w in (-1, -2 ** 31, 5 - 2 ** 32):
+        with pytest.raises((ValueError, fa.FAError)):
+            fa.decode_paged(q, kc, vc, tb, sl, window=w)
+        with pytest.raises((ValueError, fa.FAError)):
+            fa.fwd_paged(q, kc, vc, tb, sl, cu, 1, window=w)
+    for m in (2 ** 31, 2 ** 32 + 1, 1 - 2 ** 32, 0):
+        with pytest.raises((ValueError, fa.FAError)):
+            fa.fwd_paged(q, kc, vc, tb, sl, cu, m)
+    ok()
 
 
 # ------------------------------------------------------------------ offsets that break the rules
