@@ -497,6 +497,13 @@ def _paged_env():
             torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
 
 
+@functools.lru_cache(maxsize=1)
+def _code_dtypes():
+    """What E4M3 codes come as: bytes, or torch's type of that format and no other."""
+    import torch
+    return torch.uint8, torch.float8_e4m3fn
+
+
 def _one_device(*ts) -> int:
     """Index of the one CUDA device of all tensors (None entries aside)."""
     dev = ts[0].get_device()
@@ -556,8 +563,8 @@ def _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B: int, d: int):
     pages, Hkv, page_size, cols = shape
     if cols != d:
         raise ValueError("the caches' rows must have the columns of q, k and v")
-    if t is not v_cache.dtype or (k_cache.element_size() != 1 if dtype is None else t is not dtype):
-        raise TypeError("E4M3 caches must be 1-byte tensors" if dtype is None
+    if t is not v_cache.dtype or (t not in _code_dtypes() if dtype is None else t is not dtype):
+        raise TypeError("E4M3 caches must both be uint8 or float8_e4m3fn" if dtype is None
                         else "the caches must have the dtype of q, k and v")
     if st != v_cache.stride() or st[3] != 1:
         raise ValueError("the caches must share their strides, with contiguous columns")

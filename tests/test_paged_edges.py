@@ -1,6 +1,7 @@
 """Calls on paged caches at the edges of what they document: lengths past the table, rows without
-keys beside values that are not finite, the largest queries, sizes past 32 bits, offsets that break
-the rules inside guarded tensors.  Against the definitions in 64 bits (tests/paged_util.py)."""
+keys beside values that are not finite, the largest queries, sizes past 32 bits, other 1-byte
+types, and offsets that break the rules inside guarded tensors.  Against the definitions in 64
+bits (tests/paged_util.py)."""
 import math
 
 import pytest
@@ -204,6 +205,21 @@ def test_windows_and_bounds_past_32_bits():
         with pytest.raises((ValueError, fa.FAError)):
             fa.fwd_paged(q, kc, vc, tb, sl, cu, m)
     ok()
+
+
+# ------------------------------------------------------------------ types of codes
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.int8, torch.bool])
+def test_python_refuses_other_one_byte_caches(dtype):
+    fa = fa_()
+    t, n = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for good in (torch.uint8, torch.float8_e4m3fn):
+        c = torch.zeros(4, 2, 16, 128, dtype=torch.uint8).view(good)
+        assert fa._paged(c, c.clone(), t, n, None, 2, 128)[1] == 2
+    c = torch.zeros(4, 2, 16, 128, dtype=torch.uint8).view(dtype)
+    with pytest.raises(TypeError):
+        fa._paged(c, c.clone(), t, n, None, 2, 128)
+    with pytest.raises(TypeError):                # one cache right, the other not
+        fa._paged(c.view(torch.uint8), c, t, n, None, 2, 128)
 
 
 # ------------------------------------------------------------------ offsets that break the rules
