@@ -405,18 +405,12 @@ __device__ __forceinline__ void paged_load(const PagedArgs& px, const CUtensorMa
     }
   }
 }
-// Which keys a row of a paged query tile may attend, [lo, lim), and where a KV tile needs
-// masks at all: above `full` for the tile's first row, below `past` for its last.
+// Which keys a row of a paged query tile may attend: [lo, lim).
 struct RowKeys {
-  int lo, lim, past, full;
+  int lo, lim;
 };
-__device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row0, int row, int pack) {
-  RowKeys r;
-  r.lim = min((row >> pack) + k.hi + 1, k.n);
-  r.lo = (row >> pack) + k.lo;
-  r.full = min((row0 >> pack) + k.hi + 1, k.n);
-  r.past = ((row0 + BM - 1) >> pack) + k.lo;
-  return r;
+__device__ __forceinline__ RowKeys row_keys(const KeyRows& k, int row, int pack) {
+  return {(row >> pack) + k.lo, min((row >> pack) + k.hi + 1, k.n)};
 }
 // A KV tile's mask in the ring, a bit per key whose page is there.  The d = 128 kernel reads it
 // before it waits for the scores (2 x 2048 tokens: 350 against 345 us); at d <= 64 the order
@@ -433,10 +427,13 @@ __device__ __forceinline__ void load_mask(uint32_t slot, uint32_t (&w)[4]) {
 // against 371 us).  At d <= 64 words of 32 keys that are whole are skipped, which most of a
 // diagonal tile's are (ragged prompts, window 512: 38.4 against 36.4 us); the branches cost
 // the d = 128 kernel more than they save (2 x 2048 tokens: 350 against 355 us).
+// The unmasked tile's test is the thread's own row, voted on: limits of the whole tile beside the
+// row's are two more registers (1 x 8192, 32 heads, d = 64: 280.1 against 285.6 us).
 template <bool WORDS>
 __device__ __forceinline__ void paged_masks(const RowKeys& r, int kbase, uint32_t (&w)[4],
                                             uint32_t (&s)[BN]) {
-  if (kbase + BN <= r.full && kbase >= r.past && (w[0] & w[1] & w[2] & w[3]) == ~0u) return;
+  const bool all = kbase + BN <= r.lim && kbase >= r.lo && (w[0] & w[1] & w[2] & w[3]) == ~0u;
+  if (__all_sync(0xffffffffu, all)) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int hi = r.lim - kbase - 32 * i, lo = r.lo - kbase - 32 * i;   // bits [lo, hi) stay
@@ -755,8 +752,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int nt = hi - lo, g0 = g + lo - p.j0;   // this tile's KV tiles, its first step
       const int Nk = p.kr.n;
       const KeyRows kr = {Nk, p.kr.lo, p.kr.hi};
-      const int tile_row0 = p.row0 + t * BM;
-      const RowKeys rk = row_keys(kr, tile_row0, tile_row0 + rit, pack);
+      const RowKeys rk = row_keys(kr, p.row0 + t * BM + rit, pack);
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nt; ++j) {
         if (!(ok = mbar_wait_warp(bar(B_SF(t)), (ns + j) & 1, ctl))) break;
@@ -1299,7 +1295,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       if (tile < 0) break;
       const Piece* ti = info(k & 1);
       const int lo = ti->j0, nt = ti->j1 - lo, row0 = ti->row0, Nk = ti->kr.n;
-      const RowKeys rk = row_keys(ti->kr, row0, row0 + rit, pack);
+      const RowKeys rk = row_keys(ti->kr, row0 + rit, pack);
       const int grow = row0 + rit;               // query row
       // where a row lies in O, in the workspace, and in L or the workspace's L
       auto row_at = [&](int r) -> size_t {
@@ -1415,7 +1411,7 @@ __global__ void __launch_bounds__(one::THREADS, 2)
       tc_fence_after();
       const int Nr = ti->nr;
       const bool shared = ti->part >= 0;
-      const bool none = l_run == 0.f;            // as in the d = 128 kernel: O = 0
+      const bool none = l_run == 0.f;            // a row whose keys are all masked
       const float inv_l = none ? 0.f : 1.f / l_run;
       const bool valid = grow < Nr;
       // Each thread writes its row of O (16-bit) to this warp's 32 staging rows in shared
@@ -1443,14 +1439,17 @@ __global__ void __launch_bounds__(one::THREADS, 2)
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = none ? 0u
-                      : pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
-                                    __uint_as_float(o[2 * i + 1]) * inv_l);
+          w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
+                             __uint_as_float(o[2 * i + 1]) * inv_l);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           stage[lane * CPR + ((4 * cc + i) ^ (lane % CPR))] =
               make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
       }
+      // O = 0 as in the d = 128 kernel, over what was staged: choosing each word costs the rows with
+      // keys more here (1 x 8192, d = 64: 284.3 against 283.0 us; there 336.4 against 338.7)
+      if (none && !shared)
+        for (int i = 0; i < CPR; ++i) stage[lane * CPR + i] = make_uint4(0u, 0u, 0u, 0u);
       tc_fence_before();                         // O read before the next tile's p_full
       if (valid)
         *lse_at(grow) = none ? -INFINITY : (m_run - P_LOG2<BF16> + log2f(l_run)) * 0.69314718055994531f;
