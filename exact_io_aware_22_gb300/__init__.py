@@ -183,13 +183,13 @@ def _kv_heads(q, k, v) -> int:
 def _window(causal: bool, window: int) -> int:
     if window < 0 or (window > 0 and not causal):
         raise ValueError("window > 0 is a causal sliding window (causal=True)")
-    return min(int(window), 2 ** 31 - 1)          # no sequence is longer
+    return int(window) if window < 2 ** 31 else 2 ** 31 - 1   # no sequence is longer
 
 
 def _bound(max_seqlen: int) -> int:
-    if not -2 ** 31 <= max_seqlen < 2 ** 31:
-        raise ValueError("max_seqlen must be below 2^31")
-    return int(max_seqlen)
+    if -2 ** 31 <= max_seqlen < 2 ** 31:
+        return max_seqlen
+    raise ValueError("max_seqlen must be below 2^31")
 
 
 def fwd(q, k, v, causal: bool = True, scale: float | None = None, out=None, lse=None,
@@ -322,7 +322,7 @@ def fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = True,
         raise ValueError("out must match q; lse must be (H, total) fp32")
     _check(load_library().fa_fwd_varlen(
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens), B, total,
-        _bound(max_seqlen), H, Hkv, d, int(causal), window, float(scale), _dtype_code(q), _stream()),
+        _bound(int(max_seqlen)), H, Hkv, d, int(causal), window, float(scale), _dtype_code(q), _stream()),
         "fa_fwd_varlen")
     return out, lse
 
@@ -351,7 +351,7 @@ def bwd_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, causal: bool = 
         ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _check(load_library().fa_bwd_varlen(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-        ws_ptr, ws_bytes, _ptr(cu_seqlens), B, total, _bound(max_seqlen), H, Hkv, d, int(causal),
+        ws_ptr, ws_bytes, _ptr(cu_seqlens), B, total, _bound(int(max_seqlen)), H, Hkv, d, int(causal),
         window, float(scale), _dtype_code(q), _stream()), "fa_bwd_varlen")
     return dq, dk, dv
 
@@ -719,7 +719,7 @@ def _decode_paged(q, k_cache, v_cache, page_table, cache_seqlens, scales, scale,
                   decode_paged_workspace_size(H, Hkv, d) if workspace is None else 0,
                   lib.fa_decode_paged_fp8 if scales else lib.fa_decode_paged,
                   (q.data_ptr(), pc, out.data_ptr(), lse.data_ptr()),
-                  (B, H, Hkv, d, _window(True, window),
+                  (B, H, Hkv, d, window and _window(True, window),
                    1.0 / math.sqrt(d) if scale is None else scale, *scales, code))
     if st:
         _check(st, "fa_decode_paged_fp8" if scales else "fa_decode_paged")
@@ -769,7 +769,9 @@ def fwd_paged(q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens, max_se
     total, H, d = shape
     code = _16bit(dtype, codes)
     B = _offsets(cu_seqlens, i32)
-    window, max_seqlen = _window(causal, window), _bound(max_seqlen)
+    if window:
+        window = _window(causal, window)
+    max_seqlen = _bound(max_seqlen)
     pc, Hkv = _paged(k_cache, v_cache, page_table, cache_seqlens, dtype, B, d)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
