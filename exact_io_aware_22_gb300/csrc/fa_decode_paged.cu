@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(32 * DP_WARPS, ctas_of(NT))
   constexpr int KEYS = G::KEYS, MT = KEYS / 16, KS = D / 16, RG = 8 * NT, STAGES = stages_of(NT);
   constexpr bool MB = BF16 && !C8;               // operands of the products: bf16 or f16
   // A state's m is the maximum less SH: p <= 2^(SH + 8) = 2^15 where P is f16, so that the
-  // small p of a long context, which add up, stay clear of f16's subnormals.
+  // small p of a long context, which add up, stay clear of f16's subnormals: a weight of less than
+  // 2^-21 of the largest is off by up to 2^-32 of that, others by 2^-16 of themselves or less.
   constexpr float SH = MB ? 0.f : 7.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;         // fragment row, column pair

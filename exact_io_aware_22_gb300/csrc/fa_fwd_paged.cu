@@ -28,10 +28,13 @@
 //              tokens of 10 / 16 sequences of 16384-32768 keys: 163 / 252 us (6.2 and 6.4 TB/s);
 //              a CTA for each tile: 355 / 356 us.
 //
-// Bound: at d = 128 the tensor pipe and the exponentials (2 x 2048 tokens on 8192 keys, 32/8
-// heads: 0.335 ms, 1425 TFLOP/s), at d <= 64 the exponentials and the softmax threads' issue
-// slots; with few tokens the latency of start, split and join (the 5 tokens above: 18 us for 34 MB
-// of keys), with few tokens on long caches the cache's bytes.
+// Bound: at d = 128 the products and exponentials of a KV tile, 1.55 us where the products alone
+// take 1.35 at the rate of a large matrix product, and the last, part-filled round of query tiles
+// (2 x 2048 tokens on 8192 keys, 32/8 heads: 0.335 ms, 1422 TFLOP/s; 512 tiles on 152 SMs give a
+// CTA up to 216 KV tiles where the mean is 189); at d <= 64 the latency of a KV tile's chain (S,
+// maximum, exponentials, P, P.V) under two CTAs per SM; with few tokens that of start, split and
+// join (the 5 tokens above: 18 us for 34 MB of keys), with few tokens on long caches the cache's
+// bytes.
 //
 // The kernels stand apart from fa_fwd.cu's although the pipelines are alike: pages, packed heads
 // and ranges reach into every role, and the dense kernels' code does not change with them.
@@ -47,8 +50,14 @@ constexpr int BN = 128;       // keys per K/V tile
 constexpr int NT = 2;         // Q tiles per CTA
 constexpr int THREADS = 384;
 constexpr float RESCALE_LOG2 = 8.0f;   // the running maximum moves in steps of 2^8 or more
+// P is rounded to 16 bits once, as the tensor cores take it and as in the dense forward: each
+// weight is off by at most half a step (2^-8 of it in bf16, 2^-11 in f16), l sums them unrounded.
+// Against 64 bits the result is off by 1.4 times the rounding of O alone (0.0023 of its size
+// against 0.0017 in bf16).  Two terms, as decoding has them, would take half as many products
+// again, and the tensor pipe is what long prompts wait for.
 // P is formed with 2^7 times its weight where it is f16 (p <= 2^15), so that the small p of a
-// long context, which add up, stay clear of f16's subnormals; l carries the same factor.
+// long context, which add up, stay clear of f16's subnormals (weights below 2^-21 of the largest
+// are off by up to 2^-32 of that); l carries the same factor.
 template <bool BF16>
 constexpr float P_LOG2 = BF16 ? 0.f : 7.f;
 constexpr int kMaskSlots = 8;         // ring of 128-bit key masks, one per KV tile

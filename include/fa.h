@@ -347,6 +347,8 @@ fa_status fa_decode_paged_fp8(const void* Q, const fa_paged_cache* cache, void* 
  *            aligned), or NULL: allocated and freed on `stream`.  0 bytes, and then unused,
  *            where there are query rows enough to fill the GPU without splitting the keys.  Its
  *            contents do not matter before a call.
+ *   The softmax weights are rounded to `dtype` before their product with V, as in fa_fwd (the
+ *   decoding calls keep twice the bits).
  *   A V element that is not finite reaches the query rows of its 128-key tile that have keys even
  *   where the causal mask or the window hides its key (0 x NaN), as in fa_fwd; what lies in absent
  *   pages and past the last key never does, and rows without keys are 0 whatever the tile holds.
