@@ -57,7 +57,7 @@ class _Heads(ctypes.Structure):
     """struct fa_heads of include/fa.h."""
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong),
                 ("head_stride", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
-                ("heads", ctypes.c_int)]
+                ("heads", ctypes.c_int), ("zero_rest", ctypes.c_int)]
 
 
 class _HeadNorm(ctypes.Structure):
@@ -756,16 +756,17 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda")
     return torch.cat([a.cos(), a.sin()], 1).float()
 
 
-def _heads(t, shape, dtype, name: str):
-    """struct fa_heads of a (B, heads, N, d) or packed (total, heads, d) tensor of a shape."""
+def _heads(t, shape, dtype, name: str, made: bool = False):
+    """struct fa_heads of a (B, heads, N, d) or packed (total, heads, d) tensor of a shape.  made: an
+    output that the call has made, whose rows that are left out become zeros."""
     st = t.stride()
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have contiguous columns")
     if len(st) == 3:
-        return _Heads(t.data_ptr(), 0, st[1], st[0], shape[1])
-    return _Heads(t.data_ptr(), st[0], st[1], st[2], shape[1])
+        return _Heads(t.data_ptr(), 0, st[1], st[0], shape[1], made)
+    return _Heads(t.data_ptr(), st[0], st[1], st[2], shape[1], made)
 
 
 def _rotation(cos_sin, interleaved, positions, cu_seqlens, shape, i32, f32):
@@ -818,26 +819,27 @@ def norm_rope(q, k, q_weight=None, k_weight=None, eps: float | None = None, cos_
     or (2i, 2i + 1) if ``interleaved``, of the first rot_dim columns turn by the row of the token's
     position: its index n, or in packed sequences with ``cu_seqlens`` (int32, offsets) its index in
     its sequence, or ``positions`` (int32 (N,), (B, N), or (total,)).  Rows of no sequence are left
-    as they were; one whose position lies outside the table too, and ``device_status()`` then
-    reports FA_ERR_INVALID_VALUE."""
+    out: 0 in outputs made here, as they were in those given; one whose position lies outside the
+    table too, and ``device_status()`` then reports FA_ERR_INVALID_VALUE."""
     torch, i32, f32, codes, _, _ = _paged_env()
     dev = _one_device(q, k, q_weight, k_weight, cos_sin, positions, cu_seqlens, q_out, k_out)
     shape, ks, dtype = _q_and_k(q, k, "qk")
     code, d = _16bit(dtype, codes), shape[-1]
     norm = _norm(q_weight, k_weight, eps, dtype, d, f32)
     rot, B, N = _rotation(cos_sin, interleaved, positions, cu_seqlens, shape, i32, f32)
-    if q_out is None:
+    q_made, k_made = q_out is None, k_out is None
+    if q_made:
         q_out = torch.empty(shape, dtype=dtype, device=q.device)
     if k is None:
-        if k_out is not None:
+        if not k_made:
             raise ValueError("k_out without k")
         kh = ko = None
     else:
-        if k_out is None:
+        if k_made:
             k_out = torch.empty(ks, dtype=dtype, device=q.device)
-        kh, ko = _heads(k, ks, dtype, "k"), _heads(k_out, ks, dtype, "k_out")
+        kh, ko = _heads(k, ks, dtype, "k"), _heads(k_out, ks, dtype, "k_out", k_made)
     st = _call(dev, load_library().fa_norm_rope, _heads(q, shape, dtype, "q"), kh,
-               _heads(q_out, shape, dtype, "q_out"), ko, norm, rot, B, N, d, code)
+               _heads(q_out, shape, dtype, "q_out", q_made), ko, norm, rot, B, N, d, code)
     if st:
         _check(st, "fa_norm_rope")
     return q_out, k_out
@@ -869,8 +871,10 @@ def norm_rope_bwd(dq_out, dk_out, q=None, k=None, q_weight=None, k_weight=None,
     """Gradients dq, dk, dq_weight, dk_weight of ``norm_rope``'s inputs from those of its outputs
     (``bwd``'s dq and dk), with the forward's other arguments.  q and k, the forward's inputs, are
     needed with ``eps`` only.  dq and dk: contiguous unless given, of any strides with contiguous
-    columns (slices of the projection's gradient); dq may be dq_out or q itself, dk likewise.  The
-    weights' gradients are fp32 (d,), summed over all rows and heads in an order that depends on
+    columns (slices of the projection's gradient); dq may be dq_out or q itself, dk likewise.  Rows
+    that the forward leaves out get 0 in a dq or dk made here and stay as they were in one given,
+    which then has to hold zeros there if the projection's gradient sums over them.  The weights'
+    gradients are fp32 (d,), summed over all rows and heads in an order that depends on
     sizes alone; None without that weight.  ``workspace``: an optional CUDA tensor of at least
     ``norm_rope_bwd_workspace_size(d)`` bytes; calls that may overlap need one each."""
     torch, i32, f32, codes, _, _ = _paged_env()
@@ -885,17 +889,18 @@ def norm_rope_bwd(dq_out, dk_out, q=None, k=None, q_weight=None, k_weight=None,
         if q is None or ks is not None and k is None:
             raise ValueError("the gradient of a norm needs the forward's inputs q and k")
         qh = _heads(q, shape, dtype, "q")
-    if dq is None:
+    q_made, k_made = dq is None, dk is None
+    if q_made:
         dq = torch.empty(shape, dtype=dtype, device=dq_out.device)
     if ks is None:
-        if dk is not None or k_weight is not None:
+        if not k_made or k_weight is not None:
             raise ValueError("dk or k_weight without dk_out")
     else:
         if norm is not None:
             kh = _heads(k, ks, dtype, "k")
-        if dk is None:
+        if k_made:
             dk = torch.empty(ks, dtype=dtype, device=dq_out.device)
-        kg, ko = _heads(dk_out, ks, dtype, "dk_out"), _heads(dk, ks, dtype, "dk")
+        kg, ko = _heads(dk_out, ks, dtype, "dk_out"), _heads(dk, ks, dtype, "dk", k_made)
     dq_weight, qp = _weight_grad(q_weight, dq_weight, f32, "dq_weight")
     dk_weight, kp = _weight_grad(k_weight, dk_weight, f32, "dk_weight")
     need = 0
@@ -903,7 +908,7 @@ def norm_rope_bwd(dq_out, dk_out, q=None, k=None, q_weight=None, k_weight=None,
         need = norm_rope_bwd_workspace_size(d)
     st = _call_ws(dev, workspace, need, load_library().fa_norm_rope_bwd,
                   (_heads(dq_out, shape, dtype, "dq_out"), kg, qh, kh,
-                   _heads(dq, shape, dtype, "dq"), ko, norm, rot, qp, kp), (B, N, d, code))
+                   _heads(dq, shape, dtype, "dq", q_made), ko, norm, rot, qp, kp), (B, N, d, code))
     if st:
         _check(st, "fa_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight

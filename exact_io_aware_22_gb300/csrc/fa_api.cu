@@ -908,7 +908,8 @@ fa_status norm_rope_impl(const fa_heads* const (&x)[2], const fa_heads* const (&
   }
   if ((st = ctl_for_launch(&a.ctl)) != FA_OK) return st;
   auto view = [](const fa_heads* v) {
-    return v ? fa::HeadView{v->data, v->batch_stride, v->head_stride, v->row_stride, v->heads}
+    return v ? fa::HeadView{v->data, v->batch_stride, v->head_stride, v->row_stride, v->heads,
+                            v->zero_rest == 1}
              : fa::HeadView{};
   };
   for (int i = 0; i < 2; ++i) {
@@ -1155,12 +1156,12 @@ fa_status append_impl(const fa_paged_cache* cache, const void* K, long long k_st
   if (norm) {
     fa::NormRopeArgs n;
     std::memset(&n, 0, sizeof(n));
-    n.x[0] = {const_cast<void*>(Q), 0, d, q_stride, Q ? H : 0};
-    n.x[1] = {const_cast<void*>(K), 0, d, k_stride, Hkv};
-    n.x[2] = {const_cast<void*>(V), 0, d, v_stride, Hkv};
-    n.y[0] = {Qout, 0, d, q_row, Q ? H : 0};
-    n.y[1] = {c.K, 0, c.head_stride, 0, Hkv};
-    n.y[2] = {c.V, 0, c.head_stride, 0, Hkv};
+    n.x[0] = {const_cast<void*>(Q), 0, d, q_stride, Q ? H : 0, false};
+    n.x[1] = {const_cast<void*>(K), 0, d, k_stride, Hkv, false};
+    n.x[2] = {const_cast<void*>(V), 0, d, v_stride, Hkv, false};
+    n.y[0] = {Qout, 0, d, q_row, Q ? H : 0, false};
+    n.y[1] = {c.K, 0, c.head_stride, 0, Hkv, false};
+    n.y[2] = {c.V, 0, c.head_stride, 0, Hkv, false};
     n.w[0] = norm->q_weight;
     n.w[1] = norm->k_weight;
     n.norm = true;

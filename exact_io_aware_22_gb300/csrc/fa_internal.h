@@ -207,6 +207,7 @@ struct HeadView {
   void* data;
   long long batch_stride, head_stride, row_stride;
   int heads;
+  bool zero_rest;              // of an output: rows that are left out get zeros
 };
 // Norms of query ([0]) and key ([1]) heads and their rotation, the gradient of both, or appending
 // them and values ([2]) to a paged cache.

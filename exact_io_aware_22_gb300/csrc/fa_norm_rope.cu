@@ -279,6 +279,16 @@ __global__ void __launch_bounds__(NR_THREADS, Shape<MODE>::CTAS)
             }
           }
         }
+        if (!APP && !known && (kind ? a.y[1].zero_rest : a.y[0].zero_rest)) {
+          // zeros to all that this thread, or another warp's in its place, has of the token: here, once a
+          // token, and not where its items are skipped below (the gradient of 4 x 8192 tokens 159
+          // against 162 us)
+          uint16_t* y = token_at(vo, b, n);
+          for (int h = pf.h; h < H; h += SLOTS) {
+            *reinterpret_cast<uint4*>(y + h * vo.head_stride + it.c0) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(y + h * vo.head_stride + it.c1) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
       }
       have = (have & ~(1u << stage)) | (static_cast<uint32_t>(known) << stage);
       const uint16_t* x = fx + pf.h * vx.head_stride;

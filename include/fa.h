@@ -240,11 +240,15 @@ fa_status fa_decode_fp8(const void* Q, const void* Kc8, const void* Vc8, const i
 /* Heads of a (B, heads, N, d) tensor: element (b, h, n, c) at
  * b * batch_stride + h * head_stride + n * row_stride + c (elements; a stride of a dimension of
  * extent 1 is not used).  So dense (B, heads, N, d), (B, N, heads, d), packed (total, heads, d)
- * with B = 1, and slices of one projection's output all fit. */
+ * with B = 1, and slices of one projection's output all fit.
+ * zero_rest is of outputs: 1 writes zeros to the rows that the call leaves out (fa_rotation: those of
+ * no sequence and those whose position lies outside the table), as a gradient that goes on to the
+ * projection's has to have; any other value leaves them as they were. */
 typedef struct fa_heads {
   void* data;
   long long batch_stride, head_stride, row_stride;
   int heads;
+  int zero_rest;
 } fa_heads;
 
 /* Norm of query and key heads: weights w (d), fp32 (weights_fp32 = 1) or of the call's dtype, or NULL:
@@ -263,10 +267,11 @@ typedef struct fa_head_norm {
  *                (2i, 2i + 1).  rot_dim a multiple of 16 in [0, d]; 0: no rotation.
  *   cu_seqlens   device int32 [n_seq + 1], or NULL.  With it B is 1 and the rows are packed
  *                sequences: sequence i has rows cu[i] .. cu[i+1]-1.  Rows of no sequence are left
- *                as they were and have no part in gradients.
+ *                out: an output keeps what it held there (or gets zeros, fa_heads), and they
+ *                have no part in the weights' gradients.
  *   positions    device int32, row n of batch entry b at b * positions_stride + n (0: the same
  *                for all entries), or NULL: the row's index in its batch entry or sequence.
- *   A row whose position lies outside the table is left out whole, and fa_device_status then
+ *   A row whose position lies outside the table is left out, too, and fa_device_status then
  *   reports FA_ERR_INVALID_VALUE. */
 typedef struct fa_rotation {
   const float* cos_sin;
