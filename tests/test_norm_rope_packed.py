@@ -1,10 +1,14 @@
-"""Norms and rotation of rows that belong to no sequence or lie past the table: what they hold in
-outputs that the call makes."""
+"""Norms and rotation of packed sequences long enough that a warp goes on from piece to piece, with
+rows that belong to no sequence or lie past the table among them, and what such rows hold in outputs
+that the call makes.  Against the definitions in 64 bits (tests/norm_rope_util.py, where the tolerances
+are derived)."""
 import contextlib
 
 import pytest
 import torch
 
+from tests import norm_rope_util as nu
+from tests import paged_util as pu
 from tests.test_paged_edges import ints
 
 gpu = pytest.mark.gpu
@@ -32,6 +36,95 @@ def nan_in_new_tensors():
     finally:
         torch.use_deterministic_algorithms(was[0])
         torch.utils.deterministic.fill_uninitialized_memory = was[1]
+
+
+def packed_rows(lens, first, total, max_pos, bad=()):
+    """Rows that a call turns and their positions, for sequences of ``lens`` from row ``first`` on; rows
+    of ``bad`` are given a position outside the table of ``max_pos``."""
+    rows, at, n = [], [], first
+    for m in lens:
+        rows += range(n, n + m)
+        at += range(m)
+        n += m
+    assert n <= total
+    keep = [i for i, (r, p) in enumerate(zip(rows, at)) if p < max_pos and r not in bad]
+    return torch.tensor([rows[i] for i in keep]), torch.tensor([at[i] for i in keep])
+
+
+# ------------------------------------------------------------------ many pieces to a warp
+# d, tokens of whole sequences (about), rotated columns, interleaved, eps, dtype, weights, outputs given
+MANY = [
+    (128, 5200, 128, False, 1e-6, "bf16", "fp32", True),
+    (128, 5200, 64, True, 1e-6, "fp16", "16", False),
+    (128, 5200, 128, True, None, "bf16", None, True),
+    (128, 5200, 96, False, None, "fp16", None, False),
+    (64, 9000, 64, False, 1e-6, "fp16", "16", True),
+    (32, 16500, 32, False, 1e-6, "bf16", "16", True),
+    (32, 16500, 16, True, 1e-6, "fp16", "fp32", False),
+    (32, 16500, 32, True, None, "bf16", None, False),
+]
+
+
+@gpu
+@pytest.mark.parametrize("by_position", [False, True])
+@pytest.mark.parametrize("case", MANY, ids=["-".join(str(x) for x in c) for c in MANY])
+def test_pieces_of_many_packed_sequences(case, by_position):
+    """32/8 heads: 16 steps and more to a warp.  Empty sequences, of one token and of many, gaps at both
+    ends, a sequence longer than the table, and by positions some outside it in the middle."""
+    d, tokens, rot, inter, eps, dtype, wk, given = case
+    H, Hkv, t, fa = 32, 8, pu.DT[dtype], fa_()
+    g = torch.Generator().manual_seed(d + rot + by_position)
+    lens = [0, 1, 1, 0, 700, 1, 33, 0, 0, 2]
+    while sum(lens) < tokens:
+        lens += [int(torch.randint(1, 900, (), generator=g)), 0, 1]
+    first, max_pos = 5, 600
+    total = first + sum(lens) + 37
+    offsets = [first + sum(lens[:i]) for i in range(len(lens) + 1)]
+    bad, pos = (), None
+    if by_position:                              # the sequences' indices, some rows' outside the table
+        pos = torch.full((total,), 3, dtype=torch.int32)
+        for a, m in zip(offsets, lens):
+            pos[a:a + m] = torch.arange(m, dtype=torch.int32)
+        bad = [first, first + 2, first + 300, first + 301, first + tokens // 2, offsets[-1] - 1]
+        pos[bad] = torch.tensor([-1, max_pos, 2 ** 31 - 1, -2 ** 31, max_pos + 5, -7], dtype=torch.int32)
+    rows, at = packed_rows(lens, first, total, max_pos, set(bad))
+    rest = torch.ones(total, dtype=torch.bool)
+    rest[rows] = False
+    x = torch.randn((total, H + Hkv, d), generator=g).to(t).cuda()
+    dy = (torch.randn((total, H + Hkv, d), generator=g) * 0.7).to(t).cuda()
+    w = None if wk is None else (1 + 0.3 * torch.randn((2, d), generator=g)).to(torch.float32 if wk == "fp32" else t).cuda()
+    cs = nu.table(max_pos, rot).cuda()
+    args = dict(cos_sin=cs, cu_seqlens=ints(offsets), interleaved=inter, eps=eps,
+                positions=None if pos is None else pos.cuda())
+    if w is not None:
+        args.update(q_weight=w[0], k_weight=w[1])
+    q, k, gq, gk = x[:, :H], x[:, H:], dy[:, :H], dy[:, H:]
+    y, dx = (torch.full_like(x, 7.0) for _ in range(2))
+    if given:
+        outs, grads = fa.norm_rope(q, k, q_out=y[:, :H], k_out=y[:, H:], **args), \
+            fa.norm_rope_bwd(gq, gk, q, k, dq=dx[:, :H], dk=dx[:, H:], **args)
+    else:
+        with nan_in_new_tensors():
+            outs, grads = fa.norm_rope(q, k, **args), fa.norm_rope_bwd(gq, gk, q, k, **args)
+    ok(1)                                        # some rows lie outside the table
+    rows, rest, rot_rows = rows.cuda(), rest.cuda(), cs[at.cuda()][:, None]
+    for i, (v, g_v) in enumerate(((q, gq), (k, gk))):
+        assert (outs[i][rest] == (7 if given else 0)).all(), "rows that are left out"
+        assert (grads[i][rest] == (7 if given else 0)).all(), "rows that are left out, backward"
+        ww = None if w is None else w[i].double()
+        if eps is not None and ww is None:
+            ww = torch.ones(d, dtype=torch.float64, device="cuda")
+        want, tol = nu.forward(v[rows], ww, eps, rot_rows, inter)
+        nu.close(outs[i][rows], want.cpu(), tol.cpu(), t, "y")
+        want, tol, terms, sizes = nu.backward(g_v[rows], v[rows], ww, eps, rot_rows, inter)
+        nu.close(grads[i][rows], want.cpu(), tol.cpu(), t, "dx")
+        if w is not None:
+            nu.close_dw(grads[2 + i], terms.cpu(), sizes.cpu(), "dw")
+    # again, over the same data: bit for bit
+    again = fa.norm_rope_bwd(gq, gk, q, k, **args)
+    ok(1)
+    for a, b in zip(again, grads):
+        assert a is None and b is None or torch.equal(a if a.dim() == 1 else a[rows], b if b.dim() == 1 else b[rows])
 
 
 # ------------------------------------------------------------------ rows that are left out
