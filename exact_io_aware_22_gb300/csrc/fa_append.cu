@@ -21,8 +21,7 @@
 // 1.9 us, 64 tokens 2.2 us.
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
-
-#include <cuda_fp8.h>
+#include "fa_tokens.cuh"
 
 namespace fa {
 
@@ -30,31 +29,6 @@ namespace {
 
 constexpr int APP_THREADS = 128;
 constexpr int APP_CTAS = 8;                       // CTAs per SM up to which a thread has one head
-
-// The sequence b and key position pos of token t; false for a token that belongs to no
-// sequence or lies before its sequence's first key.
-__device__ __forceinline__ bool locate(const AppendArgs& a, int t, int& b, int& pos) {
-  int end;
-  if (!a.cu) {
-    b = t;
-    end = t + 1;
-  } else {
-    // last b with cu[b] <= t; offsets that are not ascending may lead to a sequence that
-    // does not hold t, which the comparison below refuses
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    end = a.cu[b + 1];
-    if (a.cu[b] > t || end <= t) return false;
-  }
-  const long long p = static_cast<long long>(a.pg.seqlens[b]) - (end - t);
-  pos = static_cast<int>(p);
-  return p >= 0;
-}
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
@@ -71,14 +45,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
                     pack2<BF16>(x[6], x[7]));
 }
-// 8 values times inv as E4M3 codes, nearest even, saturated to +-448 (NaN stays NaN).
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE,
-                                    __NV_E4M3);
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  const float2 p[4] = {make_float2(x[0], x[1]), make_float2(x[2], x[3]), make_float2(x[4], x[5]),
+                       make_float2(x[6], x[7])};
+  return fa::codes8(p, inv);
 }
 
 // How the heads of a token (K's, V's, then Q's) go to threads: `lanes` threads per column group
@@ -119,10 +89,10 @@ __global__ void __launch_bounds__(APP_THREADS) append_kernel(const AppendArgs a,
     w1[m] = *reinterpret_cast<const uint4*>(src + (turn ? r1 : p1));
   }
 
-  int b, pos;
-  if (!locate(a, t, b, pos)) return;
-  const int pi = static_cast<int>(a.pg.page.quot(pos));
-  const int id = pi < a.pg.max_pages ? a.pg.table[b * a.pg.table_stride + pi] : -1;
+  int b, pos, pi;
+  Sequence seq = {0, 0, 0, 0};
+  if (!locate_token(a.pg, a.cu, a.B, t, seq, b, pos)) return;
+  const int id = page_id(a.pg, b, pos, pi);
   float c[8], s[8];
   if (a.rot > 0) {
     // a token whose angle lies outside the table is left out whole

@@ -24,8 +24,7 @@
 // tokens 66 us (5.2 TB/s), about as much the instructions of a warp's items as bytes.
 #include "fa_internal.h"
 #include "fa_heads.cuh"
-
-#include <cuda_fp8.h>
+#include "fa_tokens.cuh"
 
 #include <type_traits>
 
@@ -49,24 +48,6 @@ struct Shape {
   static constexpr int PART = 16 * NR_THREADS, SMEM = RING * PARTS * PART;
 };
 
-// The sequence that a thread has found last: its rows are [lo, hi) of the packed ones.
-struct Sequence {
-  int lo, hi, b;
-};
-// Whether packed row n lies in a sequence; then seq is that one.
-__device__ __forceinline__ bool find_sequence(const int* cu, int n_seq, int n, Sequence& seq) {
-  if (n >= seq.lo && n < seq.hi) return true;
-  // last sequence with cu <= n; offsets that are not ascending may lead to one that does not hold n,
-  // which the comparison below refuses
-  int lo = 0, hi = n_seq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= n) lo = mid;
-    else hi = mid;
-  }
-  seq = {cu[lo], cu[lo + 1], lo};
-  return n >= seq.lo && n < seq.hi;
-}
 // Row of the angles' table for row n of batch entry b (packed: token n); false: it belongs to no
 // sequence.
 __device__ __forceinline__ bool token_angle(const NormRopeArgs& a, int b, int n, Sequence& seq,
@@ -87,31 +68,14 @@ struct Slot {
 };
 __device__ __forceinline__ bool append_place(const NormRopeArgs& a, int t, Sequence& seq, Slot& slot,
                                              int& ang) {
-  int b = t, end = t + 1;
-  if (a.cu) {
-    if (!find_sequence(a.cu, a.n_seq, t, seq)) return false;
-    b = seq.b;
-    end = seq.hi;
-  }
-  const long long p = static_cast<long long>(a.pg.seqlens[b]) - (end - t);
-  if (p < 0) return false;
-  const int pos = static_cast<int>(p), pi = static_cast<int>(a.pg.page.quot(pos));
+  int b, pos, pi;
+  if (!locate_token(a.pg, a.cu, a.n_seq, t, seq, b, pos)) return false;
+  const int id = page_id(a.pg, b, pos, pi);
   ang = a.positions ? a.positions[t] : pos;
-  const int id = pi < a.pg.max_pages ? a.pg.table[b * a.pg.table_stride + pi] : -1;
   const bool in_pool = id >= 0 && id < a.pg.pages;
   slot.row = !in_pool ? -1 : id * a.page_stride +
                              (pos - pi * static_cast<int>(a.pg.page.div)) * a.row_stride;
   return true;
-}
-
-// 8 values times inv as E4M3 codes, nearest even, saturated to +-448 (NaN stays NaN).
-__device__ __forceinline__ uint2 codes8(const float2 (&x)[4], float inv) {
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[i].x * inv, x[i].y * inv), __NV_SATFINITE,
-                                    __NV_E4M3);
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
 // An item's chunks begin at columns c0 and c1, apart so that a head's lanes read and write runs of
@@ -237,7 +201,7 @@ __global__ void __launch_bounds__(NR_THREADS, Shape<MODE>::CTAS)
   seek(pf);
   p = pf;
   const uint32_t mine = smem_u32(ring) + 16 * tid;
-  Sequence seq = {0, 0, 0};
+  Sequence seq = {0, 0, 0, 0};
   const uint16_t *fx = nullptr, *fg = nullptr;   // the token's first head
   int t_fetched = -1;
   bool known = false;                            // its token is to be computed
