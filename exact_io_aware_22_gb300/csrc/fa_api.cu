@@ -861,6 +861,7 @@ fa_status norm_rope_impl(const fa_heads* const (&x)[2], const fa_heads* const (&
       ins[n_in++] = v;
     }
     if ((need_x && !x[i]) || (bwd && !dy[i])) return FA_ERR_INVALID_VALUE;
+    if (static_cast<long long>(B) * N * y[i]->heads > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   }
   if (norm && (st = check_norm(*norm)) != FA_OK) return st;
   fa_rotation r = {};
@@ -1088,6 +1089,7 @@ fa_status append_impl(const fa_paged_cache* cache, const void* K, long long k_st
   if (norm && (st = check_norm(*norm)) != FA_OK) return st;
   if ((st = check_heads(H, Hkv)) != FA_OK) return st;
   if (T < 1 || (!cu_seqlens && T != B)) return FA_ERR_INVALID_VALUE;
+  if (norm && static_cast<long long>(T) * (Q ? H : Hkv) > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (!K || !V || (Q == nullptr) != (Qout == nullptr)) return FA_ERR_INVALID_VALUE;
   if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_VALUE;
   if (rot_dim < 0 || rot_dim > d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;

@@ -283,14 +283,16 @@ typedef struct fa_rotation {
 } fa_rotation;
 
 /* Forward: q_out and k_out from q and k.  k and k_out may both be NULL.  norm and rot may be NULL.
- * An output may be its own input (same data and strides); otherwise outputs overlap nothing
- * (views that interleave without sharing an element, such as slices of one projection, do not).
+ * An output may be its own input (same data and strides); otherwise outputs overlap nothing.  Views
+ * that interleave without sharing an element do not, where they have a stride in common of which their
+ * larger ones are multiples (slices of one projection); others are refused.
  *   Errors: FA_ERR_INVALID_VALUE for NULL pointers, B, N or heads < 1, q and q_out (k and k_out) of
  *   different heads, negative strides, outputs whose elements coincide or that overlap, a norm
  *   whose eps is not positive and finite, weights_fp32 or interleaved not 0/1, rot_dim > 0 without
  *   cos_sin or with max_pos < 1, cu_seqlens with n_seq < 1 or B > 1, a negative positions_stride;
  *   FA_ERR_UNSUPPORTED for d not 32/64/128, another dtype, rot_dim not a multiple of 16 in [0, d],
- *   B * N * heads >= 2^31, or strides of 2^40 bytes or more;
+ *   B * N * heads >= 2^31, strides of 2^40 bytes or more, a view whose (extent - 1) * stride passes 2^46
+ *   elements in any dimension, or positions_stride >= 2^40;
  *   FA_ERR_MISALIGNED for data, weights or cos_sin not 16-byte aligned, strides that are not
  *   multiples of 8 elements, or int arrays not 4-byte aligned.
  *   Asynchronous on `stream`; launches are not traced. */
@@ -306,7 +308,9 @@ fa_status fa_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_o
  *                and freed on `stream` if a weight's gradient is asked for; unused otherwise.  Its
  *                contents do not matter before a call; calls that may overlap need one each.
  *   dq may be dq_out or q itself, dk likewise.  Errors as for the forward, and
- *   FA_ERR_INVALID_VALUE for a short workspace or a weight's gradient without norm. */
+ *   FA_ERR_INVALID_VALUE for a short workspace, a weight's gradient without norm or without its heads,
+ *   or weights' gradients or a workspace that overlap anything else; FA_ERR_MISALIGNED where they are
+ *   not aligned as above. */
 size_t fa_norm_rope_bwd_workspace_size(int d);
 fa_status fa_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa_heads* q,
                            const fa_heads* k, const fa_heads* dq, const fa_heads* dk,
@@ -395,8 +399,9 @@ fa_status fa_append_paged_fp8(const fa_paged_cache* cache, const void* K, long l
                               fa_dtype dtype, void* stream);
 
 /* fa_append_paged and fa_append_paged_fp8 with the norm of fa_norm_rope: query and key heads are
- * normed before they turn (and are quantised); values are not.  Errors as there, and those of a
- * norm as for fa_norm_rope; norm must not be NULL (FA_ERR_INVALID_VALUE). */
+ * normed before they turn (and are quantised); values are not.  Errors as there, with T * heads >= 2^31
+ * of any of the tensors in the place of the blocks of work (FA_ERR_UNSUPPORTED), and those of a norm as
+ * for fa_norm_rope; norm must not be NULL (FA_ERR_INVALID_VALUE). */
 fa_status fa_append_paged_norm(const fa_paged_cache* cache, const void* K, long long k_stride,
                                const void* V, long long v_stride, const void* Q, long long q_stride,
                                void* Qout, const int* cu_seqlens, const int* positions,
