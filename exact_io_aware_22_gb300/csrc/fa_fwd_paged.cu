@@ -597,12 +597,15 @@ __device__ __forceinline__ void clear_row(uint32_t tile, int r) {
 // a ring of its own, into a ring of f16 tiles, and the softmax threads turn bf16 query rows when a
 // tile of them arrives.  Every code is an f16 value, so K and V lose nothing; P is f16 for both
 // types of queries.  Bound: as with 16-bit pools for many rows (2 x 2048 tokens on 8192 keys, 32/8
-// heads: 343 against 336 us); for few the shared memory's port, which a KV tile's copy, conversion
-// and products hold for 1800 of its 2150 cycles, not the codes' bytes (16 x 5 tokens on
-// 16384-32768 keys: 186 us, 4.3 TB/s, from 16-bit pools 258).  Measured against this split: one converter
-// warp for K and one for V 432 us for the former (a tile's conversion is waited for), four converter
-// warps in a warpgroup of their own 358 and 213 (they share the one port, and leave the softmax
-// threads 184 registers); two tiles of codes ahead instead of four 220 for the latter.
+// heads: 337 against 335 us); for few the shared memory's port, which a KV tile's copy, conversion
+// and products hold for 1790 of its 2040 cycles, not the codes' bytes (16 x 5 tokens on
+// 16384-32768 keys: 167 us, 4.8 TB/s of codes, from 16-bit pools 258).  Other splits, measured when the
+// two took 343 and 186 us: one converter warp for K and one for V 432 us for the former (a tile's
+// conversion is waited for), four converter warps in a warpgroup of their own 358 and 213 (they share
+// the one port, and leave the softmax threads 184 registers); two tiles of codes ahead instead of four
+// 220 for the latter.  With ranges 40 bytes of a thread's registers spill (8 from 16-bit pools),
+// which costs little: 4800 of the 2.1 million warp instructions of 4 x 5 tokens on 1500-2500 keys move
+// them, and 31 thousand of the 56 million of the long ones.
 // SCALE_LAST: v_scale multiplies means of the codes, which are at most 448.  Whole tiles otherwise take
 // v_scale / l_run for 1 / l_run, which costs nothing but falls below fp32's normal numbers for a very
 // small one (the multiplication costs 2 x 2048 tokens on 8192 keys 1 to 2 %: 342 to 346 against 338 us).
@@ -660,8 +663,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // A piece of codes whose query tile has rows in its first half only: both softmax warpgroups work on
   // these rows, on every other KV tile each, and the first one joins the two results.  That costs
-  // about what two KV tiles take (pieces of four: 21.7 against 20.0 us for 4 x 5 tokens on 2000
-  // keys; 16 x 5 tokens on 16384-32768 keys: 186 against 248).
+  // about what two KV tiles take: 16 x 5 tokens on 16384-32768 keys 167 against 229 us; pieces of
+  // four too, 4 x 5 tokens on 1500-2500 keys 18.6 against 17.7 (on 2000 each 16.8 against 17.8).
   auto halved = [&](const volatile Piece& p) {
     return HALVES && p.nr - p.row0 <= BM && p.j1 - p.j0 >= 6;
   };

@@ -19,9 +19,11 @@
 // thread has one set of weights (and of sums of dw).  A thread copies its coming items' data, and with
 // a new token its angles, to shared memory itself, asynchronously, a ring of them ahead: what is in
 // flight takes no registers, needs no barrier, and nothing waits for a look-up.
-// Measured, 32/8 heads, d = 128, bf16: 4 x 8192 tokens forward 109 us (6.2 TB/s, 91 % of the copy
-// rate), backward 161 us (6.3 TB/s) with the weights' gradients; appending 16 prompts of 600-1100
-// tokens 66 us (5.2 TB/s), about as much the instructions of a warp's items as bytes.
+// Measured, 32/8 heads, d = 128, bf16: 4 x 8192 tokens forward 108 us (6.3 TB/s, 92 % of the copy
+// rate), backward 159 us (6.3 TB/s) with the weights' gradients; appending 16 prompts of 600-1100
+// tokens 66 us (5.2 TB/s), to E4M3 pages 68 (4.7 TB/s), about as much the instructions of a warp's items
+// as bytes.  So are smaller heads: d = 64 forward 63 us (5.3 TB/s), backward 91 (5.6); d = 32 40 (4.2) and
+// 54 (4.7).
 #include "fa_internal.h"
 #include "fa_heads.cuh"
 #include "fa_tokens.cuh"
@@ -96,7 +98,7 @@ __device__ __forceinline__ Item item_of(int j, int rot) {
   return {8 * j, 8 * j + rot / 2, 8 * j, 8 * j + 4, true, true};
 }
 // Turns an item: c, s are the cosines and sines of its 8 pairs.  (Keeping the negated sines too
-// spills in the gradient: 4 x 8192 tokens 225 against 161 us.)
+// spills in the gradient: 4 x 8192 tokens 225 us when this took 161.)
 template <bool INTER>
 __device__ __forceinline__ void rotate(const Item& it, float2 (&x)[4], float2 (&y)[4],
                                        const float2 (&c)[4], const float2 (&s)[4]) {

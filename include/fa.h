@@ -473,7 +473,9 @@ fa_status fa_fwd_paged(const void* Q, const fa_paged_cache* cache, void* O, floa
 /* The same from pools of E4M3 codes (d = 128) standing for k_scale * K and v_scale * V: prompts and
  * drafts of a model whose cache fa_append_paged_fp8 writes and fa_decode_paged_fp8 reads.  Keys and
  * values are used as their codes stand; queries are not quantised (a bf16 value below 2^-28 of its
- * row's largest loses bits) and the softmax weights are rounded to fp16 for either dtype.  Workspace and
+ * row's largest loses bits) and the softmax weights are rounded to fp16 for either dtype
+ * (fa_decode_paged_fp8 keeps twice the bits: a draft is checked a little more coarsely than its tokens
+ * would be decoded one by one; fp16 results are off by 1.4 times their own rounding).  Workspace and
  * errors as for fa_fwd_paged, with fa_decode_paged_fp8's for the scales. */
 fa_status fa_fwd_paged_fp8(const void* Q, const fa_paged_cache* cache, void* O, float* L,
                            void* workspace, size_t workspace_bytes, const int* cu_seqlens, int B,
